@@ -150,7 +150,7 @@ __global__ __launch_bounds__(ROUTE_MAX_THREADS) void route_kernel(const int32_t*
   const int E = experts;
   int32_t* cnt = sm;                   // [T][E]
   const int S = T >= E ? T / E : 1;    // scan segments per expert
-  const int R = T / S;                 // counter rows per segment
+  const int R = (T + S - 1) / S;       // counter rows per segment (the last ones may have fewer)
   int32_t* part = cnt + T * E;         // [S][E] segment sums
   int32_t* base = part + S * E;        // [E] first slot of each expert in this range
   const int tid = threadIdx.x;
@@ -179,7 +179,7 @@ __global__ __launch_bounds__(ROUTE_MAX_THREADS) void route_kernel(const int32_t*
   for (int idx = tid; idx < S * E; idx += T) {
     const int e = idx % E, g = idx / E;
     int32_t sum = 0;
-    for (int r = g * R; r < g * R + R; ++r) sum += cnt[r * E + e];
+    for (int r = g * R; r < g * R + R && r < T; ++r) sum += cnt[r * E + e];
     part[g * E + e] = sum;
   }
   __syncthreads();
@@ -215,7 +215,7 @@ __global__ __launch_bounds__(ROUTE_MAX_THREADS) void route_kernel(const int32_t*
     const int e = idx % E, g = idx / E;
     int32_t run = base[e];
     for (int gg = 0; gg < g; ++gg) run += part[gg * E + e];
-    for (int r = g * R; r < g * R + R; ++r) {
+    for (int r = g * R; r < g * R + R && r < T; ++r) {
       const int32_t v = cnt[r * E + e];
       cnt[r * E + e] = run;
       run += v;
