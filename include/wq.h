@@ -40,6 +40,12 @@
  *                           (group = 0) (FastDeploy "Quantization" precision list: INT8 weights,
  *                           BF16 activations; lesson E6.4 "Math and notation" at b = 8).
  *
+ *       WQ_FMT_MXFP4        microscaled 4-bit floating point (OCP Microscaling Formats
+ *                           specification 1.0): e2m1 codes, two per byte, the first in the low
+ *                           nibble (bit 3 the sign, bits 0..2 the magnitude 0, 0.5, 1, 1.5, 2, 3,
+ *                           4, 6), and one scale byte b per block of 32 along k;
+ *                           x_hat = bf16(value * 2^(b - 127)), exact below 2^128; b = 255: NaN.
+ *
  * Layouts (every matrix is W[n][k], k contiguous, y = x W^T; an MoE tensor adds a leading
  * expert dimension; group = 64 along k; G = k / 64):
  *   INT4:   codes u8[E][n][k/2]; scales bf16[E][n][G] (group 64) or bf16[E][n] (group 0).
@@ -52,6 +58,8 @@
  *   CCQ_HYBRID: codes u8[E][n][G*20] (each group's 10 u16 words, little endian);
  *           super_scale f32[E][n]; zp (4 for the 3-bit states).
  *   INT8:   codes i8[E][n][k]; scales bf16[E][n][G] (group 64) or bf16[E][n] (group 0).
+ *
+ *   MXFP4:  codes u8[E][n][k/2]; qscale u8[E][n][k/32], the blocks' scale bytes; group = 32.
  *
  * Conventions for every call below:
  *   - Every pointer inside wq_weight and every tensor argument of a compute call is DEVICE
@@ -74,6 +82,7 @@
  *   - The products (wq_gemm, wq_moe_gate_up, wq_moe_down, wq_moe_ffn) also require every scale
  *     to be below 2^100 in magnitude: they rescale it by up to 2^24 on its way into the decode
  *     (wq_dequantize has no such limit).  Real weights sit many orders of magnitude below it.
+ *     MXFP4 scale bytes have no limit: the products use the values wq_dequantize gives.
  *   - Sizes are element counts (int64).  Device pointers must be 16-byte aligned.  The products
  *     address one expert's arrays and one activation row with 32-bit byte offsets: they return
  *     WQ_ERR_UNSUPPORTED for k >= 2^30 or when one expert's codes exceed 2^31 - 24 bytes.
@@ -104,20 +113,24 @@ typedef enum {
   WQ_FMT_CCQ2 = 3,
   WQ_FMT_CCQ432 = 4,
   WQ_FMT_CCQ_HYBRID = 5,
-  WQ_FMT_INT8 = 6
+  WQ_FMT_INT8 = 6,
+  WQ_FMT_MXFP4 = 7
 } wq_format;
+
+/* Element type of the tensors that may be either. */
+typedef enum { WQ_TYPE_BF16 = 0, WQ_TYPE_F32 = 1 } wq_type;
 
 /* A packed weight tensor [experts][n][k] in device memory (see layouts above). */
 typedef struct {
   int32_t format;            /* wq_format                                                  */
-  int32_t group;             /* 64, or 0 = per output channel (INT4 and INT8)              */
+  int32_t group;             /* 64; 32 (MXFP4); 0 = per output channel (INT4 and INT8)     */
   int64_t experts;           /* 1 for a dense matrix                                       */
   int64_t n;                 /* output channels per expert                                 */
   int64_t k;                 /* input channels; a multiple of 64                           */
   const uint8_t* codes;
   const uint16_t* scales;    /* bf16 bits; INT4, INT8 and AFFINE                           */
   const uint8_t* zeros;      /* AFFINE                                                     */
-  const uint8_t* qscale;     /* CCQ2                                                       */
+  const uint8_t* qscale;     /* CCQ2; MXFP4 scale bytes                                    */
   const float* super_scale;  /* CCQ2, CCQ432, CCQ_HYBRID                                   */
   const float* code_scale;   /* CCQ2                                                       */
   const float* code_zero;    /* CCQ2                                                       */
@@ -248,6 +261,75 @@ wq_status wq_moe_combine(const float* d, const float* topk_weights, int64_t t, i
 wq_status wq_quantize_ccq(const float* w, int64_t n, int64_t k, int32_t zp, int32_t refine,
                           uint8_t* codes, uint8_t* qscale, float* super_scale, float* code_scale,
                           float* code_zero, void* stream);
+
+/* ---- Microscaled 4-bit floating point (MXFP4) -----------------------------------------------
+ * WQ_FMT_MXFP4 weights are taken by every call above with bf16 activations.  The calls below
+ * quantise, and multiply MXFP4 activations with MXFP4 weights: every product of two codes is
+ * exact, each pair of blocks' sum is scaled by both blocks' scales, and the sums are fp32. */
+
+/* n rows of k values (x_type; device) to MXFP4: codes u8[n][k/2], scales u8[n][k/32].  Per block
+ * of 32 with largest magnitude a:
+ *   b = max(floor(log2 a) - 2 + 127, 0)   (a = 0 or subnormal: 0)
+ *   code = e2m1(v / 2^(b - 127)), rounded to the nearest value, half way to the even code,
+ *   magnitudes above 6 to 6; signs are kept, those of zeros too
+ * and a block that holds an infinity or a NaN becomes NaN (b = 255, codes 0).  An MoE tensor is
+ * n = experts x rows.  k % 64 == 0; n == 0 is a no-op.  codes, scales and x 16-byte aligned. */
+wq_status wq_quantize_mx(const void* x, int32_t x_type, int64_t n, int64_t k, uint8_t* codes,
+                         uint8_t* scales, void* stream);
+
+/* y[m][n] = x W^T with x in MXFP4 (x_codes u8[m][k/2], x_scales u8[m][k/32]) and w in
+ * WQ_FMT_MXFP4, experts == 1; y of y_type.  m == 0 is a no-op. */
+wq_status wq_gemm_mx(const uint8_t* x_codes, const uint8_t* x_scales, int64_t m,
+                     const wq_weight* w, void* y, int32_t y_type, void* stream);
+
+/* wq_moe_gate_up with x in MXFP4 (x_codes u8[t][hidden/2], x_scales u8[t][hidden/32]): the
+ * product gathers the tokens' rows itself.  h bf16 [t*topk][inter], rows in expert order; rows of
+ * dropped pairs (behind expert_offsets[experts]) are left as they were. */
+wq_status wq_moe_gate_up_mx(const uint8_t* x_codes, const uint8_t* x_scales, int64_t t,
+                            const int32_t* expert_offsets, const int32_t* sorted_pairs,
+                            int32_t topk, const wq_weight* gate, const wq_weight* up, uint16_t* h,
+                            void* stream);
+
+/* d[r] = W_down[e] h[r] for every row r in expert order (h_codes u8[npairs][inter/2], h_scales
+ * u8[npairs][inter/32]); d of d_type [npairs][hidden], rows in expert order as well
+ * (wq_moe_unpermute brings them back); rows behind expert_offsets[experts] are left as they
+ * were. */
+wq_status wq_moe_down_mx(const uint8_t* h_codes, const uint8_t* h_scales, int64_t npairs,
+                         const int32_t* expert_offsets, const wq_weight* down, void* d,
+                         int32_t d_type, void* stream);
+
+/* ---- Token dispatch: rows in expert order and back, with gradients --------------------------
+ * wq_moe_route sorts the pairs; the calls below move rows.  positions i32[t][topk] holds the row
+ * of every pair p = t*topk + j in expert order, -1 for a dropped pair (id outside [0, experts)):
+ * a dropped pair contributes nothing, and nothing is written for it.  Rows, tokens and their
+ * gradients are of one type; sums are fp32, slots in order, rounded once. */
+
+/* positions from what wq_moe_route was given and gave: positions[sorted_pairs[r]] = r. */
+wq_status wq_moe_positions(const int32_t* topk_ids, int64_t t, int32_t topk, int32_t experts,
+                           const int32_t* expert_offsets, const int32_t* sorted_pairs,
+                           int32_t* positions, void* stream);
+
+/* rows[positions[t][j]] = x[t]: x [t][hidden], rows [t*topk][hidden] of `type`; rows that no pair
+ * has are left as they were.  Its gradient is wq_moe_unpermute without weights.  positions must
+ * not hold a row twice. */
+wq_status wq_moe_permute(const void* x, int32_t type, int64_t t, int32_t topk, int64_t hidden,
+                         const int32_t* positions, void* rows, void* stream);
+
+/* y[t] = sum_j topk_weights[t][j] * rows[positions[t][j]] (topk_weights f32, NULL: every weight
+ * 1); a token whose pairs are all dropped gets zeros. */
+wq_status wq_moe_unpermute(const void* rows, int32_t type, const int32_t* positions,
+                           const float* topk_weights, int64_t t, int32_t topk, int64_t hidden,
+                           void* y, void* stream);
+
+/* Gradients of wq_moe_unpermute for dy [t][hidden]:
+ *   d_rows[positions[t][j]] = topk_weights[t][j] * dy[t]      (rows of no pair left as they were)
+ *   d_weights[t][j] = <dy[t], rows[positions[t][j]]>           (0 for a dropped pair)
+ * Either output may be NULL and is then not computed; rows may be NULL when d_weights is.
+ * topk_weights NULL: every weight 1.  positions must not hold a row twice. */
+wq_status wq_moe_unpermute_grad(const void* dy, int32_t type, const void* rows,
+                                const int32_t* positions, const float* topk_weights, int64_t t,
+                                int32_t topk, int64_t hidden, void* d_rows, float* d_weights,
+                                void* stream);
 
 /* Host helpers for the INT4 storage format (lesson E6.4, "Do it in code"); host memory.
  * wq_pack_int4: two codes per byte, the first in the low nibble, an odd count padded with 0;

@@ -5,7 +5,9 @@ PyTorch provides device memory and the current HIP stream.  If the library has n
 built, importing works but every call raises (there is no CPU fallback).
 
 Names follow the C ABI: ``wq_dequantize``, ``wq_gemm``, ``wq_moe_route``, ``wq_moe_ffn``,
-``wq_moe_workspace_bytes``, ``wq_pack_int4``, ``wq_unpack_int4``, ``wq_packed_size``.
+``wq_moe_workspace_bytes``, ``wq_pack_int4``, ``wq_unpack_int4``, ``wq_packed_size``; MXFP4:
+``wq_quantize_mx``, ``wq_gemm_mx``, ``wq_moe_gate_up_mx``, ``wq_moe_down_mx``; the token dispatch:
+``wq_moe_positions``, ``wq_moe_permute``, ``wq_moe_unpermute``, ``wq_moe_unpermute_grad``.
 """
 from __future__ import annotations
 
@@ -27,13 +29,17 @@ WQ_ERR_WORKSPACE = -5
 WQ_ERR_HIP = -6
 
 FMT_INT4, FMT_INT2_AFFINE, FMT_CCQ2, FMT_CCQ432, FMT_CCQ_HYBRID, FMT_INT8 = 1, 2, 3, 4, 5, 6
+FMT_MXFP4 = 7
+
+TYPE_BF16, TYPE_F32 = 0, 1  # wq_type
 
 # Every symbol include/wq.h declares.
 EXPORTS = ("wq_dequantize", "wq_gemm", "wq_moe_workspace_bytes", "wq_moe_route_workspace_bytes",
            "wq_moe_route", "wq_moe_ffn",
            "wq_moe_gate_up", "wq_moe_down", "wq_moe_combine", "wq_pack_int4", "wq_unpack_int4",
            "wq_packed_size", "wq_status_string", "wq_last_error", "wq_last_error_detail", "wq_quantize_ccq",
-           "wq_moe_ffn_noalloc")
+           "wq_moe_ffn_noalloc", "wq_quantize_mx", "wq_gemm_mx", "wq_moe_gate_up_mx", "wq_moe_down_mx",
+           "wq_moe_positions", "wq_moe_permute", "wq_moe_unpermute", "wq_moe_unpermute_grad")
 
 
 class WqError(RuntimeError):
@@ -82,6 +88,14 @@ def lib() -> ctypes.CDLL:
             "wq_moe_down": (i32, [vp, i64, i32, vp, vp, W, vp, vp]),
             "wq_moe_combine": (i32, [vp, vp, i64, i32, i64, vp, vp]),
             "wq_quantize_ccq": (i32, [vp, i64, i64, i32, i32, vp, vp, vp, vp, vp, vp]),
+            "wq_quantize_mx": (i32, [vp, i32, i64, i64, vp, vp, vp]),
+            "wq_gemm_mx": (i32, [vp, vp, i64, W, vp, i32, vp]),
+            "wq_moe_gate_up_mx": (i32, [vp, vp, i64, vp, vp, i32, W, W, vp, vp]),
+            "wq_moe_down_mx": (i32, [vp, vp, i64, vp, W, vp, i32, vp]),
+            "wq_moe_positions": (i32, [vp, i64, i32, i32, vp, vp, vp, vp]),
+            "wq_moe_permute": (i32, [vp, i32, i64, i32, i64, vp, vp, vp]),
+            "wq_moe_unpermute": (i32, [vp, i32, vp, vp, i64, i32, i64, vp, vp]),
+            "wq_moe_unpermute_grad": (i32, [vp, i32, vp, vp, vp, i64, i32, i64, vp, vp, vp]),
             "wq_pack_int4": (i32, [vp, i64, vp]),
             "wq_unpack_int4": (i32, [vp, i64, vp]),
             "wq_packed_size": (i64, [i64, i32]),
@@ -166,6 +180,8 @@ def _layout(fmt, E, n, k, group):
         return {"codes": (rows * k // 2, 1), "scales": (per_row_scale, 2)}
     if fmt == FMT_INT8 and group in (0, 64):
         return {"codes": (rows * k, 1), "scales": (per_row_scale, 2)}
+    if fmt == FMT_MXFP4 and group == 32:
+        return {"codes": (rows * k // 2, 1), "qscale": (rows * k // 32, 1)}
     if fmt == FMT_INT2_AFFINE and group == 64:
         return {"codes": (rows * k // 4, 1), "scales": (rows * G, 2), "zeros": (rows * G, 1)}
     if fmt == FMT_CCQ2 and group == 64:
@@ -346,7 +362,8 @@ def wq_moe_ffn_noalloc(x, topk_ids, topk_weights, gate: PackedWeight, up: Packed
     _check(lib().wq_moe_ffn_noalloc(_ptr(x), t, hidden, _ptr(topk_ids), _ptr(topk_weights), topk,
                                     ctypes.byref(gate.cstruct()), ctypes.byref(up.cstruct()),
                                     ctypes.byref(down.cstruct()), _ptr(y), _stream()),
-           "wq_moe_ffn_noalloc")
+           "wq_moe_ffn_noalloc", "wq_quantize_mx", "wq_gemm_mx", "wq_moe_gate_up_mx", "wq_moe_down_mx",
+           "wq_moe_positions", "wq_moe_permute", "wq_moe_unpermute", "wq_moe_unpermute_grad")
     return y
 
 
@@ -430,6 +447,203 @@ def wq_quantize_ccq(w, zp: int = 32, refine=True) -> PackedWeight:
     _check(lib().wq_quantize_ccq(_ptr(w), rows, k, zp, mask, _ptr(codes), _ptr(qscale),
                                  _ptr(sup), _ptr(cs), _ptr(cz), _stream()), "wq_quantize_ccq")
     return PackedWeight(FMT_CCQ2, n, k, E, 64, codes, None, None, qscale, sup, cs, cz, zp)
+
+
+# ---------------------------------------------------------------------------------------------
+# MXFP4: quantisation, and the products of two MXFP4 operands
+# ---------------------------------------------------------------------------------------------
+
+def _value_type(t, name):
+    """(wq_type, _need kind) of a tensor that may hold bf16 (or its bits) or fp32."""
+    import torch
+
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch tensor, got {type(t).__name__}")
+    if t.dtype in _dtypes()["bf16"]:
+        return TYPE_BF16, "bf16"
+    if t.dtype == torch.float32:
+        return TYPE_F32, "f32"
+    raise TypeError(f"{name}: dtype {t.dtype} is neither bf16 nor f32")
+
+
+def wq_quantize_mx(x) -> PackedWeight:
+    """MXFP4 encoding (include/wq.h) of bf16 or fp32 values [n, k] or [E, n, k] on the GPU: weights,
+    or the activations of the products below."""
+    import torch
+
+    vt, kind = _value_type(x, "wq_quantize_mx x")
+    if x.dim() not in (2, 3):
+        raise ValueError("wq_quantize_mx: x must be [n, k] or [E, n, k]")
+    E, n, k = x.shape if x.dim() == 3 else (1, *x.shape)
+    if k <= 0 or k % 64:
+        raise ValueError(f"wq_quantize_mx: k = {k} is not a positive multiple of 64")
+    x = _need(x.contiguous(), "wq_quantize_mx x", kind)
+    codes = torch.empty((E, n, k // 2), dtype=torch.uint8, device=x.device)
+    scales = torch.empty((E, n, k // 32), dtype=torch.uint8, device=x.device)
+    _check(lib().wq_quantize_mx(_ptr(x), vt, E * n, k, _ptr(codes), _ptr(scales), _stream()),
+           "wq_quantize_mx")
+    return PackedWeight(FMT_MXFP4, n, k, E, 32, codes=codes, qscale=scales)
+
+
+def _mx_rows(x, what, rows=None, k=None):
+    """x: MXFP4 rows [rows, k] as wq_quantize_mx gives them for a matrix."""
+    if not isinstance(x, PackedWeight):
+        raise TypeError(f"{what}: expected the PackedWeight of wq_quantize_mx, got {type(x).__name__}")
+    if x.format != FMT_MXFP4 or x.group != 32 or x.experts != 1:
+        raise ValueError(f"{what}: must be one MXFP4 matrix")
+    if k is not None and x.k != k:
+        raise ValueError(f"{what}: k = {x.k} != {k}")
+    if rows is not None and x.n != rows:
+        raise ValueError(f"{what}: {x.n} rows, {rows} are needed")
+    _need(x.codes, f"{what} codes", "u8", numel=x.n * x.k // 2)
+    _need(x.qscale, f"{what} scales", "u8", numel=x.n * x.k // 32)
+    return x
+
+
+def wq_gemm_mx(x, w: PackedWeight, y=None, dtype=None):
+    """y = x @ W^T with both operands in MXFP4; x: wq_quantize_mx of the rows [m, k].  y is bf16, or
+    fp32 with dtype=torch.float32 (or a y of that type)."""
+    import torch
+
+    _mx_rows(x, "wq_gemm_mx x", k=w.k)
+    if y is None:
+        y = torch.empty((x.n, w.n), dtype=dtype or torch.bfloat16, device=x.codes.device)
+    vt, kind = _value_type(y, "wq_gemm_mx y")
+    _need(y, "wq_gemm_mx y", kind, shape=(x.n, w.n))
+    _check(lib().wq_gemm_mx(_ptr(x.codes), _ptr(x.qscale), x.n, ctypes.byref(w.cstruct()), _ptr(y), vt,
+                            _stream()), "wq_gemm_mx")
+    return y
+
+
+def wq_moe_gate_up_mx(x, offsets, sorted_pairs, topk: int, gate: PackedWeight, up: PackedWeight, h=None):
+    """wq_moe_gate_up with both operands in MXFP4; x: wq_quantize_mx of the tokens [t, hidden].
+    h [t*topk, inter] bf16, rows in expert order."""
+    import torch
+
+    _mx_rows(x, "wq_moe_gate_up_mx x", k=gate.k)
+    t = x.n
+    _need(offsets, "wq_moe_gate_up_mx offsets", "i32", numel=gate.experts + 1)
+    _need(sorted_pairs, "wq_moe_gate_up_mx sorted_pairs", "i32", numel=t * topk)
+    if h is None:
+        h = torch.empty((t * topk, gate.n), dtype=torch.bfloat16, device=x.codes.device)
+    _need(h, "wq_moe_gate_up_mx h", "bf16", shape=(t * topk, gate.n))
+    _check(lib().wq_moe_gate_up_mx(_ptr(x.codes), _ptr(x.qscale), t, _ptr(offsets), _ptr(sorted_pairs),
+                                   topk, ctypes.byref(gate.cstruct()), ctypes.byref(up.cstruct()),
+                                   _ptr(h), _stream()), "wq_moe_gate_up_mx")
+    return h
+
+
+def wq_moe_down_mx(h, offsets, down: PackedWeight, d=None, dtype=None):
+    """d [npairs, hidden] = down h with both operands in MXFP4; h: wq_quantize_mx of the rows
+    [npairs, inter] in expert order, the order d is in too.  bf16, or fp32 as in wq_gemm_mx."""
+    import torch
+
+    _mx_rows(h, "wq_moe_down_mx h", k=down.k)
+    _need(offsets, "wq_moe_down_mx offsets", "i32", numel=down.experts + 1)
+    if d is None:
+        d = torch.empty((h.n, down.n), dtype=dtype or torch.bfloat16, device=h.codes.device)
+    vt, kind = _value_type(d, "wq_moe_down_mx d")
+    _need(d, "wq_moe_down_mx d", kind, shape=(h.n, down.n))
+    _check(lib().wq_moe_down_mx(_ptr(h.codes), _ptr(h.qscale), h.n, _ptr(offsets),
+                                ctypes.byref(down.cstruct()), _ptr(d), vt, _stream()), "wq_moe_down_mx")
+    return d
+
+
+# ---------------------------------------------------------------------------------------------
+# Token dispatch: rows in expert order and back, with gradients
+# ---------------------------------------------------------------------------------------------
+
+def wq_moe_positions(topk_ids, offsets, sorted_pairs, positions=None):
+    """positions int32 [t, topk]: the row of every (token, slot) pair in expert order, -1 for a pair
+    whose id is no expert's; offsets and sorted_pairs as wq_moe_route gave them for topk_ids."""
+    import torch
+
+    if topk_ids.dim() != 2:
+        raise ValueError("wq_moe_positions: topk_ids must be [t, topk]")
+    t, topk = topk_ids.shape
+    _need(topk_ids, "wq_moe_positions topk_ids", "i32")
+    _need(offsets, "wq_moe_positions offsets", "i32")
+    _need(sorted_pairs, "wq_moe_positions sorted_pairs", "i32", numel=t * topk)
+    if positions is None:
+        positions = torch.empty((t, topk), dtype=torch.int32, device=topk_ids.device)
+    _need(positions, "wq_moe_positions positions", "i32", shape=(t, topk))
+    _check(lib().wq_moe_positions(_ptr(topk_ids), t, topk, offsets.numel() - 1, _ptr(offsets),
+                                  _ptr(sorted_pairs), _ptr(positions), _stream()), "wq_moe_positions")
+    return positions
+
+
+def _positions(positions, what):
+    _need(positions, f"{what} positions", "i32")
+    if positions.dim() != 2:
+        raise ValueError(f"{what}: positions must be [t, topk]")
+    return positions.shape
+
+
+def wq_moe_permute(x, positions, rows=None):
+    """rows [t*topk, hidden] in expert order: rows[positions[t, j]] = x[t] (bf16 or fp32).  Its
+    gradient is wq_moe_unpermute(d_rows, positions)."""
+    import torch
+
+    t, topk = _positions(positions, "wq_moe_permute")
+    vt, kind = _value_type(x, "wq_moe_permute x")
+    if x.dim() != 2:
+        raise ValueError("wq_moe_permute: x must be [t, hidden]")
+    hidden = x.shape[1]
+    _need(x, "wq_moe_permute x", kind, shape=(t, hidden))
+    if rows is None:
+        rows = torch.empty((t * topk, hidden), dtype=x.dtype, device=x.device)
+    _need(rows, "wq_moe_permute rows", kind, shape=(t * topk, hidden))
+    _check(lib().wq_moe_permute(_ptr(x), vt, t, topk, hidden, _ptr(positions), _ptr(rows), _stream()),
+           "wq_moe_permute")
+    return rows
+
+
+def wq_moe_unpermute(rows, positions, topk_weights=None, y=None):
+    """y [t, hidden] = sum_j topk_weights[t, j] * rows[positions[t, j]] (weights None: 1)."""
+    import torch
+
+    t, topk = _positions(positions, "wq_moe_unpermute")
+    vt, kind = _value_type(rows, "wq_moe_unpermute rows")
+    if rows.dim() != 2:
+        raise ValueError("wq_moe_unpermute: rows must be [t*topk, hidden]")
+    hidden = rows.shape[1]
+    _need(rows, "wq_moe_unpermute rows", kind, shape=(t * topk, hidden))
+    if topk_weights is not None:
+        _need(topk_weights, "wq_moe_unpermute topk_weights", "f32", shape=(t, topk))
+    if y is None:
+        y = torch.empty((t, hidden), dtype=rows.dtype, device=rows.device)
+    _need(y, "wq_moe_unpermute y", kind, shape=(t, hidden))
+    _check(lib().wq_moe_unpermute(_ptr(rows), vt, _ptr(positions), _ptr(topk_weights), t, topk, hidden,
+                                  _ptr(y), _stream()), "wq_moe_unpermute")
+    return y
+
+
+def wq_moe_unpermute_grad(dy, rows, positions, topk_weights=None, d_rows=None, d_weights=None):
+    """(d_rows [t*topk, hidden], d_weights f32 [t, topk]) of wq_moe_unpermute for dy [t, hidden].
+    rows None: only d_rows is computed, and d_weights is None."""
+    import torch
+
+    t, topk = _positions(positions, "wq_moe_unpermute_grad")
+    vt, kind = _value_type(dy, "wq_moe_unpermute_grad dy")
+    if dy.dim() != 2:
+        raise ValueError("wq_moe_unpermute_grad: dy must be [t, hidden]")
+    hidden = dy.shape[1]
+    _need(dy, "wq_moe_unpermute_grad dy", kind, shape=(t, hidden))
+    if topk_weights is not None:
+        _need(topk_weights, "wq_moe_unpermute_grad topk_weights", "f32", shape=(t, topk))
+    if d_rows is None:
+        d_rows = torch.empty((t * topk, hidden), dtype=dy.dtype, device=dy.device)
+    _need(d_rows, "wq_moe_unpermute_grad d_rows", kind, shape=(t * topk, hidden))
+    if rows is not None:
+        _need(rows, "wq_moe_unpermute_grad rows", kind, shape=(t * topk, hidden))
+        if d_weights is None:
+            d_weights = torch.empty((t, topk), dtype=torch.float32, device=dy.device)
+    if d_weights is not None:
+        _need(d_weights, "wq_moe_unpermute_grad d_weights", "f32", shape=(t, topk))
+    _check(lib().wq_moe_unpermute_grad(_ptr(dy), vt, _ptr(rows), _ptr(positions), _ptr(topk_weights), t,
+                                       topk, hidden, _ptr(d_rows), _ptr(d_weights), _stream()),
+           "wq_moe_unpermute_grad")
+    return d_rows, d_weights
 
 
 # ---------------------------------------------------------------------------------------------

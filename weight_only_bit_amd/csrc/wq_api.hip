@@ -48,7 +48,8 @@ bool is_ccq(int32_t f) {
 // Bytes of one packed row of k weights.
 int64_t row_code_bytes(const wq_weight* w) {
   switch (w->format) {
-    case WQ_FMT_INT4: return w->k / 2;
+    case WQ_FMT_INT4:
+    case WQ_FMT_MXFP4: return w->k / 2;
     case WQ_FMT_INT8: return w->k;
     case WQ_FMT_CCQ432: return w->k / 64 * 22;
     case WQ_FMT_CCQ_HYBRID: return w->k / 64 * 20;
@@ -124,6 +125,11 @@ wq_status check_weight(const wq_weight* w, const char* what) {
         return fail(WQ_ERR_ALIGN, "%s: super_scale not 16-byte aligned", what);
       if (w->zp < 0 || w->zp > 127)
         return fail(WQ_ERR_UNSUPPORTED, "%s: CCQ zero point must lie in 0..127", what);
+      break;
+    case WQ_FMT_MXFP4:
+      if (w->group != 32) return fail(WQ_ERR_UNSUPPORTED, "%s: MXFP4 needs group 32", what);
+      if (!w->qscale) return fail(WQ_ERR_ARG, "%s: null qscale", what);
+      if (!aligned16(w->qscale)) return fail(WQ_ERR_ALIGN, "%s: qscale not 16-byte aligned", what);
       break;
     default:
       return fail(WQ_ERR_UNSUPPORTED, "%s: unknown format %d", what, w->format);
@@ -622,3 +628,193 @@ extern "C" wq_status wq_moe_ffn_noalloc(const uint16_t* x, int64_t t, int64_t hi
   return moe_ffn_in("wq_moe_ffn_noalloc", x, t, hidden, topk_ids, topk_weights, topk, gate, up,
                     down, y, ws, (size_t)WQ_NOALLOC_SCRATCH_BYTES, stream);
 }
+
+// ---------------------------------------------------------------------------------------------
+// MXFP4 quantisation, the products of two MXFP4 operands, and the token dispatch.
+// ---------------------------------------------------------------------------------------------
+namespace {
+
+wq_status check_type(int32_t type, const char* what) {
+  if (type != WQ_TYPE_BF16 && type != WQ_TYPE_F32)
+    return fail(WQ_ERR_UNSUPPORTED, "%s: type %d is neither WQ_TYPE_BF16 nor WQ_TYPE_F32", what, type);
+  return WQ_OK;
+}
+
+wq_status check_mx_weight(const wq_weight* w, const char* what) {
+  wq_status st = check_weight(w, what);
+  if (st != WQ_OK) return st;
+  if (w->format != WQ_FMT_MXFP4)
+    return fail(WQ_ERR_UNSUPPORTED, "%s: the weight must be WQ_FMT_MXFP4", what);
+  return check_product_zp(w, what);
+}
+
+// Sizes of a (token, slot) array and of rows of `hidden` elements.
+wq_status check_pairs(int64_t t, int32_t topk, int64_t hidden, const char* what) {
+  if (t < 0 || topk <= 0 || hidden <= 0) return fail(WQ_ERR_ARG, "%s: bad sizes", what);
+  if (t > (1ll << 30) || t * topk > (1ll << 30)) return fail(WQ_ERR_UNSUPPORTED, "%s: too many pairs", what);
+  if (hidden > (1ll << 31)) return fail(WQ_ERR_UNSUPPORTED, "%s: hidden must not exceed 2^31", what);
+  return WQ_OK;
+}
+
+wq::MxArgs mx_args(const wq_weight* w, const wq_weight* up, const uint8_t* codes, const uint8_t* scales,
+                   int64_t rows, void* out) {
+  wq::MxArgs a{};
+  a.w0_codes = w->codes;
+  a.w0_scales = w->qscale;
+  a.w1_codes = up->codes;
+  a.w1_scales = up->qscale;
+  a.x_codes = codes;
+  a.x_scales = scales;
+  a.out = out;
+  a.out_stride = w->n;
+  a.topk = 1;
+  a.M = rows;
+  a.N = w->n;
+  a.K = w->k;
+  return a;
+}
+
+}  // namespace
+
+extern "C" {
+
+wq_status wq_quantize_mx(const void* x, int32_t x_type, int64_t n, int64_t k, uint8_t* codes,
+                         uint8_t* scales, void* stream) {
+  wq_status st = check_type(x_type, "wq_quantize_mx");
+  if (st != WQ_OK) return st;
+  if (n < 0 || k <= 0) return fail(WQ_ERR_ARG, "wq_quantize_mx: bad sizes");
+  if (k % 64 != 0) return fail(WQ_ERR_UNSUPPORTED, "wq_quantize_mx: k = %lld is not a multiple of 64", (long long)k);
+  if (k > (1ll << 31) || n > (1ll << 42) / k)
+    return fail(WQ_ERR_UNSUPPORTED, "wq_quantize_mx: more than 2^42 values");
+  if (n == 0) return WQ_OK;
+  if (!x || !codes || !scales) return fail(WQ_ERR_ARG, "wq_quantize_mx: null pointer");
+  if (!aligned16(x) || !aligned16(codes) || !aligned16(scales))
+    return fail(WQ_ERR_ALIGN, "wq_quantize_mx: x, codes and scales must be 16-byte aligned");
+  return hip_status(wq::launch_mx_quantize(x, x_type == WQ_TYPE_F32, n, k, codes, scales,
+                                           static_cast<hipStream_t>(stream)),
+                    "wq_quantize_mx launch");
+}
+
+wq_status wq_gemm_mx(const uint8_t* x_codes, const uint8_t* x_scales, int64_t m,
+                     const wq_weight* w, void* y, int32_t y_type, void* stream) {
+  wq_status st = check_mx_weight(w, "wq_gemm_mx");
+  if (st != WQ_OK) return st;
+  if ((st = check_type(y_type, "wq_gemm_mx")) != WQ_OK) return st;
+  if (m < 0) return fail(WQ_ERR_ARG, "wq_gemm_mx: negative m");
+  if (w->experts != 1) return fail(WQ_ERR_ARG, "wq_gemm_mx: a dense weight has experts == 1");
+  if (m == 0) return WQ_OK;
+  if (!x_codes || !x_scales || !y) return fail(WQ_ERR_ARG, "wq_gemm_mx: null x or y");
+  if (!aligned16(x_codes) || !aligned16(x_scales) || !aligned16(y))
+    return fail(WQ_ERR_ALIGN, "wq_gemm_mx: x or y not 16-byte aligned");
+  if (m > (1ll << 31)) return fail(WQ_ERR_UNSUPPORTED, "wq_gemm_mx: m must not exceed 2^31");
+  wq::MxArgs a = mx_args(w, w, x_codes, x_scales, m, y);
+  a.out_f32 = y_type == WQ_TYPE_F32;
+  return hip_status(wq::launch_mx_product(wq::MODE_DENSE, a, 1, static_cast<hipStream_t>(stream)),
+                    "wq_gemm_mx launch");
+}
+
+wq_status wq_moe_gate_up_mx(const uint8_t* x_codes, const uint8_t* x_scales, int64_t t,
+                            const int32_t* expert_offsets, const int32_t* sorted_pairs,
+                            int32_t topk, const wq_weight* gate, const wq_weight* up, uint16_t* h,
+                            void* stream) {
+  if (!gate || !up) return fail(WQ_ERR_ARG, "wq_moe_gate_up_mx: null descriptor");
+  wq_status st = check_moe_weights(gate, up, nullptr, "wq_moe_gate_up_mx");
+  if (st != WQ_OK) return st;
+  if ((st = check_mx_weight(gate, "wq_moe_gate_up_mx")) != WQ_OK) return st;
+  if ((st = check_pairs(t, topk, gate->n, "wq_moe_gate_up_mx")) != WQ_OK) return st;
+  if (t == 0) return WQ_OK;
+  if (!x_codes || !x_scales || !expert_offsets || !sorted_pairs || !h)
+    return fail(WQ_ERR_ARG, "wq_moe_gate_up_mx: null pointer");
+  if (!aligned16(x_codes) || !aligned16(x_scales) || !aligned16(h))
+    return fail(WQ_ERR_ALIGN, "wq_moe_gate_up_mx: x and h must be 16-byte aligned");
+  wq::MxArgs a = mx_args(gate, up, x_codes, x_scales, t * topk, h);
+  a.offsets = expert_offsets;
+  a.sorted_pairs = sorted_pairs;
+  a.topk = topk;
+  return hip_status(wq::launch_mx_product(wq::MODE_GATEUP, a, gate->experts, static_cast<hipStream_t>(stream)),
+                    "wq_moe_gate_up_mx launch");
+}
+
+wq_status wq_moe_down_mx(const uint8_t* h_codes, const uint8_t* h_scales, int64_t npairs,
+                         const int32_t* expert_offsets, const wq_weight* down, void* d,
+                         int32_t d_type, void* stream) {
+  if (!down) return fail(WQ_ERR_ARG, "wq_moe_down_mx: null descriptor");
+  wq_status st = check_moe_weights(nullptr, nullptr, down, "wq_moe_down_mx");
+  if (st != WQ_OK) return st;
+  if ((st = check_mx_weight(down, "wq_moe_down_mx")) != WQ_OK) return st;
+  if ((st = check_type(d_type, "wq_moe_down_mx")) != WQ_OK) return st;
+  if ((st = check_pairs(npairs, 1, down->n, "wq_moe_down_mx")) != WQ_OK) return st;
+  if (npairs == 0) return WQ_OK;
+  if (!h_codes || !h_scales || !expert_offsets || !d) return fail(WQ_ERR_ARG, "wq_moe_down_mx: null pointer");
+  if (!aligned16(h_codes) || !aligned16(h_scales) || !aligned16(d))
+    return fail(WQ_ERR_ALIGN, "wq_moe_down_mx: h and d must be 16-byte aligned");
+  wq::MxArgs a = mx_args(down, down, h_codes, h_scales, npairs, d);
+  a.offsets = expert_offsets;
+  a.out_f32 = d_type == WQ_TYPE_F32;
+  return hip_status(wq::launch_mx_product(wq::MODE_DOWN, a, down->experts, static_cast<hipStream_t>(stream)),
+                    "wq_moe_down_mx launch");
+}
+
+wq_status wq_moe_positions(const int32_t* topk_ids, int64_t t, int32_t topk, int32_t experts,
+                           const int32_t* expert_offsets, const int32_t* sorted_pairs,
+                           int32_t* positions, void* stream) {
+  wq_status st = check_pairs(t, topk, 1, "wq_moe_positions");
+  if (st != WQ_OK) return st;
+  if (experts <= 0) return fail(WQ_ERR_ARG, "wq_moe_positions: bad sizes");
+  if (experts > kMaxExperts) return fail(WQ_ERR_UNSUPPORTED, "wq_moe_positions: at most %d experts", kMaxExperts);
+  if (t == 0) return WQ_OK;
+  if (!topk_ids || !expert_offsets || !sorted_pairs || !positions)
+    return fail(WQ_ERR_ARG, "wq_moe_positions: null pointer");
+  return hip_status(wq::launch_positions(topk_ids, t * topk, experts, expert_offsets, sorted_pairs,
+                                         positions, static_cast<hipStream_t>(stream)),
+                    "wq_moe_positions launch");
+}
+
+wq_status wq_moe_permute(const void* x, int32_t type, int64_t t, int32_t topk, int64_t hidden,
+                         const int32_t* positions, void* rows, void* stream) {
+  wq_status st = check_type(type, "wq_moe_permute");
+  if (st != WQ_OK) return st;
+  if ((st = check_pairs(t, topk, hidden, "wq_moe_permute")) != WQ_OK) return st;
+  if (t == 0) return WQ_OK;
+  if (!x || !positions || !rows) return fail(WQ_ERR_ARG, "wq_moe_permute: null pointer");
+  if (!aligned16(x) || !aligned16(rows))
+    return fail(WQ_ERR_ALIGN, "wq_moe_permute: x and rows must be 16-byte aligned");
+  return hip_status(wq::launch_permute(x, type == WQ_TYPE_F32, t, topk, hidden, positions, rows,
+                                       static_cast<hipStream_t>(stream)),
+                    "wq_moe_permute launch");
+}
+
+wq_status wq_moe_unpermute(const void* rows, int32_t type, const int32_t* positions,
+                           const float* topk_weights, int64_t t, int32_t topk, int64_t hidden,
+                           void* y, void* stream) {
+  wq_status st = check_type(type, "wq_moe_unpermute");
+  if (st != WQ_OK) return st;
+  if ((st = check_pairs(t, topk, hidden, "wq_moe_unpermute")) != WQ_OK) return st;
+  if (t == 0) return WQ_OK;
+  if (!rows || !positions || !y) return fail(WQ_ERR_ARG, "wq_moe_unpermute: null pointer");
+  if (!aligned16(rows) || !aligned16(y))
+    return fail(WQ_ERR_ALIGN, "wq_moe_unpermute: rows and y must be 16-byte aligned");
+  return hip_status(wq::launch_unpermute(rows, type == WQ_TYPE_F32, positions, topk_weights, t, topk,
+                                         hidden, y, static_cast<hipStream_t>(stream)),
+                    "wq_moe_unpermute launch");
+}
+
+wq_status wq_moe_unpermute_grad(const void* dy, int32_t type, const void* rows,
+                                const int32_t* positions, const float* topk_weights, int64_t t,
+                                int32_t topk, int64_t hidden, void* d_rows, float* d_weights,
+                                void* stream) {
+  wq_status st = check_type(type, "wq_moe_unpermute_grad");
+  if (st != WQ_OK) return st;
+  if ((st = check_pairs(t, topk, hidden, "wq_moe_unpermute_grad")) != WQ_OK) return st;
+  if (t == 0 || (!d_rows && !d_weights)) return WQ_OK;
+  if (!dy || !positions || (d_weights && !rows))
+    return fail(WQ_ERR_ARG, "wq_moe_unpermute_grad: null pointer");
+  if (!aligned16(dy) || !aligned16(rows) || !aligned16(d_rows))
+    return fail(WQ_ERR_ALIGN, "wq_moe_unpermute_grad: dy, rows and d_rows must be 16-byte aligned");
+  return hip_status(wq::launch_unpermute_grad(dy, rows, type == WQ_TYPE_F32, positions, topk_weights, t,
+                                              topk, hidden, d_rows, d_weights,
+                                              static_cast<hipStream_t>(stream)),
+                    "wq_moe_unpermute_grad launch");
+}
+
+}  // extern "C"

@@ -18,7 +18,8 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint64_t u64x2 __attribute__((ext_vector_type(2)));
 
-enum { FMT_INT4 = 1, FMT_AFFINE2 = 2, FMT_CCQ2 = 3, FMT_CCQ432 = 4, FMT_CCQH = 5, FMT_INT8 = 6 };
+enum { FMT_INT4 = 1, FMT_AFFINE2 = 2, FMT_CCQ2 = 3, FMT_CCQ432 = 4, FMT_CCQH = 5, FMT_INT8 = 6,
+       FMT_MXFP4 = 7 };
 
 // The CCQ formats without code cluster: the group scale rides in the last code word.
 __host__ __device__ constexpr bool is_alg2(int f) { return f == FMT_CCQ432 || f == FMT_CCQH; }
@@ -35,7 +36,7 @@ struct DevWeight {
   const float* code_scale;
   const float* code_zero;
   int64_t n, k;
-  int32_t group;  // 64 or 0 (per channel)
+  int32_t group;  // 64, 32 (MXFP4) or 0 (per channel)
   int32_t zp;
 };
 
@@ -239,6 +240,24 @@ __device__ __forceinline__ void affine2_decode16(uint32_t w, float s24, float mz
   }
 #pragma unroll
   for (int j = 0; j < 8; ++j) p[j] = cvt_pk_bf16(r[2 * j], r[2 * j + 1]);
+}
+
+// MXFP4: two dwords = 16 e2m1 codes (first weight in the low nibble) of one block with scale byte
+// b: v_cvt_scalef32_pk_bf16_fp4 turns a byte of codes into a bf16 pair and multiplies it by the
+// power of two 2^(b - 127), taken from the exponent field of its fp32 operand (field 0 stands for
+// 2^-127, field 255 for NaN).  Half an instruction per weight, and exact: the products of e2m1
+// values and powers of two are bf16 values, subnormal ones included (2^128 and above: infinity).
+__device__ __forceinline__ void mxfp4_decode16(uint32_t w0, uint32_t w1, uint32_t b,
+                                               uint32_t (&p)[8]) {
+  const float s = __uint_as_float(b << 23);
+  p[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w0, s, 0));
+  p[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w0, s, 1));
+  p[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w0, s, 2));
+  p[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w0, s, 3));
+  p[4] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w1, s, 0));
+  p[5] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w1, s, 1));
+  p[6] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w1, s, 2));
+  p[7] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w1, s, 3));
 }
 
 // CCQ without code cluster ("CCQ", section 3.5, "Dequantization without Code Cluster"): one

@@ -1,0 +1,304 @@
+// wq_dispatch.hip -- token rows into expert order and back: positions of the (token, slot) pairs,
+// the permutation, the weighted way back, and the gradients of both.
+//
+// Everything is driven per token through positions[p], the row of pair p = token * topk + slot in
+// expert order (-1: dropped), so every output element is written by one thread that adds its
+// contributions in slot order: no atomics, the same bits every run.  All of it is bound by
+// memory: rows are read and written once in 16-byte pieces; a row of odd length starts at any
+// element, which these accesses allow, and its last pieces go element by element.
+#include <hip/hip_runtime.h>
+
+#include "wq_kernels.hpp"
+
+namespace wq {
+namespace {
+
+// 16 bytes at any element's address.
+struct __attribute__((packed, aligned(2))) Piece {
+  u32x4 v;
+};
+
+template <typename T>
+__device__ __forceinline__ u32x4 load_piece(const T* p) {
+  return reinterpret_cast<const Piece*>(p)->v;
+}
+template <typename T>
+__device__ __forceinline__ void store_piece(T* p, const u32x4& v) {
+  reinterpret_cast<Piece*>(p)->v = v;
+}
+
+__device__ __forceinline__ float to_f32(float v) { return v; }
+__device__ __forceinline__ float to_f32(uint16_t v) { return bf16_bits_to_f32(v); }
+template <typename T>
+__device__ __forceinline__ T from_f32(float v);
+template <>
+__device__ __forceinline__ float from_f32<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ uint16_t from_f32<uint16_t>(float v) { return (uint16_t)f32_to_bf16_bits(v); }
+
+// The E = 16 / sizeof(T) values of a piece in fp32, and back with one rounding.
+__device__ __forceinline__ void unpack(const u32x4& v, float (&f)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f[i] = __uint_as_float(v[i]);
+}
+__device__ __forceinline__ void unpack(const u32x4& v, float (&f)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = __uint_as_float(v[i] << 16);
+    f[2 * i + 1] = __uint_as_float(v[i] & 0xFFFF0000u);
+  }
+}
+__device__ __forceinline__ u32x4 pack(const float (&f)[4]) {
+  return (u32x4){__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3])};
+}
+__device__ __forceinline__ u32x4 pack(const float (&f)[8]) {
+  return (u32x4){pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                 pack_bf16x2(f[6], f[7])};
+}
+
+// positions[p] = the row of pair p, from the two directions that the routing sort leaves: a
+// placed pair by its place, a pair whose id is no expert's by its id.
+__global__ __launch_bounds__(256) void positions_kernel(const int32_t* __restrict__ ids, int32_t npairs,
+                                                        int32_t experts,
+                                                        const int32_t* __restrict__ offsets,
+                                                        const int32_t* __restrict__ sorted_pairs,
+                                                        int32_t* __restrict__ positions) {
+  const int32_t i = (int32_t)(blockIdx.x * 256 + threadIdx.x);
+  if (i >= npairs) return;
+  if ((uint32_t)ids[i] >= (uint32_t)experts) positions[i] = -1;
+  if (i < offsets[experts]) {
+    const int32_t p = sorted_pairs[i];
+    if ((uint32_t)p < (uint32_t)npairs) positions[p] = i;
+  }
+}
+
+// One work item: a lane's piece of one token's row.  LPR lanes (a power of two, at most a wave)
+// take consecutive pieces of a row; a row needs `slices` such groups.  With LPR = 64 the token
+// is the same in the whole wave.
+struct Item {
+  int64_t token;
+  int64_t col;
+};
+template <int LPR, int E>
+__device__ __forceinline__ Item item(int64_t t, int64_t hidden) {
+  const uint32_t slices = (uint32_t)((hidden + LPR * E - 1) / (LPR * E));
+  int64_t group = ((int64_t)blockIdx.x * 256 + threadIdx.x) / LPR;
+  if constexpr (LPR == 64)
+    group = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  Item r;
+  r.token = group / slices;
+  r.col = ((group % slices) * LPR + (threadIdx.x & (LPR - 1))) * E;
+  if (r.col >= hidden) r.token = t;  // nothing to do
+  return r;
+}
+
+template <typename T, int LPR>
+__global__ __launch_bounds__(256) void permute_kernel(const T* __restrict__ x, int64_t t, int32_t topk,
+                                                      int64_t hidden, const int32_t* __restrict__ positions,
+                                                      T* __restrict__ rows) {
+  constexpr int E = 16 / (int)sizeof(T);
+  const Item it = item<LPR, E>(t, hidden);
+  if (it.token >= t) return;
+  const int64_t npairs = t * topk;
+  const int32_t* pos = positions + it.token * topk;
+  const T* src = x + it.token * hidden + it.col;
+  if (it.col + E <= hidden) {
+    const u32x4 v = load_piece(src);
+    for (int j = 0; j < topk; ++j) {
+      const int64_t r = pos[j];
+      if (r >= 0 && r < npairs) store_piece(rows + r * hidden + it.col, v);
+    }
+  } else {
+    for (int64_t c = it.col; c < hidden; ++c) {
+      const T v = src[c - it.col];
+      for (int j = 0; j < topk; ++j) {
+        const int64_t r = pos[j];
+        if (r >= 0 && r < npairs) rows[r * hidden + c] = v;
+      }
+    }
+  }
+}
+
+// y[t] = sum_j w[t][j] rows[pos[t][j]] in fp32, j in order; w null: 1.
+template <typename T, int LPR>
+__global__ __launch_bounds__(256) void unpermute_kernel(const T* __restrict__ rows,
+                                                        const int32_t* __restrict__ positions,
+                                                        const float* __restrict__ weights, int64_t t,
+                                                        int32_t topk, int64_t hidden, T* __restrict__ y) {
+  constexpr int E = 16 / (int)sizeof(T);
+  const Item it = item<LPR, E>(t, hidden);
+  if (it.token >= t) return;
+  const int64_t npairs = t * topk;
+  const int64_t p0 = it.token * topk;
+  T* dst = y + it.token * hidden + it.col;
+  if (it.col + E <= hidden) {
+    float acc[E];
+#pragma unroll
+    for (int i = 0; i < E; ++i) acc[i] = 0.f;
+    for (int j0 = 0; j0 < topk; j0 += 8) {
+      u32x4 v[8];
+      float w[8];
+#pragma unroll
+      for (int jj = 0; jj < 8; ++jj) {
+        w[jj] = 0.f;
+        v[jj] = (u32x4){0, 0, 0, 0};
+        if (j0 + jj < topk) {
+          const int64_t r = positions[p0 + j0 + jj];
+          if (r >= 0 && r < npairs) {
+            v[jj] = load_piece(rows + r * hidden + it.col);
+            w[jj] = weights ? weights[p0 + j0 + jj] : 1.f;
+          }
+        }
+      }
+#pragma unroll
+      for (int jj = 0; jj < 8; ++jj) {
+        float f[E];
+        unpack(v[jj], f);
+#pragma unroll
+        for (int i = 0; i < E; ++i) acc[i] = __builtin_fmaf(w[jj], f[i], acc[i]);
+      }
+    }
+    store_piece(dst, pack(acc));
+  } else {
+    for (int64_t c = it.col; c < hidden; ++c) {
+      float acc = 0.f;
+      for (int j = 0; j < topk; ++j) {
+        const int64_t r = positions[p0 + j];
+        if (r >= 0 && r < npairs)
+          acc = __builtin_fmaf(weights ? weights[p0 + j] : 1.f, to_f32(rows[r * hidden + c]), acc);
+      }
+      dst[c - it.col] = from_f32<T>(acc);
+    }
+  }
+}
+
+// One wave per pair: d_rows[pos] = w dy[token], d_w = <dy[token], rows[pos]> in fp32 (each lane
+// its pieces in order, then a tree over the lanes: a fixed order).
+template <typename T>
+__global__ __launch_bounds__(256) void unpermute_grad_kernel(const T* __restrict__ dy,
+                                                             const T* __restrict__ rows,
+                                                             const int32_t* __restrict__ positions,
+                                                             const float* __restrict__ weights,
+                                                             int64_t npairs, int32_t topk, int64_t hidden,
+                                                             T* __restrict__ d_rows,
+                                                             float* __restrict__ d_weights) {
+  constexpr int E = 16 / (int)sizeof(T);
+  const int lane = threadIdx.x & 63;
+  const int64_t p = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  if (p >= npairs) return;
+  const int64_t r = positions[p];
+  if (r < 0 || r >= npairs) {
+    if (d_weights && lane == 0) d_weights[p] = 0.f;
+    return;
+  }
+  const float w = weights ? weights[p] : 1.f;
+  const T* g = dy + p / topk * hidden;
+  float dot = 0.f;
+  for (int64_t c = (int64_t)lane * E; c < hidden; c += 64 * E) {
+    if (c + E <= hidden) {
+      float f[E], o[E];
+      unpack(load_piece(g + c), f);
+      if (d_weights) {
+        float v[E];
+        unpack(load_piece(rows + r * hidden + c), v);
+#pragma unroll
+        for (int i = 0; i < E; ++i) dot = __builtin_fmaf(f[i], v[i], dot);
+      }
+      if (d_rows) {
+#pragma unroll
+        for (int i = 0; i < E; ++i) o[i] = w * f[i];
+        store_piece(d_rows + r * hidden + c, pack(o));
+      }
+    } else {
+      for (int64_t cc = c; cc < hidden; ++cc) {
+        const float f = to_f32(g[cc]);
+        if (d_weights) dot = __builtin_fmaf(f, to_f32(rows[r * hidden + cc]), dot);
+        if (d_rows) d_rows[r * hidden + cc] = from_f32<T>(w * f);
+      }
+    }
+  }
+  if (d_weights) {
+#pragma unroll
+    for (int d = 32; d >= 1; d >>= 1) dot += __shfl_xor(dot, d);
+    if (lane == 0) d_weights[p] = dot;
+  }
+}
+
+// Workgroups for t rows of `hidden` elements, E per lane and LPR lanes per slice.
+int64_t row_wgs(int64_t t, int64_t hidden, int E, int LPR) {
+  const int64_t groups = t * ((hidden + (int64_t)LPR * E - 1) / ((int64_t)LPR * E));
+  return (groups * LPR + 255) / 256;
+}
+
+// Lanes per row slice: a whole wave, fewer for rows shorter than a wave's pieces.
+int row_lanes(int64_t hidden, int E) { return hidden > 32 * E ? 64 : hidden > 8 * E ? 32 : 8; }
+
+}  // namespace
+
+hipError_t launch_positions(const int32_t* ids, int64_t npairs, int32_t experts, const int32_t* offsets,
+                            const int32_t* sorted_pairs, int32_t* positions, hipStream_t stream) {
+  hipLaunchKernelGGL(positions_kernel, dim3((unsigned)((npairs + 255) / 256)), dim3(256), 0, stream, ids,
+                     (int32_t)npairs, experts, offsets, sorted_pairs, positions);
+  return hipGetLastError();
+}
+
+template <typename T>
+static hipError_t permute_t(const T* x, int64_t t, int32_t topk, int64_t hidden, const int32_t* positions,
+                            T* rows, hipStream_t s) {
+  constexpr int E = 16 / (int)sizeof(T);
+  const int lpr = row_lanes(hidden, E);
+  const int64_t wgs = row_wgs(t, hidden, E, lpr);
+  if (wgs > 0x7FFFFFFF) return hipErrorInvalidValue;
+  const dim3 grid((unsigned)wgs), block(256);
+  if (lpr == 64) hipLaunchKernelGGL((permute_kernel<T, 64>), grid, block, 0, s, x, t, topk, hidden, positions, rows);
+  else if (lpr == 32) hipLaunchKernelGGL((permute_kernel<T, 32>), grid, block, 0, s, x, t, topk, hidden, positions, rows);
+  else hipLaunchKernelGGL((permute_kernel<T, 8>), grid, block, 0, s, x, t, topk, hidden, positions, rows);
+  return hipGetLastError();
+}
+
+hipError_t launch_permute(const void* x, int f32, int64_t t, int32_t topk, int64_t hidden,
+                          const int32_t* positions, void* rows, hipStream_t stream) {
+  return f32 ? permute_t(static_cast<const float*>(x), t, topk, hidden, positions, static_cast<float*>(rows), stream)
+             : permute_t(static_cast<const uint16_t*>(x), t, topk, hidden, positions,
+                         static_cast<uint16_t*>(rows), stream);
+}
+
+template <typename T>
+static hipError_t unpermute_t(const T* rows, const int32_t* positions, const float* weights, int64_t t,
+                              int32_t topk, int64_t hidden, T* y, hipStream_t s) {
+  constexpr int E = 16 / (int)sizeof(T);
+  const int lpr = row_lanes(hidden, E);
+  const int64_t wgs = row_wgs(t, hidden, E, lpr);
+  if (wgs > 0x7FFFFFFF) return hipErrorInvalidValue;
+  const dim3 grid((unsigned)wgs), block(256);
+  if (lpr == 64) hipLaunchKernelGGL((unpermute_kernel<T, 64>), grid, block, 0, s, rows, positions, weights, t, topk, hidden, y);
+  else if (lpr == 32) hipLaunchKernelGGL((unpermute_kernel<T, 32>), grid, block, 0, s, rows, positions, weights, t, topk, hidden, y);
+  else hipLaunchKernelGGL((unpermute_kernel<T, 8>), grid, block, 0, s, rows, positions, weights, t, topk, hidden, y);
+  return hipGetLastError();
+}
+
+hipError_t launch_unpermute(const void* rows, int f32, const int32_t* positions, const float* weights,
+                            int64_t t, int32_t topk, int64_t hidden, void* y, hipStream_t stream) {
+  return f32 ? unpermute_t(static_cast<const float*>(rows), positions, weights, t, topk, hidden,
+                           static_cast<float*>(y), stream)
+             : unpermute_t(static_cast<const uint16_t*>(rows), positions, weights, t, topk, hidden,
+                           static_cast<uint16_t*>(y), stream);
+}
+
+hipError_t launch_unpermute_grad(const void* dy, const void* rows, int f32, const int32_t* positions,
+                                 const float* weights, int64_t t, int32_t topk, int64_t hidden,
+                                 void* d_rows, float* d_weights, hipStream_t stream) {
+  const int64_t npairs = t * topk;
+  const dim3 grid((unsigned)((npairs + 3) / 4)), block(256);
+  if (f32)
+    hipLaunchKernelGGL(unpermute_grad_kernel<float>, grid, block, 0, stream, static_cast<const float*>(dy),
+                       static_cast<const float*>(rows), positions, weights, npairs, topk, hidden,
+                       static_cast<float*>(d_rows), d_weights);
+  else
+    hipLaunchKernelGGL(unpermute_grad_kernel<uint16_t>, grid, block, 0, stream,
+                       static_cast<const uint16_t*>(dy), static_cast<const uint16_t*>(rows), positions,
+                       weights, npairs, topk, hidden, static_cast<uint16_t*>(d_rows), d_weights);
+  return hipGetLastError();
+}
+
+}  // namespace wq

@@ -94,6 +94,37 @@ hipError_t launch_ccq_encode(const float* w, int64_t n, int64_t k, int32_t zp, i
                              uint8_t* codes, uint8_t* qscale, float* super_scale,
                              float* code_scale, float* code_zero, hipStream_t stream);
 
+// MXFP4 quantisation of n rows of k values (bf16, or fp32 where f32 is set).
+hipError_t launch_mx_quantize(const void* x, int f32, int64_t n, int64_t k, uint8_t* codes,
+                              uint8_t* scales, hipStream_t stream);
+
+// Arguments of the products of two MXFP4 operands.
+struct MxArgs {
+  const uint8_t *w0_codes, *w0_scales;  // dense W / MoE gate / MoE down [experts][N][K]
+  const uint8_t *w1_codes, *w1_scales;  // MoE up (gate+up mode only)
+  const uint8_t *x_codes, *x_scales;    // rows: dense x; gate+up: tokens; down: h in expert order
+  void* out;                            // dense y [M][N]; MoE [pairs][N] in expert order
+  int64_t out_stride;                   // elements per output row
+  int32_t out_f32;                      // fp32 output instead of bf16 (not gate+up)
+  int32_t topk;
+  int64_t M;                            // dense rows; MoE: the largest number of pairs
+  int64_t N, K;
+  const int32_t* offsets;               // MoE: expert_offsets [experts + 1]
+  const int32_t* sorted_pairs;          // gate+up
+};
+hipError_t launch_mx_product(int mode, const MxArgs& args, int64_t experts, hipStream_t stream);
+
+// Token dispatch (rows bf16, or fp32 where f32 is set).
+hipError_t launch_positions(const int32_t* ids, int64_t npairs, int32_t experts, const int32_t* offsets,
+                            const int32_t* sorted_pairs, int32_t* positions, hipStream_t stream);
+hipError_t launch_permute(const void* x, int f32, int64_t t, int32_t topk, int64_t hidden,
+                          const int32_t* positions, void* rows, hipStream_t stream);
+hipError_t launch_unpermute(const void* rows, int f32, const int32_t* positions, const float* weights,
+                            int64_t t, int32_t topk, int64_t hidden, void* y, hipStream_t stream);
+hipError_t launch_unpermute_grad(const void* dy, const void* rows, int f32, const int32_t* positions,
+                                 const float* weights, int64_t t, int32_t topk, int64_t hidden,
+                                 void* d_rows, float* d_weights, hipStream_t stream);
+
 // Rows of one tile of the tiled kernel.
 int tiled_rows();
 

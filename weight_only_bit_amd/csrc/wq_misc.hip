@@ -69,6 +69,18 @@ __global__ __launch_bounds__(256) void dequant_kernel(const DevWeight w, int64_t
                    cvt_pk_bf16(v[14], v[15])};
 }
 
+// MXFP4: one thread per 8 weights (a dword of codes, one 16-byte store); blocks of 32 tile the
+// flat array, so rows play no part.
+__global__ __launch_bounds__(256) void dequant_mxfp4_kernel(const uint8_t* __restrict__ codes,
+                                                            const uint8_t* __restrict__ scales,
+                                                            int64_t octets, uint16_t* __restrict__ out) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= octets) return;
+  uint32_t p[8];
+  mxfp4_decode16(reinterpret_cast<const uint32_t*>(codes)[i], 0u, scales[i >> 2], p);
+  reinterpret_cast<u32x4*>(out)[i] = (u32x4){p[0], p[1], p[2], p[3]};
+}
+
 // CCQ without code cluster ("CCQ", section 3.5, "Dequantization without Code Cluster", with the
 // (4,3,2) and (3,3,2)(3,4,2) rows of the configuration table): one thread per 16 weights of a
 // group; each weight is read from its own code word,
@@ -429,6 +441,14 @@ __global__ __launch_bounds__(256) void combine_kernel(const float* __restrict__ 
 hipError_t launch_dequant(int fmt, const DevWeight& w, int64_t experts, uint16_t* out,
                           hipStream_t stream) {
   const int64_t rows = experts * w.n;
+  if (fmt == FMT_MXFP4) {
+    const int64_t octets = rows * (w.k / 8);
+    const int64_t wgs = (octets + 255) / 256;
+    if (wgs > 0x7FFFFFFF) return hipErrorInvalidValue;
+    hipLaunchKernelGGL(dequant_mxfp4_kernel, dim3((unsigned)wgs), dim3(256), 0, stream, w.codes,
+                       w.qscale, octets, out);
+    return hipGetLastError();
+  }
   const int64_t threads = rows * (w.k / 16);
   const dim3 grid((unsigned)((threads + 255) / 256));
   if (fmt == FMT_INT4)

@@ -35,12 +35,14 @@ constexpr int FMT_INT4PC = 8;  // INT4 with one scale per output channel (kernel
 constexpr int FMT_INT8PC = 9;  // INT8 with one scale per output channel (kernel variant)
 
 __host__ __device__ constexpr bool is_int4(int f) { return f == FMT_INT4 || f == FMT_INT4PC; }
+// Two weights per byte: 32 weights (an MXFP4 block) in a lane's 16 bytes.
+__host__ __device__ constexpr bool is_nibble(int f) { return is_int4(f) || f == FMT_MXFP4; }
 __host__ __device__ constexpr bool is_int8(int f) { return f == FMT_INT8 || f == FMT_INT8PC; }
 
 // Weights one lane decodes per step: 16 bytes of codes, or one group of the CCQ formats
 // without code cluster (22 or 20 bytes).
 template <int FMT>
-__host__ __device__ constexpr int lane_weights() { return is_int8(FMT) ? 16 : is_int4(FMT) ? 32 : 64; }
+__host__ __device__ constexpr int lane_weights() { return is_int8(FMT) ? 16 : is_nibble(FMT) ? 32 : 64; }
 
 // Columns per wave per LDS chunk: at least one step (4 lanes x lane_weights).
 template <int FMT, int KSPLIT>
@@ -52,7 +54,8 @@ __host__ __device__ constexpr int chunk_cols() {
 template <int FMT>
 struct Raw {
   u32x4 codes;
-  uint32_t scale;  // CCQ: the byte holding the 4-bit group scale; INT4 g64 / affine: bf16 bits
+  uint32_t scale;  // CCQ: the byte holding the 4-bit group scale; INT4 g64 / affine: bf16 bits;
+                   // MXFP4: the block's scale byte
   uint32_t zero;   // affine zero point
   u32x2 extra;     // (4,3,2): code bytes 16..23 of the aligned window; hybrid: bytes 16..19
 };
@@ -90,6 +93,7 @@ struct WaveW {
   int32_t row_zeros;
   uint32_t qshift;     // CCQ: 0 or 4, the nibble of the scale byte that is this lane's group;
                        // (4,3,2): 0 or 16, the bit offset of the group in its first dword
+  int32_t blocks;      // MXFP4: blocks from this lane's first one to the end of its row
   float cs, cz;        // CCQ code scale / code zero of this lane's row
   float fin;           // CCQ super scale / INT4 per-channel scale of this lane's row
 };
@@ -101,6 +105,7 @@ __device__ __forceinline__ WaveW<FMT> wave_weight(const DevWeight& w, int64_t e,
   WaveW<FMT> v;
   const int64_t n = w.n, k = w.k, G = k / 64;
   v.qshift = 0;
+  v.blocks = 0;
   v.cs = v.cz = 0.f;
   v.fin = 1.0f;
   v.row_scales = v.row_zeros = 0;
@@ -114,6 +119,12 @@ __device__ __forceinline__ WaveW<FMT> wave_weight(const DevWeight& w, int64_t e,
     } else {
       v.fin = bf16_bits_to_f32(w.scales[e * n + row]);
     }
+  } else if constexpr (FMT == FMT_MXFP4) {  // lane kb's 32 weights of step j: block 2 gb + 4 j + kb
+    v.codes = view(w.codes + e * n * (k / 2), n * (k / 2));
+    v.row_codes = (int32_t)(row * (k / 2) + gb * 32 + kb * 16);
+    v.scales = view(w.qscale + e * n * (k / 32), n * (k / 32));
+    v.row_scales = (int32_t)(row * (k / 32) + gb * 2 + kb);
+    v.blocks = (int32_t)(k / 32) - (gb * 2 + kb);
   } else if constexpr (is_int8(FMT)) {
     // a step is one group: lane kb holds weights 16 kb .. 16 kb + 15 of group gb + j
     v.codes = view(w.codes + e * n * k, n * k);
@@ -182,6 +193,11 @@ __device__ __forceinline__ void load_raw(Raw<FMT>& r, const WaveW<FMT>& v, int32
     r.zero = __builtin_amdgcn_raw_buffer_load_b8(at(v.zeros, st * 4), v.row_zeros, 0, 0);
   } else if constexpr (FMT == FMT_CCQ2) {
     r.scale = __builtin_amdgcn_raw_buffer_load_b8(at(v.scales, st * 2), v.row_scales, 0, 0);
+  } else if constexpr (FMT == FMT_MXFP4) {
+    // a block past the row's end would take the next row's scale, and its weights, multiplied by
+    // zero activations, would be NaN where that scale is: it reads past the array, that is 0
+    const int32_t off = 4 * st < v.blocks ? v.row_scales : 0x7FFFFFFF;
+    r.scale = __builtin_amdgcn_raw_buffer_load_b8(at(v.scales, st * 4), off, 0, 0);
   }
 }
 
@@ -240,7 +256,7 @@ __device__ __forceinline__ void step_mma(const Raw<FMT>& rw, const WaveW<FMT>& W
   } else if constexpr (FMT == FMT_INT8PC) {
     s24 = fin24;
     mzs = fin24 * (-128.0f / kTwo24);
-  } else {
+  } else if constexpr (FMT == FMT_AFFINE2) {
     const float s = bf16_bits_to_f32(rw.scale & 0xFFFFu);
     s24 = s * kTwo24;
     mzs = -(float)(rw.zero & 0xFFu) * s;
@@ -255,6 +271,8 @@ __device__ __forceinline__ void step_mma(const Raw<FMT>& rw, const WaveW<FMT>& W
       int4_decode16(rw.codes[2 * q], rw.codes[2 * q + 1], s24, mzs, p);
     } else if constexpr (is_int8(FMT)) {
       int8_decode16(rw.codes, s24, mzs, p);
+    } else if constexpr (FMT == FMT_MXFP4) {
+      mxfp4_decode16(rw.codes[2 * q], rw.codes[2 * q + 1], rw.scale & 0xFFu, p);
     } else {
       affine2_decode16(rw.codes[q], s24, mzs, p);
     }
@@ -533,7 +551,7 @@ constexpr int GEMV_LDS_MAX = 135168;  // 132 KiB: 16 rows of K = 4096 (one workg
 // with 16: their parts are shorter and their register budget a quarter).
 template <int FMT, int KS>
 __host__ __device__ constexpr int gemv_steps() {
-  return KS == 4 ? (is_int8(FMT) || is_int4(FMT) ? 16 : 8) : (is_int8(FMT) || is_int4(FMT) ? 4 : 2);
+  return KS == 4 ? (is_int8(FMT) || is_nibble(FMT) ? 16 : 8) : (is_int8(FMT) || is_nibble(FMT) ? 4 : 2);
 }
 
 template <int FMT, int KS, int MODE>
@@ -768,6 +786,7 @@ hipError_t dispatch_gemv(int fmt, int mode, const SkinnyArgs& args, int ks, int6
       return launch_gemv_fmt<FMT_INT8>(mode, args, ks, gy, pass_rows, stream);
     case FMT_CCQ432: return launch_gemv_fmt<FMT_CCQ432>(mode, args, ks, gy, pass_rows, stream);
     case FMT_CCQH: return launch_gemv_fmt<FMT_CCQH>(mode, args, ks, gy, pass_rows, stream);
+    case FMT_MXFP4: return launch_gemv_fmt<FMT_MXFP4>(mode, args, ks, gy, pass_rows, stream);
     default: return launch_gemv_fmt<FMT_CCQ2>(mode, args, ks, gy, pass_rows, stream);
   }
 }
@@ -791,6 +810,8 @@ hipError_t launch_skinny(int fmt, int mode, int m_tiles, int ksplit, const Skinn
       return launch_fmt<FMT_CCQ432>(mode, m_tiles, ksplit, args, grid_y, grid_z, stream);
     case FMT_CCQH:
       return launch_fmt<FMT_CCQH>(mode, m_tiles, ksplit, args, grid_y, grid_z, stream);
+    case FMT_MXFP4:
+      return launch_fmt<FMT_MXFP4>(mode, m_tiles, ksplit, args, grid_y, grid_z, stream);
     default: return launch_fmt<FMT_CCQ2>(mode, m_tiles, ksplit, args, grid_y, grid_z, stream);
   }
 }

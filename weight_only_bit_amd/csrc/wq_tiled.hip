@@ -41,6 +41,9 @@
 namespace wq {
 namespace {
 
+// Two weights per byte: 32 bytes of codes per 64-weight group.
+__host__ __device__ constexpr bool is_nibble(int f) { return f == FMT_INT4 || f == FMT_MXFP4; }
+
 constexpr int BM = 256;        // activation rows per full tile (8 MFMA row blocks of 32)
 constexpr int BN = 256;        // weight rows per tile (4 waves x 64)
 constexpr int BK = 64;         // k per step (one group)
@@ -70,8 +73,8 @@ __device__ __forceinline__ uint8_t* a_stage() {
 // without code cluster: the 64 weights of one row).
 template <int FMT>
 struct Codes {
-  u32x4 c;         // 2-bit formats: c.x, c.y (8 bytes); INT4 and (4,3,2) / hybrid: 16 bytes
-  uint32_t scale;  // CCQ: scale byte; INT4 / affine: bf16 bits
+  u32x4 c;         // 2-bit formats: c.x, c.y (8 bytes); INT4, MXFP4 and (4,3,2) / hybrid: 16 bytes
+  uint32_t scale;  // CCQ, MXFP4: scale byte; INT4 / affine: bf16 bits
   uint32_t zero;   // affine zero point
   u32x2 t;         // (4,3,2): bytes 16..23 of the aligned window; hybrid: bytes 16..19
   u32x4 c2;        // INT8: the second 16 bytes of the lane's 32 weights
@@ -80,9 +83,9 @@ struct Codes {
 // Where one weight row's packed data lives; the row is copied to LDS by one lane of its wave.
 struct RowSrc {
   const uint8_t* codes;    // row start
-  const uint8_t* scale;    // INT4 / affine: scales row (bf16, byte address); CCQ: qscale row
+  const uint8_t* scale;    // INT4 / affine: scales row (bf16, byte address); CCQ, MXFP4: qscale row
   const uint8_t* zeros;    // affine zero points row
-  int32_t gstep;           // bytes between groups' scales: 2 (INT4 g64, affine) or 0 (INT4
+  int32_t gstep;           // bytes between groups' scales: 2 (INT4 g64, MXFP4, affine) or 0 (INT4
                            // per channel); CCQ: unused (two 4-bit scales per byte)
 };
 
@@ -101,6 +104,10 @@ __device__ __forceinline__ RowSrc row_src(const DevWeight& w, int64_t e, int64_t
       r.scale = reinterpret_cast<const uint8_t*>(w.scales + grow);
       r.gstep = 0;
     }
+  } else if (FMT == FMT_MXFP4) {  // a group is two blocks, two scale bytes
+    r.codes = w.codes + grow * (k / 2);
+    r.scale = w.qscale + grow * (k / 32);
+    r.gstep = 2;
   } else if (FMT == FMT_AFFINE2) {
     r.codes = w.codes + grow * (k / 4);
     r.scale = reinterpret_cast<const uint8_t*>(w.scales + grow * G);
@@ -129,6 +136,9 @@ __device__ __forceinline__ void cdecode(const Codes<FMT>& p, const RowConst& r, 
     const float m128s = r.fin24 * (-128.0f / kTwo24);
     int8_decode16(p.c, r.fin24, m128s, a);
     int8_decode16(p.c2, r.fin24, m128s, b);
+  } else if (FMT == FMT_MXFP4) {
+    mxfp4_decode16(p.c.x, p.c.y, p.scale & 0xFFu, a);
+    mxfp4_decode16(p.c.z, p.c.w, p.scale & 0xFFu, b);
   } else if (FMT == FMT_INT4) {
     const float s24 = bf16_bits_to_f32(p.scale & 0xFFFFu) * kTwo24;
     const float m8s = s24 * (-8.0f / kTwo24);
@@ -151,7 +161,8 @@ __device__ __forceinline__ void cdecode(const Codes<FMT>& p, const RowConst& r, 
   }
 }
 
-// Packed-data LDS ring, per wave and stage: codes (64 rows x 16 bytes, INT4: two such halves),
+// Packed-data LDS ring, per wave and stage: codes (64 rows x 16 bytes, INT4 and MXFP4: two such
+// halves),
 // then one dword per row for the scale, then (affine) one for the zero point.  (4,3,2) and
 // hybrid: the first 16 bytes of each row's group window, then one (hybrid) or two ((4,3,2))
 // dwords per row for the rest.
@@ -159,16 +170,16 @@ __device__ __forceinline__ void cdecode(const Codes<FMT>& p, const RowConst& r, 
 // (the row's scale is read once); two stages fill the 160 KB with the activation ring exactly.
 template <int FMT>
 struct CodeRing {
-  static constexpr int CODE_BYTES = (FMT == FMT_INT8 ? 4 : FMT == FMT_INT4 ? 2 : 1) * 64 * 16;
+  static constexpr int CODE_BYTES = (FMT == FMT_INT8 ? 4 : is_nibble(FMT) ? 2 : 1) * 64 * 16;
   static constexpr int WAVE_BYTES =
       CODE_BYTES + (FMT == FMT_INT8 ? 0 : 256 * ((FMT == FMT_AFFINE2 || FMT == FMT_CCQ432) ? 2 : 1));
   static constexpr int STAGE_BYTES = 4 * WAVE_BYTES;
-  static constexpr int DEPTH = (FMT == FMT_INT4 || FMT == FMT_INT8) ? 2 : 4;  // fits 160 KB with A
+  static constexpr int DEPTH = (is_nibble(FMT) || FMT == FMT_INT8) ? 2 : 4;  // fits 160 KB with A
   static constexpr int AHEAD = DEPTH - 1 > 2 ? DEPTH - 1 : 2;  // steps between copy and decode
   // memory instructions per step per lane: codes, scale, zero / window pieces
   static constexpr int VMEM = FMT == FMT_INT8 ? 4
                              : is_alg2(FMT) ? (FMT == FMT_CCQ432 ? 3 : 2)
-                                            : (FMT == FMT_INT4 ? 2 : 1) + 1 + (FMT == FMT_AFFINE2 ? 1 : 0);
+                                            : (is_nibble(FMT) ? 2 : 1) + 1 + (FMT == FMT_AFFINE2 ? 1 : 0);
 };
 
 // Row tiles.  An expert's (or the dense matrix's) rows are covered by full 256-row tiles; the
@@ -345,7 +356,7 @@ __device__ __forceinline__ void tile_body(const TiledArgs& args, const CodeStage
             (__attribute__((address_space(3))) void*)(base + 1024 * i), 16, 0, 0);
       return;
     }
-    if constexpr (FMT == FMT_INT4) {
+    if constexpr (is_nibble(FMT)) {
       __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(rs.codes + g * 32),
                                        (__attribute__((address_space(3))) void*)(base), 16, 0, 0);
       __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(rs.codes + g * 32 + 16),
@@ -425,10 +436,10 @@ __device__ __forceinline__ void tile_body(const TiledArgs& args, const CodeStage
       return;
     }
     const uint32_t ca = (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) uint8_t*)(
-        base + (FMT == FMT_INT4 ? kh * 1024 + l32 * 16 : l32 * 16 + kh * 8));
+        base + (is_nibble(FMT) ? kh * 1024 + l32 * 16 : l32 * 16 + kh * 8));
     const uint32_t sa = (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) uint8_t*)(
         base + Ring::CODE_BYTES + l32 * 4);
-    if constexpr (FMT == FMT_INT4) {
+    if constexpr (is_nibble(FMT)) {
       u32x4 c0, c1;
       uint32_t s0, s1;
       asm volatile(
@@ -442,8 +453,9 @@ __device__ __forceinline__ void tile_body(const TiledArgs& args, const CodeStage
           : "memory");
       cc[0].c = c0;
       cc[1].c = c1;
-      cc[0].scale = s0;
-      cc[1].scale = s1;
+      // MXFP4: the lane's half of the group is one block, its scale the byte kh of the pair
+      cc[0].scale = FMT == FMT_MXFP4 ? s0 >> (8 * kh) : s0;
+      cc[1].scale = FMT == FMT_MXFP4 ? s1 >> (8 * kh) : s1;
     } else if constexpr (FMT == FMT_AFFINE2) {
       u32x2 c0, c1;
       uint32_t s0, s1, z0, z1;
@@ -935,6 +947,7 @@ hipError_t launch_mode(int fmt, const TiledArgs& a, int64_t row_tiles, hipStream
       return launch_t<FMT_INT8, MODE>(a, row_tiles, s);
     case FMT_CCQ432: return launch_t<FMT_CCQ432, MODE>(a, row_tiles, s);
     case FMT_CCQH: return launch_t<FMT_CCQH, MODE>(a, row_tiles, s);
+    case FMT_MXFP4: return launch_t<FMT_MXFP4, MODE>(a, row_tiles, s);
     default: return hipErrorInvalidValue;
   }
 }
