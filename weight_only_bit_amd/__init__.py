@@ -362,8 +362,7 @@ def wq_moe_ffn_noalloc(x, topk_ids, topk_weights, gate: PackedWeight, up: Packed
     _check(lib().wq_moe_ffn_noalloc(_ptr(x), t, hidden, _ptr(topk_ids), _ptr(topk_weights), topk,
                                     ctypes.byref(gate.cstruct()), ctypes.byref(up.cstruct()),
                                     ctypes.byref(down.cstruct()), _ptr(y), _stream()),
-           "wq_moe_ffn_noalloc", "wq_quantize_mx", "wq_gemm_mx", "wq_moe_gate_up_mx", "wq_moe_down_mx",
-           "wq_moe_positions", "wq_moe_permute", "wq_moe_unpermute", "wq_moe_unpermute_grad")
+           "wq_moe_ffn_noalloc")
     return y
 
 
