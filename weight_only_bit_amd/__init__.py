@@ -12,6 +12,7 @@ Names follow the C ABI: ``wq_dequantize``, ``wq_gemm``, ``wq_moe_route``, ``wq_m
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from dataclasses import dataclass, field
 
@@ -124,13 +125,18 @@ def _check(st: int, what: str):
 
 
 def _stream():
+    """The current device's current stream, as an address.  torch.cuda.current_stream() builds a
+    Stream object around the same number, 2.6 us a call; the number alone takes 0.2."""
     import torch
 
-    return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    if raw is not None:
+        return raw(torch.cuda.current_device())
+    return torch.cuda.current_stream().cuda_stream
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 # ---------------------------------------------------------------------------------------------
@@ -139,11 +145,17 @@ def _ptr(t):
 # bounds.  Every wrapper therefore checks its tensors here before the call.
 # ---------------------------------------------------------------------------------------------
 
-def _dtypes():
-    import torch
+_kinds = None
 
-    return {"bf16": (torch.bfloat16, torch.int16), "i32": (torch.int32,), "f32": (torch.float32,),
-            "u8": (torch.uint8, torch.int8)}
+
+def _dtypes():
+    global _kinds
+    if _kinds is None:
+        import torch
+
+        _kinds = {"bf16": (torch.bfloat16, torch.int16), "i32": (torch.int32,), "f32": (torch.float32,),
+                  "u8": (torch.uint8, torch.int8)}
+    return _kinds
 
 
 def _need(t, name, kind, shape=None, numel=None):
@@ -152,9 +164,9 @@ def _need(t, name, kind, shape=None, numel=None):
 
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch tensor, got {type(t).__name__}")
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{name}: must be a GPU tensor, got {t.device}")
-    if t.device.index != torch.cuda.current_device():
+    if t.get_device() != torch.cuda.current_device():
         raise ValueError(f"{name}: must be on the current GPU (cuda:{torch.cuda.current_device()}), "
                          f"got {t.device}")
     if t.dtype not in _dtypes()[kind]:
@@ -171,6 +183,7 @@ def _need(t, name, kind, shape=None, numel=None):
 # Element count and element size of each array a packed weight [E][n][k] holds, per format
 # (include/wq.h layouts); None where the format / group / k combination is not one the
 # library accepts (the library's own status then names the problem).
+@functools.lru_cache(maxsize=1024)
 def _layout(fmt, E, n, k, group):
     if k <= 0 or k % 64 or n <= 0 or E <= 0:
         return None
@@ -220,20 +233,18 @@ class PackedWeight:
             t = getattr(self, name)
             if t is None:
                 raise ValueError(f"PackedWeight.{name}: required by format {self.format}")
-            if not isinstance(t, torch.Tensor) or t.device.type != "cuda":
+            if not isinstance(t, torch.Tensor) or not t.is_cuda:
                 raise ValueError(f"PackedWeight.{name}: must be a GPU tensor")
-            if t.device.index != torch.cuda.current_device():
+            if t.get_device() != torch.cuda.current_device():
                 raise ValueError(f"PackedWeight.{name}: must be on the current GPU")
             if not t.is_contiguous():
                 raise ValueError(f"PackedWeight.{name}: must be contiguous")
             if t.element_size() != size or t.numel() != numel:
                 raise ValueError(f"PackedWeight.{name}: {t.numel()} elements of {t.element_size()} "
                                  f"bytes, the layout needs {numel} of {size}")
-        self._c = _CWeight(self.format, self.group, self.experts, self.n, self.k,
-                           *[None if getattr(self, f) is None else getattr(self, f).data_ptr()
-                             for f in ("codes", "scales", "zeros", "qscale", "super_scale",
-                                       "code_scale", "code_zero")],
-                           self.zp)
+        self._c = _CWeight(self.format, self.group, self.experts, self.n, self.k, _ptr(self.codes),
+                           _ptr(self.scales), _ptr(self.zeros), _ptr(self.qscale), _ptr(self.super_scale),
+                           _ptr(self.code_scale), _ptr(self.code_zero), self.zp)
         return self._c
 
     def nbytes(self) -> int:

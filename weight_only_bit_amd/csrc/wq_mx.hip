@@ -8,6 +8,8 @@
 // operands runs at four times the bf16 rate and reads 17/32 of a byte per value.
 #include <hip/hip_runtime.h>
 
+#include <type_traits>
+
 #include "wq_kernels.hpp"
 
 namespace wq {
@@ -75,16 +77,21 @@ __global__ __launch_bounds__(256) void mx_quantize_kernel(const T* __restrict__ 
 }
 
 // ---------------------------------------------------------------------------------------------
-// Products of two MXFP4 operands.  v_mfma_scale_f32_16x16x128_f8f6f4: lane l supplies row l % 16
-// of A (column of B), block l / 16 of the step's four blocks of 32, and that block's scale byte;
-// it receives D[4 (l / 16) + i][l % 16].  Every product of two codes is exact, the blocks' scales
-// are applied to the blocks' sums, and the accumulation is fp32.
+// Products of two MXFP4 operands.  Every product of two codes is exact, the blocks' scales are
+// applied to the blocks' sums, and the accumulation is fp32.
+//
+// Few rows: the weights stream from memory straight into v_mfma_scale_f32_16x16x128_f8f6f4 operands.
+// Lane l supplies row l % 16 of A (column of B) and one block of 32 with its scale byte; it receives
+// D[4 (l / 16) + i][l % 16].  In a step of 512 along k lane group q = l / 16 takes the blocks
+// 4 q .. 4 q + 3, one per instruction: 64 contiguous bytes of codes and one dword of scales, of which
+// instruction s reads byte s.  Any order of the k sum is the same product.
 // ---------------------------------------------------------------------------------------------
+template <int S>
 __device__ __forceinline__ f32x4 mfma_mx16(const u32x4& a, uint32_t sa, const u32x4& b, uint32_t sb,
                                            const f32x4& c) {
   const i32x8 av = {(int)a[0], (int)a[1], (int)a[2], (int)a[3], 0, 0, 0, 0};
   const i32x8 bv = {(int)b[0], (int)b[1], (int)b[2], (int)b[3], 0, 0, 0, 0};
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(av, bv, c, 4, 4, 0, (int)sa, 0, (int)sb);
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(av, bv, c, 4, 4, S, (int)sa, S, (int)sb);
 }
 
 __device__ __forceinline__ void store_out(void* out, int f32, int64_t at, float v) {
@@ -92,9 +99,33 @@ __device__ __forceinline__ void store_out(void* out, int f32, int64_t at, float 
   else reinterpret_cast<uint16_t*>(out)[at] = (uint16_t)f32_to_bf16_bits(v);
 }
 
+struct __attribute__((packed, aligned(2))) Scales4 {
+  uint32_t v;
+};
+
+// A lane's four blocks of a step: the row's codes and scales start at `codes` and `scales`.  A row
+// holds an even number of blocks; of those behind its end the codes are the row's first (any codes
+// do) and the scales 2^-127 on both sides: 2^-254 times 32 products of at most 36 is zero in fp32.
+struct Part {
+  u32x4 c[4];
+  uint32_t s;
+};
+__device__ __forceinline__ void load_part(Part& p, const uint8_t* codes, const uint8_t* scales, int32_t block,
+                                          int32_t nb) {
+  if (block + 4 <= nb) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) p.c[i] = *reinterpret_cast<const u32x4*>(codes + ((int64_t)(block + i) << 4));
+    p.s = reinterpret_cast<const Scales4*>(scales + block)->v;
+  } else {
+    const int64_t at = block < nb ? block : 0;
+    p.c[0] = p.c[2] = *reinterpret_cast<const u32x4*>(codes + (at << 4));
+    p.c[1] = p.c[3] = *reinterpret_cast<const u32x4*>(codes + (at << 4) + 16);
+    p.s = block < nb ? *reinterpret_cast<const uint16_t*>(scales + block) : 0u;
+  }
+}
+
 // One workgroup of KS waves computes 16 MT rows by 16 columns (gate+up: of both matrices); its
-// waves split the steps of 128 along k and their sums meet in LDS, in order.  Lanes whose block
-// lies past k multiply zero codes with scale 1.
+// waves split the steps along k and their sums meet in LDS, in order.
 template <int MODE, int MT, int KS>
 __global__ __launch_bounds__(64 * KS) void mx_stream_kernel(const MxArgs a) {
   constexpr int NM = MODE == MODE_GATEUP ? 2 : 1;
@@ -104,9 +135,8 @@ __global__ __launch_bounds__(64 * KS) void mx_stream_kernel(const MxArgs a) {
   const int nl = lane & 15, q = lane >> 4;
   const int64_t N = a.N;
   const int32_t nb = (int32_t)(a.K / 32);
-  const int32_t steps = (nb + 3) / 4;
-  const int32_t s_begin = (int32_t)((int64_t)steps * wave / KS);
-  const int32_t s_end = (int32_t)((int64_t)steps * (wave + 1) / KS);
+  const int32_t steps = (nb + 15) / 16;
+  const int32_t s_begin = steps * wave / KS, s_end = steps * (wave + 1) / KS;
 
   int64_t e = 0, m_base = 0, m_total = a.M;
   if constexpr (MODE == MODE_DENSE) {
@@ -147,61 +177,56 @@ __global__ __launch_bounds__(64 * KS) void mx_stream_kernel(const MxArgs a) {
     for (int j = 0; j < NM; ++j)
 #pragma unroll
       for (int t = 0; t < MT; ++t) acc[j][t] = (f32x4){0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-    for (int32_t s = s_begin; s < s_end; ++s) {
-      const int32_t blk = 4 * s + q;
-      const bool in = blk < nb;
-      const int32_t b = in ? blk : 0;
-      u32x4 w[NM], x[MT];
-      uint32_t wsc[NM], xsc[MT];
+    struct Step {
+      Part w[NM], x[MT];
+    };
+    auto load = [&](Step& p, int32_t s) __attribute__((always_inline)) {
 #pragma unroll
-      for (int j = 0; j < NM; ++j) {
-        w[j] = *reinterpret_cast<const u32x4*>(wc[j] + (int64_t)b * 16);
-        wsc[j] = ws[j][b];
-      }
+      for (int j = 0; j < NM; ++j) load_part(p.w[j], wc[j], ws[j], 16 * s + 4 * q, nb);
 #pragma unroll
-      for (int t = 0; t < MT; ++t) {
-        x[t] = *reinterpret_cast<const u32x4*>(xc[t] + (int64_t)b * 16);
-        xsc[t] = xs[t][b];
-      }
-      if (!in) {
+      for (int t = 0; t < MT; ++t) load_part(p.x[t], xc[t], xs[t], 16 * s + 4 * q, nb);
+    };
+    auto multiply = [&](const Step& p) __attribute__((always_inline)) {
 #pragma unroll
-        for (int j = 0; j < NM; ++j) {
-          w[j] = (u32x4){0, 0, 0, 0};
-          wsc[j] = 127;
-        }
+      for (int j = 0; j < NM; ++j)
 #pragma unroll
         for (int t = 0; t < MT; ++t) {
-          x[t] = (u32x4){0, 0, 0, 0};
-          xsc[t] = 127;
+          acc[j][t] = mfma_mx16<0>(p.x[t].c[0], p.x[t].s, p.w[j].c[0], p.w[j].s, acc[j][t]);
+          acc[j][t] = mfma_mx16<1>(p.x[t].c[1], p.x[t].s, p.w[j].c[1], p.w[j].s, acc[j][t]);
+          acc[j][t] = mfma_mx16<2>(p.x[t].c[2], p.x[t].s, p.w[j].c[2], p.w[j].s, acc[j][t]);
+          acc[j][t] = mfma_mx16<3>(p.x[t].c[3], p.x[t].s, p.w[j].c[3], p.w[j].s, acc[j][t]);
         }
+    };
+    // two steps at hand, the next one's loads in flight under each product
+    if (s_begin < s_end) {
+      Step A, B;
+      load(A, s_begin);
+      int32_t s = s_begin;
+      for (; s + 2 < s_end; s += 2) {
+        load(B, s + 1);
+        multiply(A);
+        load(A, s + 2);
+        multiply(B);
       }
-#pragma unroll
-      for (int j = 0; j < NM; ++j)
-#pragma unroll
-        for (int t = 0; t < MT; ++t) acc[j][t] = mfma_mx16(x[t], xsc[t], w[j], wsc[j], acc[j][t]);
+      if (s + 1 < s_end) load(B, s + 1);
+      multiply(A);
+      if (s + 1 < s_end) multiply(B);
     }
-    if (KS > 1) {
-      if (ms > 0) __syncthreads();  // the previous pass's sums have been read
+    if (ms > 0) __syncthreads();  // the previous pass's sums have been read
 #pragma unroll
-      for (int j = 0; j < NM; ++j)
+    for (int j = 0; j < NM; ++j)
 #pragma unroll
-        for (int t = 0; t < MT; ++t) red[wave][j * MT + t][lane] = acc[j][t];
-      __syncthreads();
-    }
+      for (int t = 0; t < MT; ++t) red[wave][j * MT + t][lane] = acc[j][t];
+    __syncthreads();
     // row tile t is finished by wave t % KS
 #pragma unroll
     for (int t = 0; t < MT; ++t) {
-      if (KS > 1 && wave != t % KS) continue;
-      f32x4 g = acc[0][t], u = acc[NM - 1][t];
-      if (KS > 1) {
-        g = red[0][t][lane];
-        u = red[0][(NM - 1) * MT + t][lane];
+      if (wave != t % KS) continue;
+      f32x4 g = red[0][t][lane], u = red[0][(NM - 1) * MT + t][lane];
 #pragma unroll
-        for (int p = 1; p < KS; ++p) {
-          g += red[p][t][lane];
-          if constexpr (NM == 2) u += red[p][MT + t][lane];
-        }
+      for (int p = 1; p < KS; ++p) {
+        g += red[p][t][lane];
+        if constexpr (NM == 2) u += red[p][MT + t][lane];
       }
       if (!nvalid) continue;
 #pragma unroll
@@ -224,6 +249,591 @@ hipError_t launch_stream(const MxArgs& a, int64_t gy, int64_t gz, hipStream_t s)
   return hipGetLastError();
 }
 
+// ---------------------------------------------------------------------------------------------
+// Many rows: tiles staged in LDS.
+//
+// One workgroup of 4 waves, one per SIMD, computes 64 WM rows by 64 WN columns (256 x 256 for the
+// large products); each wave 32 WM by 32 WN of them, as WM x WN blocks of 32 x 32 in registers.  k
+// advances 256 per stage: 128 bytes of codes and 8 scale bytes per row.
+//   * The weights are the A operand of v_mfma_scale_f32_32x32x64_f8f6f4 and the activations the B
+//     operand, so a lane ends with four consecutive outputs of one row.  Lane (l, h) supplies row l
+//     and a block of 32: slice s of a stage takes block 4 h + s, so a lane's four blocks are 64
+//     contiguous bytes and their scales one dword, of which slice s reads byte s (the instruction's
+//     byte select).  Any order of the k sum is the same product.
+//   * Codes pass through registers to LDS (16 bytes per lane, 8 lanes per row), which holds two
+//     stages; the registers hold a third, on its way.  Rows are 128 bytes, 16-byte piece p of row r
+//     in slot p ^ (r / 2 % 8), which keeps the fragment reads free of bank conflicts.  (Copies to
+//     LDS without registers have to wait for the buffer that they fill, so that all of a stage's
+//     are issued at once and its MFMAs wait behind them: measured 1.75 us per stage of 256 CUs
+//     where the copies alone and the rest alone take 0.95 each.)  Thread t carries the scales of
+//     rows t the same way.
+//   * The next slice's fragments are read under the current slice's MFMAs; the last slice of a
+//     stage is multiplied after the barrier that ends the stage, over the next stage's first reads.
+// Results of rows behind a ragged tile's end and of columns behind N are not stored.
+// ---------------------------------------------------------------------------------------------
+constexpr int kStageBytes = 128;  // codes of one row of a stage
+
+__device__ __forceinline__ f32x16 mfma_mx32(const u32x4& a, uint32_t sa, const u32x4& b, uint32_t sb,
+                                            const f32x16& c, std::integral_constant<int, 0>) {
+  const i32x8 av = {(int)a[0], (int)a[1], (int)a[2], (int)a[3], 0, 0, 0, 0};
+  const i32x8 bv = {(int)b[0], (int)b[1], (int)b[2], (int)b[3], 0, 0, 0, 0};
+  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(av, bv, c, 4, 4, 0, (int)sa, 0, (int)sb);
+}
+__device__ __forceinline__ f32x16 mfma_mx32(const u32x4& a, uint32_t sa, const u32x4& b, uint32_t sb,
+                                            const f32x16& c, std::integral_constant<int, 1>) {
+  const i32x8 av = {(int)a[0], (int)a[1], (int)a[2], (int)a[3], 0, 0, 0, 0};
+  const i32x8 bv = {(int)b[0], (int)b[1], (int)b[2], (int)b[3], 0, 0, 0, 0};
+  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(av, bv, c, 4, 4, 1, (int)sa, 1, (int)sb);
+}
+__device__ __forceinline__ f32x16 mfma_mx32(const u32x4& a, uint32_t sa, const u32x4& b, uint32_t sb,
+                                            const f32x16& c, std::integral_constant<int, 2>) {
+  const i32x8 av = {(int)a[0], (int)a[1], (int)a[2], (int)a[3], 0, 0, 0, 0};
+  const i32x8 bv = {(int)b[0], (int)b[1], (int)b[2], (int)b[3], 0, 0, 0, 0};
+  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(av, bv, c, 4, 4, 2, (int)sa, 2, (int)sb);
+}
+__device__ __forceinline__ f32x16 mfma_mx32(const u32x4& a, uint32_t sa, const u32x4& b, uint32_t sb,
+                                            const f32x16& c, std::integral_constant<int, 3>) {
+  const i32x8 av = {(int)a[0], (int)a[1], (int)a[2], (int)a[3], 0, 0, 0, 0};
+  const i32x8 bv = {(int)b[0], (int)b[1], (int)b[2], (int)b[3], 0, 0, 0, 0};
+  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(av, bv, c, 4, 4, 3, (int)sa, 3, (int)sb);
+}
+
+struct TileLds {
+  uint8_t* x[2];
+  uint8_t* w[2];
+  uint8_t* s[2];  // 8 scale bytes per row: activation rows, then weight rows
+};
+
+struct __attribute__((packed, aligned(2))) Scales8 {
+  uint64_t v;
+};
+struct __attribute__((packed, aligned(2))) Out16 {
+  u32x4 v;
+};
+
+// Rows row0 .. row0 + rows - 1 (at most 64 WM) of expert e, columns of tile ctile.
+// ROOM: bytes of LDS that the epilogue has for each wave.
+template <int MODE, int WM, int WN, int BUFS, int ROOM>
+__device__ __forceinline__ void mx_tile(const MxArgs& a, const TileLds& lds, int64_t e, int64_t row0,
+                                        int64_t rows, int64_t ctile) {
+  constexpr int XR = 64 * WM, WR = 64 * WN;                   // rows of a stage
+  constexpr int NJ = MODE == MODE_GATEUP ? WN / 2 : WN;       // output blocks of a wave's columns
+  static_assert(MODE != MODE_GATEUP || WN % 2 == 0, "gate and up blocks pair up");
+  const int tid = threadIdx.x;
+  const int lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int l32 = lane & 31, h = lane >> 5;
+  const int wx = wave & 1, ww = wave >> 1;
+  const int64_t N = a.N, half = a.K / 2;
+  const int32_t nb = (int32_t)(a.K / 32);
+  const int32_t steps = (nb + 7) / 8, last = steps - 1;
+  const int64_t n0 = ctile * (64 * NJ);
+
+  // Stage row r of the weights: wave column ww = r / (32 WN), block j = r / 32 % WN; gate+up:
+  // blocks below WN / 2 are gate channels, the others the same channels of up.
+  auto weight_row = [&](int r, bool& up) __attribute__((always_inline)) {
+    const int c = r / (32 * WN), j = r / 32 % WN;
+    up = MODE == MODE_GATEUP && j >= NJ;
+    const int64_t n = n0 + 32 * (c * NJ + (up ? j - NJ : j)) + r % 32;
+    return e * N + (n < N ? n : N - 1);
+  };
+  auto token_row = [&](int r) __attribute__((always_inline)) {
+    const int64_t g = row0 + (r < rows ? r : 0);
+    return MODE == MODE_GATEUP ? (int64_t)(a.sorted_pairs[g] / a.topk) : g;
+  };
+
+  // load role: load i of wave w brings stage rows 32 i + 8 w .. + 7, lane l the piece for its row's
+  // slot l % 8.  Loads go through buffer resources: a uniform base for the 32 rows and the stage, and
+  // a lane offset that is the same for every load (gate+up: one per row of tokens); rows behind the
+  // tile's or the matrix's end lie out of range and read zeros.
+  const int piece = (lane & 7) ^ ((4 * wave + (lane >> 4)) & 7);
+  const uint32_t off = (uint32_t)((8 * wave + (lane >> 3)) * (uint32_t)half + piece * 16);
+  uint32_t xoff[MODE == MODE_GATEUP ? 2 * WM : 1];
+  if constexpr (MODE == MODE_GATEUP) {
+#pragma unroll
+    for (int i = 0; i < 2 * WM; ++i)
+      xoff[i] = (uint32_t)(token_row(32 * i + 8 * wave + (lane >> 3)) * half) + piece * 16;
+  }
+  // scale role: thread t carries the scales of activation row t and of weight row t; with fewer rows
+  // than threads several carry the same (a branch would cut the loop's code in two, and the compiler
+  // moves MFMAs, whose results nothing waits for, from the first part into the second)
+  const int xr = tid % XR, wrow = tid % WR;
+  const uint8_t* xsc = a.x_scales + token_row(xr) * nb;
+  const uint8_t* wsc;
+  {
+    bool up;
+    const int64_t r = weight_row(wrow, up);
+    wsc = (up ? a.w1_scales : a.w0_scales) + r * nb;
+  }
+  // In the last stage of a k that is no multiple of 256 the pieces behind k are filled with the
+  // stage before's: any codes do, their blocks' scales are 2^-127 on both sides, and 2^-254 times
+  // 32 products of at most 36 is zero in fp32.
+  const int32_t behind = (int64_t)last * kStageBytes + piece * 16 >= half ? kStageBytes : 0;
+
+  // A stage's codes pass through NC registers of 16 bytes per lane, in four groups: fetch loads
+  // group q of stage g, put writes it to the buffers.
+  constexpr int NX = 2 * WM, NC = 2 * WM + 2 * WN;
+  u32x4 held[NC];
+  auto fetch_to = [&](u32x4(&to)[NC], int32_t g, auto qc) __attribute__((always_inline)) {
+    constexpr int Q = decltype(qc)::value;
+    const int32_t gc = g < last ? g : last;  // stages behind the last one load it again
+    // a lane's offset is never below zero: what it does not go back it goes on from the stage before
+    const uint32_t on = kStageBytes - (gc == last ? (uint32_t)behind : 0u);
+    const int32_t at = (gc - 1) * kStageBytes;
+    auto load = [&](const uint8_t* base, int32_t bytes, uint32_t lane_off) __attribute__((always_inline)) {
+      const int32_t left = bytes - at;  // ranges are below 2^31 - 128 (checked on the host)
+      const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
+          const_cast<uint8_t*>(base + at), (short)0, left > 0 ? left : 0, 0x00020000);
+      return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, (int)(lane_off + on), 0, 0));
+    };
+#pragma unroll
+    for (int i = NC * Q / 4; i < NC * (Q + 1) / 4; ++i) {
+      if (i < NX) {
+        if constexpr (MODE == MODE_GATEUP)
+          to[i] = load(a.x_codes, (int32_t)(a.M / a.topk * half), xoff[i < NX ? i : 0]);
+        else
+          to[i] = load(a.x_codes + (row0 + 32 * i) * half, (int32_t)((rows - 32 * i) * half), off);
+      } else {
+        // rows 32 (i - NX) .. + 31 of the stage: block (i - NX) % WN of wave column (i - NX) / WN
+        const int c = (i - NX) / WN, j = (i - NX) % WN;
+        const bool up = MODE == MODE_GATEUP && j >= NJ;
+        const int64_t n = n0 + 32 * (c * NJ + (up ? j - NJ : j));
+        to[i] = load((up ? a.w1_codes : a.w0_codes) + (e * N + n) * half, (int32_t)((N - n) * half), off);
+      }
+    }
+  };
+  auto fetch = [&](int32_t g, auto qc) __attribute__((always_inline)) { fetch_to(held, g, qc); };
+  auto put_from = [&](const u32x4(&from)[NC], auto qc, auto stc) __attribute__((always_inline)) {
+    constexpr int Q = decltype(qc)::value, ST = decltype(stc)::value;
+#pragma unroll
+    for (int i = NC * Q / 4; i < NC * (Q + 1) / 4; ++i) {
+      uint8_t* const to = i < NX ? lds.x[ST] + (32 * i + 8 * wave) * kStageBytes
+                                 : lds.w[ST] + (32 * (i - NX) + 8 * wave) * kStageBytes;
+      *reinterpret_cast<u32x4*>(to + lane * 16) = from[i];
+    }
+  };
+  auto put = [&](auto qc, auto stc) __attribute__((always_inline)) { put_from(held, qc, stc); };
+  // The stage's 8 scale bytes of a row.  The last, partial stage reads the row's last 8 bytes and
+  // moves the ones it needs down (k >= 256: a row has 8); blocks behind k get byte 0, a finite scale.
+  struct Scales {
+    uint64_t x, w;
+  };
+  Scales scales;
+  auto load_scales = [&](int32_t g) __attribute__((always_inline)) {
+    const int32_t at = 8 * g < nb - 8 ? 8 * g : nb - 8;  // also behind the last stage
+    return Scales{reinterpret_cast<const Scales8*>(xsc + at)->v, reinterpret_cast<const Scales8*>(wsc + at)->v};
+  };
+  auto put_scales = [&](const Scales& v, int32_t g, auto stc) __attribute__((always_inline)) {
+    constexpr int ST = decltype(stc)::value;
+    g = g < last ? g : last;
+    const int32_t over = 8 * g > nb - 8 ? 8 * (8 * g - (nb - 8)) : 0;
+    *reinterpret_cast<uint64_t*>(lds.s[ST] + xr * 8) = v.x >> over;
+    *reinterpret_cast<uint64_t*>(lds.s[ST] + (XR + wrow) * 8) = v.w >> over;
+  };
+
+  f32x16 acc[WM][WN];
+#pragma unroll
+  for (int i = 0; i < WM; ++i)
+#pragma unroll
+    for (int j = 0; j < WN; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
+
+  struct Frag {
+    u32x4 x[WM], w[WN];
+  };
+  uint32_t sx[2][WM], sw[2][WN];
+  // Row r's piece 4 h + s lies at 128 r + 16 ((4 h + s) ^ (r / 2 % 8)); a lane's rows are 32 apart, so
+  // its addresses of slice s are one base, its low bits exclusive-or 16 s, plus constants.
+  const uint32_t fslot = (uint32_t)(((4 * h) ^ ((l32 >> 1) & 7)) << 4);
+  const uint32_t fw = (uint32_t)((32 * WN * ww + l32) * kStageBytes) + fslot;
+  const uint32_t fx = (uint32_t)((32 * WM * wx + l32) * kStageBytes) + fslot;
+  const uint32_t fsw = (uint32_t)((XR + 32 * WN * ww + l32) * 8 + 4 * h);
+  const uint32_t fsx = (uint32_t)((32 * WM * wx + l32) * 8 + 4 * h);
+  auto read = [&](Frag& f, int s, auto stc) __attribute__((always_inline)) {
+    constexpr int ST = decltype(stc)::value;
+    const uint8_t* const w = lds.w[ST] + (fw ^ (uint32_t)(s << 4));
+    const uint8_t* const x = lds.x[ST] + (fx ^ (uint32_t)(s << 4));
+#pragma unroll
+    for (int j = 0; j < WN; ++j) f.w[j] = *reinterpret_cast<const u32x4*>(w + 32 * kStageBytes * j);
+#pragma unroll
+    for (int i = 0; i < WM; ++i) f.x[i] = *reinterpret_cast<const u32x4*>(x + 32 * kStageBytes * i);
+  };
+  auto read_scales = [&](auto stc) __attribute__((always_inline)) {
+    constexpr int ST = decltype(stc)::value;
+#pragma unroll
+    for (int j = 0; j < WN; ++j) sw[ST][j] = *reinterpret_cast<const uint32_t*>(lds.s[ST] + fsw + 256 * j);
+#pragma unroll
+    for (int i = 0; i < WM; ++i) sx[ST][i] = *reinterpret_cast<const uint32_t*>(lds.s[ST] + fsx + 256 * i);
+  };
+  auto mma = [&](const Frag& f, auto sc, auto stc) __attribute__((always_inline)) {
+    constexpr int ST = decltype(stc)::value;
+#pragma unroll
+    for (int i = 0; i < WM; ++i)
+#pragma unroll
+      for (int j = 0; j < WN; ++j)
+        acc[i][j] = mfma_mx32(f.w[j], sw[ST][j], f.x[i], sx[ST][i], acc[i][j], sc);
+  };
+  constexpr std::integral_constant<int, 0> c0{};
+  constexpr std::integral_constant<int, 1> c1{};
+  constexpr std::integral_constant<int, 2> c2{};
+  constexpr std::integral_constant<int, 3> c3{};
+
+  // ---- prologue: stage 0 written and the next on its way; with two buffers the first group of
+  // stage 1 is written, too, and that of stage 2 on its way; stage 0's first slice read ----
+  Frag X;
+  if constexpr (BUFS == 2) {
+    u32x4 early[NC];
+    const Scales s0 = load_scales(0), s1 = load_scales(1);
+    fetch_to(early, 0, c0);
+    fetch_to(early, 0, c1);
+    fetch_to(early, 0, c2);
+    fetch_to(early, 0, c3);
+    fetch(1, c0);
+    fetch(1, c1);
+    fetch(1, c2);
+    fetch(1, c3);
+    put_scales(s0, 0, c0);
+    put_from(early, c0, c0);
+    put_from(early, c1, c0);
+    put_from(early, c2, c0);
+    put_from(early, c3, c0);
+    put_scales(s1, 1, c1);
+    scales = load_scales(2);
+    put(c0, c1);
+    fetch(2, c0);
+    __syncthreads();
+    read_scales(c0);
+    read(X, 0, c0);
+  } else {
+    scales = load_scales(0);
+    fetch(0, c0);
+    fetch(0, c1);
+    fetch(0, c2);
+    fetch(0, c3);
+    put_scales(scales, 0, c0);
+    put(c0, c0);
+    put(c1, c0);
+    put(c2, c0);
+    put(c3, c0);
+    scales = load_scales(1);
+    fetch(1, c0);
+    fetch(1, c1);
+    fetch(1, c2);
+    fetch(1, c3);
+    __builtin_amdgcn_s_waitcnt(0xC07F);
+    __builtin_amdgcn_s_barrier();
+  }
+
+  // ---- stage g in buffers ST = g % 2 ----
+  // Each slice's MFMAs cover the next slice's fragment reads, one group's writes to the other
+  // buffers (a stage ahead) and, into the registers that frees, its loads (two stages ahead): a
+  // load has a whole stage to arrive, and no wait but a write's own counts it.
+  // Masks: 0x8 MFMA, 0x20 loads, 0x100 LDS reads, 0x200 LDS writes.
+  auto stage = [&](int32_t g, auto stc) __attribute__((always_inline)) {
+    constexpr int ST = decltype(stc)::value;
+    constexpr std::integral_constant<int, ST ^ 1> other{};
+    constexpr int NF = WM * WN, NR = WM + WN;  // MFMAs and fragment reads of a slice
+    constexpr int NP = (NC + 3) / 4;           // pieces of a group
+    auto interleave = [&](auto extra) __attribute__((always_inline)) {
+      constexpr int XR2 = decltype(extra)::value;  // scale reads, a write and two loads
+#pragma unroll
+      for (int i = 0; i < (NF > 4 ? NF : 4); ++i) {
+        constexpr int each = NF >= 8 ? 1 : 4;
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        if (i * each < NR + XR2) __builtin_amdgcn_sched_group_barrier(0x100, each + (XR2 ? 1 : 0), 0);
+        if (NF >= 8 ? i >= NF / 2 && i < NF / 2 + NP : true) {
+          __builtin_amdgcn_sched_group_barrier(0x200, 1, 0);
+          __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    Frag Y;
+    __builtin_amdgcn_sched_barrier(0);
+    read(Y, 1, stc);
+    put(c1, other);
+    fetch(g + 2, c1);
+    mma(X, c0, stc);
+    interleave(c0);
+    read(X, 2, stc);
+    put(c2, other);
+    fetch(g + 2, c2);
+    mma(Y, c1, stc);
+    interleave(c0);
+    read(Y, 3, stc);
+    put(c3, other);
+    fetch(g + 2, c3);
+    mma(X, c2, stc);
+    interleave(c0);
+    // This wave's writes of stage g + 1 are done and its reads of stage g returned; after the barrier
+    // that holds for every wave, so g + 1 may be read and g's buffers written.
+    __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+    read_scales(other);
+    read(X, 0, other);
+    put_scales(scales, g + 2, stc);
+    scales = load_scales(g + 3);
+    put(c0, stc);
+    fetch(g + 3, c0);
+    mma(Y, c3, stc);
+    interleave(std::integral_constant<int, NR>{});
+  };
+  // One buffer: the stage's last slice is multiplied over the writes of the next stage and the loads
+  // of the one after; the CU's second workgroup fills what the reads and the two barriers leave
+  // idle.  A wave has 256 registers, so each slice's fragments are read when the last one's are used.
+  auto stage1 = [&](int32_t g) __attribute__((always_inline)) {
+    constexpr int NF = WM * WN;
+    __builtin_amdgcn_sched_barrier(0);
+    read_scales(c0);
+    read(X, 0, c0);
+    mma(X, c0, c0);
+    __builtin_amdgcn_sched_barrier(0);
+    read(X, 1, c0);
+    mma(X, c1, c0);
+    __builtin_amdgcn_sched_barrier(0);
+    read(X, 2, c0);
+    mma(X, c2, c0);
+    __builtin_amdgcn_sched_barrier(0);
+    read(X, 3, c0);
+    __builtin_amdgcn_s_waitcnt(0xC07F);  // this wave's reads of the stage have returned
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+    put_scales(scales, g + 1, c0);
+    put(c0, c0);
+    put(c1, c0);
+    put(c2, c0);
+    put(c3, c0);
+    scales = load_scales(g + 2);
+    fetch(g + 2, c0);
+    fetch(g + 2, c1);
+    fetch(g + 2, c2);
+    fetch(g + 2, c3);
+    mma(X, c3, c0);
+#pragma unroll
+    for (int i = 0; i < NF; ++i) {
+      __builtin_amdgcn_sched_group_barrier(0x200, (NC + 2 + NF - 1) / NF, 0);
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x020, (NC + 2 + NF - 1) / NF, 0);
+    }
+    __builtin_amdgcn_s_waitcnt(0xC07F);  // the next stage is written
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  int32_t g = 0;
+  if constexpr (BUFS == 2) {
+    for (; g + 1 < steps; g += 2) {
+      stage(g, c0);
+      stage(g + 1, c1);
+    }
+    if (g < steps) stage(g, c0);
+  } else {
+    for (; g < steps; ++g) stage1(g);
+  }
+  __syncthreads();
+
+  // ---- epilogue: lane (l, h) holds, of each block, row l and columns 8 q + 4 h + t (register
+  // 4 q + t).  Each wave passes its blocks through an LDS array of its own, so that rows leave in
+  // 16-byte pieces; piece p of row m lies in slot p ^ (m / rows per 256 bytes), free of conflicts.
+  // ----
+  // Two buffers: one array per wave.  One buffer: a quarter of its arrays each.
+  uint8_t* const tile = BUFS == 2 ? (wave == 0 ? lds.x[0] : wave == 1 ? lds.x[1] : wave == 2 ? lds.w[0] : lds.w[1])
+                                  : lds.x[0] + wave * ROOM;
+  auto value = [&](int i, int j, int r) __attribute__((always_inline)) {
+    if constexpr (MODE == MODE_GATEUP) return silu_f32(acc[i][j][r]) * acc[i][NJ + j][r];
+    else return acc[i][j][r];
+  };
+  const int mw = 32 * WM * wx;  // the wave's first row of the tile
+  // BI blocks of rows at a time by BJ of columns: [32 BI rows][32 BJ columns] of EB bytes
+  auto flush = [&](auto eb, auto first, auto count, auto jfirst, auto jcount) __attribute__((always_inline)) {
+    constexpr int EB = decltype(eb)::value, I0 = decltype(first)::value, BI = decltype(count)::value;
+    constexpr int J0 = decltype(jfirst)::value, BJ = decltype(jcount)::value;
+    constexpr int P = 32 * BJ * EB / 16;  // pieces per row
+    static_assert(32 * BI * 16 * P <= ROOM, "the blocks fit");
+    const int64_t nw = n0 + 32 * (NJ * ww + J0);  // the wave's first column
+    constexpr int PE = 16 / EB;
+    auto slot = [](int m, int p) __attribute__((always_inline)) {
+      return P >= 16 ? p ^ (m & 15) : p ^ ((m / (16 / P)) & (P - 1));
+    };
+#pragma unroll
+    for (int i = 0; i < BI; ++i) {
+      const int m = 32 * i + l32;
+#pragma unroll
+      for (int j = 0; j < BJ; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          float v[4];
+#pragma unroll
+          for (int t = 0; t < 4; ++t) v[t] = value(I0 + i, J0 + j, 4 * q + t);
+          if constexpr (EB == 2) {
+            *reinterpret_cast<u32x2*>(tile + m * (16 * P) + slot(m, 4 * j + q) * 16 + 8 * h) =
+                (u32x2){cvt_pk_bf16(v[0], v[1]), cvt_pk_bf16(v[2], v[3])};
+          } else {
+            *reinterpret_cast<f32x4*>(tile + m * (16 * P) + slot(m, 8 * j + 2 * q + h) * 16) =
+                (f32x4){v[0], v[1], v[2], v[3]};
+          }
+        }
+    }
+    // only this wave reads what it wrote: its own reads follow its writes
+    __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
+    __builtin_amdgcn_wave_barrier();
+    const int left = (int)(rows - mw - 32 * I0 < 32 * BI ? rows - mw - 32 * I0 : 32 * BI);
+    uint8_t* const base = static_cast<uint8_t*>(a.out) + ((row0 + mw + 32 * I0) * a.out_stride + nw) * EB;
+    const int64_t pitch = a.out_stride * EB;
+    // pieces of whole rows: lane's piece is the same in every round when 64 lanes cover whole rows
+    const int p = lane % P;
+    const int whole = (int)(N - nw >= 32 * BJ ? PE : N - nw - p * PE >= PE ? PE : N - nw - p * PE);  // its elements
+    constexpr int RPR = 64 / P, ROUNDS = 32 * BI / RPR, BATCH = ROUNDS < 4 ? ROUNDS : 4;  // rows a round
+    const int m0 = lane / P;
+#pragma nounroll
+    for (int m = m0; m < 32 * BI; m += BATCH * RPR) {
+      u32x4 v[BATCH];
+#pragma unroll
+      for (int r = 0; r < BATCH; ++r)
+        v[r] = *reinterpret_cast<const u32x4*>(tile + (m + r * RPR) * (16 * P) + slot(m + r * RPR, p) * 16);
+#pragma unroll
+      for (int r = 0; r < BATCH; ++r)
+        if (m + r * RPR < left && whole == PE)
+          reinterpret_cast<Out16*>(base + (m + r * RPR) * pitch + p * 16)->v = v[r];
+    }
+    if (whole > 0 && whole < PE) {  // the rows' last elements, one by one
+#pragma nounroll
+      for (int m = m0; m < left; m += RPR) {
+        const uint8_t* const src = tile + m * (16 * P) + slot(m, p) * 16;
+        uint8_t* const dst = base + m * pitch + p * 16;
+#pragma nounroll
+        for (int t = 0; t < whole; ++t) {
+          if constexpr (EB == 2)
+            reinterpret_cast<uint16_t*>(dst)[t] = reinterpret_cast<const uint16_t*>(src)[t];
+          else
+            reinterpret_cast<uint32_t*>(dst)[t] = reinterpret_cast<const uint32_t*>(src)[t];
+        }
+      }
+    }
+    __builtin_amdgcn_s_waitcnt(0xC07F);
+    __builtin_amdgcn_wave_barrier();
+  };
+  // fp32 goes in two halves of the columns; row blocks at a time, as many as the wave's room holds
+  constexpr int BJ4 = NJ > 1 ? NJ / 2 : 1;
+  constexpr int F2 = ROOM / (64 * 32 * NJ), F4 = ROOM / (128 * 32 * BJ4);
+  constexpr int B2 = F2 >= WM ? WM : F2 >= 2 ? 2 : 1, B4 = F4 >= WM ? WM : F4 >= 2 ? 2 : 1;
+  auto flush_rows = [&](auto eb, auto per, auto jfirst, auto jcount) __attribute__((always_inline)) {
+    constexpr int B = decltype(per)::value;
+    flush(eb, c0, per, jfirst, jcount);
+    if constexpr (WM > B) flush(eb, std::integral_constant<int, B>{}, per, jfirst, jcount);
+    if constexpr (WM > 2 * B) flush(eb, std::integral_constant<int, 2 * B>{}, per, jfirst, jcount);
+    if constexpr (WM > 3 * B) flush(eb, std::integral_constant<int, 3 * B>{}, per, jfirst, jcount);
+  };
+  constexpr std::integral_constant<int, 4> c4{};
+  constexpr std::integral_constant<int, BJ4> half4{};
+  if (MODE == MODE_GATEUP || !a.out_f32) {
+    flush_rows(c2, std::integral_constant<int, B2>{}, c0, std::integral_constant<int, NJ>{});
+  } else {
+    flush_rows(c4, std::integral_constant<int, B4>{}, c0, half4);
+    if constexpr (NJ > 1) flush_rows(c4, std::integral_constant<int, B4>{}, half4, half4);
+  }
+}
+
+// The tile of workgroup wg among `row_tiles` x `col_tiles`, in an order for the 8 XCDs (workgroup w
+// runs on XCD w % 8, each with an L2 of its own): an XCD takes a contiguous eighth of the list
+// [groups of 4 row tiles][column tiles][row tiles of the group], so the tiles that it computes at a
+// time share 4 row tiles' activations and a few column tiles' weights.  false: no tile.
+__device__ __forceinline__ bool xcd_tile(int64_t wg, int64_t row_tiles, int64_t col_tiles, int64_t& r, int64_t& c) {
+  const uint32_t total = (uint32_t)(row_tiles * col_tiles), share = (total + 7) / 8;  // a grid: below 2^31
+  const uint32_t t = ((uint32_t)wg & 7) * share + ((uint32_t)wg >> 3);
+  if (((uint32_t)wg >> 3) >= share || t >= total) return false;
+  const uint32_t group = t / (4 * (uint32_t)col_tiles), in = t % (4 * (uint32_t)col_tiles);
+  const uint32_t left = (uint32_t)row_tiles - 4 * group, here = left < 4 ? left : 4;
+  c = in / here;
+  r = 4 * group + in % here;
+  return true;
+}
+
+// The rows of row tile `tile` of an MoE product: every expert's rows in tiles of `size`, experts in
+// order.  Every wave finds it by itself.  Returns the number of row tiles where tile < 0.
+__device__ __forceinline__ int64_t expert_tile(const int32_t* offsets, int32_t experts, int size, int64_t tile,
+                                               int64_t& e, int64_t& row0, int64_t& rows) {
+  const int lane = threadIdx.x & 63;
+  int64_t before = 0;
+  for (int32_t eb = 0; eb < experts; eb += 64) {
+    const int32_t ex = eb + lane;
+    const int32_t from = ex < experts ? offsets[ex] : 0;
+    const int32_t count = ex < experts ? offsets[ex + 1] - from : 0;
+    const int32_t nt = count > 0 ? (count + size - 1) / size : 0;
+    int32_t incl = nt;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int32_t v = __shfl_up(incl, d);
+      if (lane >= d) incl += v;
+    }
+    const int64_t all = __builtin_amdgcn_readlane(incl, 63);
+    if (tile >= before && tile < before + all) {
+      const int64_t want = tile - before;
+      const uint64_t hit = __ballot(want >= incl - nt && want < incl);
+      const int src = __ffsll((unsigned long long)hit) - 1;
+      const int at = __builtin_amdgcn_readfirstlane(src);
+      const int32_t k = (int32_t)want - __builtin_amdgcn_readlane(incl - nt, at);
+      e = eb + at;
+      row0 = __builtin_amdgcn_readlane(from, at) + k * size;
+      const int32_t left = __builtin_amdgcn_readlane(count, at) - k * size;
+      rows = left < size ? left : size;
+      return 0;
+    }
+    before += all;
+  }
+  return __builtin_amdgcn_readfirstlane((int)before);
+}
+
+// WM: the largest tile's; a tile with few rows left takes a smaller one.
+template <int MODE, int WM, int WN, int BUFS>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(BUFS == 1 ? 2 : 1, BUFS == 1 ? 2 : WM * WN >= 8 ? 1 : 2)))
+void mx_tiled_kernel(const MxArgs a, int32_t experts) {
+  constexpr int XR = 64 * WM, WR = 64 * WN;
+  __shared__ __attribute__((aligned(16))) uint8_t codes0[(BUFS == 1 ? XR + WR : XR) * kStageBytes];
+  __shared__ __attribute__((aligned(16))) uint8_t x1[BUFS == 1 ? 16 : XR * kStageBytes];
+  __shared__ __attribute__((aligned(16))) uint8_t w0[BUFS == 1 ? 16 : WR * kStageBytes];
+  __shared__ __attribute__((aligned(16))) uint8_t w1[BUFS == 1 ? 16 : WR * kStageBytes];
+  __shared__ __attribute__((aligned(16))) uint8_t s0[(XR + WR) * 8];
+  __shared__ __attribute__((aligned(16))) uint8_t s1[BUFS == 1 ? 16 : (XR + WR) * 8];
+  constexpr int ROOM = BUFS == 1 ? (XR + WR) * kStageBytes / 4 : (XR < WR ? XR : WR) * kStageBytes;
+  const TileLds lds{{codes0, x1}, {BUFS == 1 ? codes0 + XR * kStageBytes : w0, w1}, {s0, s1}};
+  constexpr int64_t cols = MODE == MODE_GATEUP ? 32 * WN : 64 * WN;
+  const int64_t col_tiles = (a.N + cols - 1) / cols;
+  int64_t r, c, e = 0, row0, rows;
+  if constexpr (MODE == MODE_DENSE) {
+    if (!xcd_tile(blockIdx.x, (a.M + XR - 1) / XR, col_tiles, r, c)) return;
+    row0 = r * XR;
+    rows = a.M - row0 < XR ? a.M - row0 : XR;
+  } else {
+    const int64_t row_tiles = expert_tile(a.offsets, experts, XR, -1, e, row0, rows);
+    if (!xcd_tile(blockIdx.x, row_tiles, col_tiles, r, c)) return;
+    expert_tile(a.offsets, experts, XR, r, e, row0, rows);
+  }
+  if constexpr (WM == 4) {
+    if (rows > 128) mx_tile<MODE, 4, WN, BUFS, ROOM>(a, lds, e, row0, rows, c);
+    else if (rows > 64) mx_tile<MODE, 2, WN, BUFS, ROOM>(a, lds, e, row0, rows, c);
+    else mx_tile<MODE, 1, WN, BUFS, ROOM>(a, lds, e, row0, rows, c);
+  } else if constexpr (WM == 2) {
+    if (rows > 64) mx_tile<MODE, 2, WN, BUFS, ROOM>(a, lds, e, row0, rows, c);
+    else mx_tile<MODE, 1, WN, BUFS, ROOM>(a, lds, e, row0, rows, c);
+  } else {
+    mx_tile<MODE, 1, WN, BUFS, ROOM>(a, lds, e, row0, rows, c);
+  }
+}
+
+template <int MODE, int WM, int WN, int BUFS>
+hipError_t launch_tiles(const MxArgs& a, int64_t experts, hipStream_t s) {
+  constexpr int64_t cols = MODE == MODE_GATEUP ? 32 * WN : 64 * WN;
+  constexpr int64_t size = 64 * WM;
+  // an expert's last tile may be partial: at most one more row tile per expert
+  const int64_t row_tiles = (a.M + size - 1) / size + (MODE == MODE_DENSE ? 0 : experts);
+  const int64_t wgs = (row_tiles * ((a.N + cols - 1) / cols) + 7) / 8 * 8;
+  if (wgs > 0x7FFFFFFF) return hipErrorInvalidValue;
+  hipLaunchKernelGGL((mx_tiled_kernel<MODE, WM, WN, BUFS>), dim3((unsigned)wgs), dim3(256), 0, s, a, (int32_t)experts);
+  return hipGetLastError();
+}
+
 }  // namespace
 
 hipError_t launch_mx_quantize(const void* x, int f32, int64_t n, int64_t k, uint8_t* codes,
@@ -240,22 +850,81 @@ hipError_t launch_mx_quantize(const void* x, int f32, int64_t n, int64_t k, uint
   return hipGetLastError();
 }
 
-hipError_t launch_mx_product(int mode, const MxArgs& a, int64_t experts, hipStream_t stream) {
-  if (mode == MODE_GATEUP) return launch_stream<MODE_GATEUP, 1, 4>(a, experts, 1, stream);
-  if (mode == MODE_DOWN) return launch_stream<MODE_DOWN, 1, 4>(a, experts, 1, stream);
-  // the grid's z extent is 16 bits: more rows take further launches
-  constexpr int64_t chunk = 65535ll * 32;
+namespace {
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Dense products: rows in passes of 16 MT; the grid's z extent is 16 bits, so more rows take further
+// launches.
+template <int MT>
+hipError_t stream_dense(const MxArgs& a, hipStream_t stream) {
+  constexpr int64_t chunk = 65535ll * 16 * MT;
   for (int64_t r0 = 0; r0 < a.M; r0 += chunk) {
     MxArgs b = a;
     b.x_codes = a.x_codes + r0 * (a.K / 2);
     b.x_scales = a.x_scales + r0 * (a.K / 32);
     b.out = static_cast<uint8_t*>(a.out) + r0 * a.out_stride * (a.out_f32 ? 4 : 2);
     b.M = a.M - r0 < chunk ? a.M - r0 : chunk;
-    const hipError_t e = b.M <= 16 ? launch_stream<MODE_DENSE, 1, 4>(b, 1, 1, stream)
-                                   : launch_stream<MODE_DENSE, 2, 4>(b, 1, (b.M + 31) / 32, stream);
+    const hipError_t e = launch_stream<MODE_DENSE, MT, 4>(b, 1, ceil_div(b.M, 16 * MT), stream);
     if (e != hipSuccess) return e;
   }
   return hipSuccess;
+}
+
+// The tiles' 32-bit ranges: one expert's codes, a tile's rows (k below 2^23) and, gathered, all tokens'
+// codes, each below 2^31 less a stage's bytes.  A stage needs 256 columns.
+bool tiles_fit(int mode, const MxArgs& a) {
+  constexpr int64_t most = (1ll << 31) - 1024;
+  if (a.K < 256 || a.K >= (1ll << 23) || a.N * (a.K / 2) > most) return false;
+  return mode != MODE_GATEUP || a.M / a.topk * (a.K / 2) <= most;
+}
+
+// Which kernel, by what was measured on both sides of each border (us, in a graph):
+//   256 x 256 tiles, one workgroup per CU, for long k; 128 x 256 with one buffer, two per CU, whose
+//   neighbour covers a tile's start and end, for short k:
+//     4096 x 8192, k 8192: 145 and 170;  8192 x 8192, k 1024: 77 and 58
+//   128 x 128 where 128 x 256 would leave CUs without a tile: 3000 x 2048, k 1024: 10.5 and 11.7
+//   64 x 64 where 128 x 128 would: 128 x 4096, k 4096: 10.4 and 13.8
+//   streaming where few workgroups of 32 x 16 suffice: 48 x 4096, k 4096: 8.9 against 10
+hipError_t product_dense(const MxArgs& a, hipStream_t stream) {
+  const auto tiles = [&](int64_t bm, int64_t bn) { return ceil_div(a.M, bm) * ceil_div(a.N, bn); };
+  if (a.M > 32 && tiles_fit(MODE_DENSE, a)) {
+    if (tiles(256, 256) >= 192 && a.K >= 4096) return launch_tiles<MODE_DENSE, 4, 4, 2>(a, 1, stream);
+    if (tiles(128, 256) >= 256) return launch_tiles<MODE_DENSE, 2, 4, 1>(a, 1, stream);
+    if (tiles(128, 128) >= 128) return launch_tiles<MODE_DENSE, 2, 2, 2>(a, 1, stream);
+    if (tiles(32, 16) >= 850) return launch_tiles<MODE_DENSE, 1, 1, 2>(a, 1, stream);
+  }
+  // 16 rows a workgroup where 32 would leave CUs without one: 64 x 1024, k 8192: 7.3 against 9.8
+  return a.M > 16 && tiles(32, 16) >= 256 ? stream_dense<2>(a, stream) : stream_dense<1>(a, stream);
+}
+
+// The same for experts, by the rows that an expert has on average (gate+up / down, 64 experts,
+// hidden 8192, inter 3584 unless said otherwise):
+//   streaming for few: 2 rows: 319 / 181 against 363 / 188 in tiles; 4 rows: 368 / 217 against
+//   339 / 195; with few tiles for more rows: 8 experts, 1024 x 1024, 16 rows: 4.6 against 5.9
+//   128 x 256 tiles (64 rows where an expert has no more) up to 128 rows: 64 rows: 490 against 503
+//   256 x 256 for long k: 512 rows: 1311 against 1545;  128 x 256 with one buffer for short k (16
+//   experts, 250 rows, 1000 x 2048: 23.2 against 27.1 with two)
+template <int MODE>
+hipError_t product_experts(const MxArgs& a, int64_t experts, hipStream_t stream) {
+  const int64_t active = a.M < experts ? a.M : experts;  // at most
+  const double rows = (double)a.M / (double)experts;
+  const int64_t cols = ceil_div(MODE == MODE_GATEUP ? 2 * a.N : a.N, 256);
+  if (!tiles_fit(MODE, a) || rows < 3.0) return launch_stream<MODE, 1, 4>(a, experts, 1, stream);
+  if ((a.M / 128 + active) * cols < 128)
+    return rows <= 32.0 ? launch_stream<MODE, 1, 4>(a, experts, 1, stream)
+                        : launch_tiles<MODE, 2, 2, 2>(a, experts, stream);
+  if (rows < 128.0) return launch_tiles<MODE, 2, 4, 2>(a, experts, stream);
+  if (a.K < 4096 || (a.M / 256 + active) * cols < 512) return launch_tiles<MODE, 2, 4, 1>(a, experts, stream);
+  return launch_tiles<MODE, 4, 4, 2>(a, experts, stream);
+}
+
+}  // namespace
+
+hipError_t launch_mx_product(int mode, const MxArgs& a, int64_t experts, hipStream_t stream) {
+  if (mode == MODE_GATEUP) return product_experts<MODE_GATEUP>(a, experts, stream);
+  if (mode == MODE_DOWN) return product_experts<MODE_DOWN>(a, experts, stream);
+  return product_dense(a, stream);
 }
 
 }  // namespace wq
