@@ -312,8 +312,7 @@ struct __attribute__((packed, aligned(2))) Out16 {
 };
 
 // Rows row0 .. row0 + rows - 1 (at most 64 WM) of expert e, columns of tile ctile.
-// ROOM: bytes of LDS that the epilogue has for each wave.
-template <int MODE, int WM, int WN, int BUFS, int ROOM>
+template <int MODE, int WM, int WN, int BUFS>
 __device__ __forceinline__ void mx_tile(const MxArgs& a, const TileLds& lds, int64_t e, int64_t row0,
                                         int64_t rows, int64_t ctile) {
   constexpr int XR = 64 * WM, WR = 64 * WN;                   // rows of a stage
@@ -631,108 +630,65 @@ __device__ __forceinline__ void mx_tile(const MxArgs& a, const TileLds& lds, int
   } else {
     for (; g < steps; ++g) stage1(g);
   }
-  __syncthreads();
 
   // ---- epilogue: lane (l, h) holds, of each block, row l and columns 8 q + 4 h + t (register
-  // 4 q + t).  Each wave passes its blocks through an LDS array of its own, so that rows leave in
-  // 16-byte pieces; piece p of row m lies in slot p ^ (m / rows per 256 bytes), free of conflicts.
-  // ----
-  // Two buffers: one array per wave.  One buffer: a quarter of its arrays each.
-  uint8_t* const tile = BUFS == 2 ? (wave == 0 ? lds.x[0] : wave == 1 ? lds.x[1] : wave == 2 ? lds.w[0] : lds.w[1])
-                                  : lds.x[0] + wave * ROOM;
+  // 4 q + t).  bf16: after packing, v_permlane32_swap gives the lower lanes the eight columns of an
+  // even q and the upper ones those of the odd q behind it, so both types leave in 16-byte pieces,
+  // 32 bytes of a row together, straight from registers. ----
   auto value = [&](int i, int j, int r) __attribute__((always_inline)) {
     if constexpr (MODE == MODE_GATEUP) return silu_f32(acc[i][j][r]) * acc[i][NJ + j][r];
     else return acc[i][j][r];
   };
-  const int mw = 32 * WM * wx;  // the wave's first row of the tile
-  // BI blocks of rows at a time by BJ of columns: [32 BI rows][32 BJ columns] of EB bytes
-  auto flush = [&](auto eb, auto first, auto count, auto jfirst, auto jcount) __attribute__((always_inline)) {
-    constexpr int EB = decltype(eb)::value, I0 = decltype(first)::value, BI = decltype(count)::value;
-    constexpr int J0 = decltype(jfirst)::value, BJ = decltype(jcount)::value;
-    constexpr int P = 32 * BJ * EB / 16;  // pieces per row
-    static_assert(32 * BI * 16 * P <= ROOM, "the blocks fit");
-    const int64_t nw = n0 + 32 * (NJ * ww + J0);  // the wave's first column
-    constexpr int PE = 16 / EB;
-    auto slot = [](int m, int p) __attribute__((always_inline)) {
-      return P >= 16 ? p ^ (m & 15) : p ^ ((m / (16 / P)) & (P - 1));
-    };
-#pragma unroll
-    for (int i = 0; i < BI; ++i) {
-      const int m = 32 * i + l32;
-#pragma unroll
-      for (int j = 0; j < BJ; ++j)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          float v[4];
-#pragma unroll
-          for (int t = 0; t < 4; ++t) v[t] = value(I0 + i, J0 + j, 4 * q + t);
-          if constexpr (EB == 2) {
-            *reinterpret_cast<u32x2*>(tile + m * (16 * P) + slot(m, 4 * j + q) * 16 + 8 * h) =
-                (u32x2){cvt_pk_bf16(v[0], v[1]), cvt_pk_bf16(v[2], v[3])};
-          } else {
-            *reinterpret_cast<f32x4*>(tile + m * (16 * P) + slot(m, 8 * j + 2 * q + h) * 16) =
-                (f32x4){v[0], v[1], v[2], v[3]};
-          }
-        }
-    }
-    // only this wave reads what it wrote: its own reads follow its writes
-    __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
-    __builtin_amdgcn_wave_barrier();
-    const int left = (int)(rows - mw - 32 * I0 < 32 * BI ? rows - mw - 32 * I0 : 32 * BI);
-    uint8_t* const base = static_cast<uint8_t*>(a.out) + ((row0 + mw + 32 * I0) * a.out_stride + nw) * EB;
+  const int64_t nw = n0 + 32 * NJ * ww;  // the wave's first column
+  const int mw = 32 * WM * wx;           // and row of the tile
+  auto store = [&](auto eb) __attribute__((always_inline)) {
+    constexpr int EB = decltype(eb)::value, PE = 16 / EB;  // elements of a piece
+    constexpr int NP = 16 / PE;                            // pieces of a lane's row in a block
     const int64_t pitch = a.out_stride * EB;
-    // pieces of whole rows: lane's piece is the same in every round when 64 lanes cover whole rows
-    const int p = lane % P;
-    const int whole = (int)(N - nw >= 32 * BJ ? PE : N - nw - p * PE >= PE ? PE : N - nw - p * PE);  // its elements
-    constexpr int RPR = 64 / P, ROUNDS = 32 * BI / RPR, BATCH = ROUNDS < 4 ? ROUNDS : 4;  // rows a round
-    const int m0 = lane / P;
-#pragma nounroll
-    for (int m = m0; m < 32 * BI; m += BATCH * RPR) {
-      u32x4 v[BATCH];
+    const int32_t cols = (int32_t)(N - nw < 32 * NJ ? N - nw : 32 * NJ) - PE * h;  // from the lane's first
+    const uint32_t lane_off = (uint32_t)(l32 * pitch) + 16 * h;
 #pragma unroll
-      for (int r = 0; r < BATCH; ++r)
-        v[r] = *reinterpret_cast<const u32x4*>(tile + (m + r * RPR) * (16 * P) + slot(m + r * RPR, p) * 16);
+    for (int i = 0; i < WM; ++i) {
+      uint8_t* const base = static_cast<uint8_t*>(a.out) + ((row0 + mw + 32 * i) * a.out_stride + nw) * EB;
+      const bool row = mw + 32 * i + l32 < rows;
+      u32x4 last{};  // the piece that N cuts
 #pragma unroll
-      for (int r = 0; r < BATCH; ++r)
-        if (m + r * RPR < left && whole == PE)
-          reinterpret_cast<Out16*>(base + (m + r * RPR) * pitch + p * 16)->v = v[r];
-    }
-    if (whole > 0 && whole < PE) {  // the rows' last elements, one by one
-#pragma nounroll
-      for (int m = m0; m < left; m += RPR) {
-        const uint8_t* const src = tile + m * (16 * P) + slot(m, p) * 16;
-        uint8_t* const dst = base + m * pitch + p * 16;
-#pragma nounroll
-        for (int t = 0; t < whole; ++t) {
-          if constexpr (EB == 2)
-            reinterpret_cast<uint16_t*>(dst)[t] = reinterpret_cast<const uint16_t*>(src)[t];
-          else
-            reinterpret_cast<uint32_t*>(dst)[t] = reinterpret_cast<const uint32_t*>(src)[t];
+      for (int j = 0; j < NJ; ++j)
+#pragma unroll
+        for (int p = 0; p < NP; ++p) {
+          u32x4 v;
+          if constexpr (EB == 2) {
+            uint32_t e[2], o[2];
+#pragma unroll
+            for (int d = 0; d < 2; ++d) {
+              e[d] = cvt_pk_bf16(value(i, j, 8 * p + 2 * d), value(i, j, 8 * p + 2 * d + 1));
+              o[d] = cvt_pk_bf16(value(i, j, 8 * p + 4 + 2 * d), value(i, j, 8 * p + 5 + 2 * d));
+            }
+            const auto r0 = __builtin_amdgcn_permlane32_swap(e[0], o[0], false, false);
+            const auto r1 = __builtin_amdgcn_permlane32_swap(e[1], o[1], false, false);
+            v = (u32x4){r0[0], r1[0], r0[1], r1[1]};
+          } else {
+#pragma unroll
+            for (int d = 0; d < 4; ++d) v[d] = __float_as_uint(value(i, j, 4 * p + d));
+          }
+          const int at = 32 * j + 2 * PE * p;  // first column, from the lane's
+          if (row && at + PE <= cols) reinterpret_cast<Out16*>(base + lane_off + at * EB)->v = v;
+          if (at < cols) last = v;
         }
+      const int cut = cols > 0 ? cols % (2 * PE) : 0;  // elements of the cut piece, if below PE
+      if (row && cut > 0 && cut < PE) {
+#pragma unroll
+        for (int t = 0; t < PE - 1; ++t)
+          if (t < cut) {
+            uint8_t* const dst = base + lane_off + (cols - cut + t) * EB;
+            if constexpr (EB == 2) *reinterpret_cast<uint16_t*>(dst) = (uint16_t)(last[t / 2] >> (16 * (t & 1)));
+            else *reinterpret_cast<uint32_t*>(dst) = last[t];
+          }
       }
     }
-    __builtin_amdgcn_s_waitcnt(0xC07F);
-    __builtin_amdgcn_wave_barrier();
   };
-  // fp32 goes in two halves of the columns; row blocks at a time, as many as the wave's room holds
-  constexpr int BJ4 = NJ > 1 ? NJ / 2 : 1;
-  constexpr int F2 = ROOM / (64 * 32 * NJ), F4 = ROOM / (128 * 32 * BJ4);
-  constexpr int B2 = F2 >= WM ? WM : F2 >= 2 ? 2 : 1, B4 = F4 >= WM ? WM : F4 >= 2 ? 2 : 1;
-  auto flush_rows = [&](auto eb, auto per, auto jfirst, auto jcount) __attribute__((always_inline)) {
-    constexpr int B = decltype(per)::value;
-    flush(eb, c0, per, jfirst, jcount);
-    if constexpr (WM > B) flush(eb, std::integral_constant<int, B>{}, per, jfirst, jcount);
-    if constexpr (WM > 2 * B) flush(eb, std::integral_constant<int, 2 * B>{}, per, jfirst, jcount);
-    if constexpr (WM > 3 * B) flush(eb, std::integral_constant<int, 3 * B>{}, per, jfirst, jcount);
-  };
-  constexpr std::integral_constant<int, 4> c4{};
-  constexpr std::integral_constant<int, BJ4> half4{};
-  if (MODE == MODE_GATEUP || !a.out_f32) {
-    flush_rows(c2, std::integral_constant<int, B2>{}, c0, std::integral_constant<int, NJ>{});
-  } else {
-    flush_rows(c4, std::integral_constant<int, B4>{}, c0, half4);
-    if constexpr (NJ > 1) flush_rows(c4, std::integral_constant<int, B4>{}, half4, half4);
-  }
+  if (MODE == MODE_GATEUP || !a.out_f32) store(c2);
+  else store(std::integral_constant<int, 4>{});
 }
 
 // The tile of workgroup wg among `row_tiles` x `col_tiles`, in an order for the 8 XCDs (workgroup w
@@ -796,7 +752,6 @@ void mx_tiled_kernel(const MxArgs a, int32_t experts) {
   __shared__ __attribute__((aligned(16))) uint8_t w1[BUFS == 1 ? 16 : WR * kStageBytes];
   __shared__ __attribute__((aligned(16))) uint8_t s0[(XR + WR) * 8];
   __shared__ __attribute__((aligned(16))) uint8_t s1[BUFS == 1 ? 16 : (XR + WR) * 8];
-  constexpr int ROOM = BUFS == 1 ? (XR + WR) * kStageBytes / 4 : (XR < WR ? XR : WR) * kStageBytes;
   const TileLds lds{{codes0, x1}, {BUFS == 1 ? codes0 + XR * kStageBytes : w0, w1}, {s0, s1}};
   constexpr int64_t cols = MODE == MODE_GATEUP ? 32 * WN : 64 * WN;
   const int64_t col_tiles = (a.N + cols - 1) / cols;
@@ -811,14 +766,14 @@ void mx_tiled_kernel(const MxArgs a, int32_t experts) {
     expert_tile(a.offsets, experts, XR, r, e, row0, rows);
   }
   if constexpr (WM == 4) {
-    if (rows > 128) mx_tile<MODE, 4, WN, BUFS, ROOM>(a, lds, e, row0, rows, c);
-    else if (rows > 64) mx_tile<MODE, 2, WN, BUFS, ROOM>(a, lds, e, row0, rows, c);
-    else mx_tile<MODE, 1, WN, BUFS, ROOM>(a, lds, e, row0, rows, c);
+    if (rows > 128) mx_tile<MODE, 4, WN, BUFS>(a, lds, e, row0, rows, c);
+    else if (rows > 64) mx_tile<MODE, 2, WN, BUFS>(a, lds, e, row0, rows, c);
+    else mx_tile<MODE, 1, WN, BUFS>(a, lds, e, row0, rows, c);
   } else if constexpr (WM == 2) {
-    if (rows > 64) mx_tile<MODE, 2, WN, BUFS, ROOM>(a, lds, e, row0, rows, c);
-    else mx_tile<MODE, 1, WN, BUFS, ROOM>(a, lds, e, row0, rows, c);
+    if (rows > 64) mx_tile<MODE, 2, WN, BUFS>(a, lds, e, row0, rows, c);
+    else mx_tile<MODE, 1, WN, BUFS>(a, lds, e, row0, rows, c);
   } else {
-    mx_tile<MODE, 1, WN, BUFS, ROOM>(a, lds, e, row0, rows, c);
+    mx_tile<MODE, 1, WN, BUFS>(a, lds, e, row0, rows, c);
   }
 }
 
