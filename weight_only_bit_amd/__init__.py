@@ -124,15 +124,31 @@ def _check(st: int, what: str):
     raise WqError(msg)
 
 
-def _stream():
-    """The current device's current stream, as an address.  torch.cuda.current_stream() builds a
-    Stream object around the same number, 2.6 us a call; the number alone takes 0.2."""
-    import torch
+# The current device's number and its current stream's address.  torch.cuda.current_stream() builds
+# a Stream object around the same address, 2.6 us a call, and torch.cuda.current_device() takes 0.2;
+# a call below asks several times, and what it launches may take 3.
+_torch_calls = None
 
-    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    if raw is not None:
-        return raw(torch.cuda.current_device())
-    return torch.cuda.current_stream().cuda_stream
+
+def _torch_fast():
+    global _torch_calls
+    if _torch_calls is None:
+        import torch
+
+        device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+        stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda index: torch.cuda.current_stream(index).cuda_stream)
+        _torch_calls = (device, stream)
+    return _torch_calls
+
+
+def _current_device() -> int:
+    return (_torch_calls or _torch_fast())[0]()
+
+
+def _stream() -> int:
+    device, stream = _torch_calls or _torch_fast()
+    return stream(device())
 
 
 def _ptr(t):
@@ -166,14 +182,13 @@ def _need(t, name, kind, shape=None, numel=None):
         raise TypeError(f"{name}: expected a torch tensor, got {type(t).__name__}")
     if not t.is_cuda:
         raise ValueError(f"{name}: must be a GPU tensor, got {t.device}")
-    if t.get_device() != torch.cuda.current_device():
-        raise ValueError(f"{name}: must be on the current GPU (cuda:{torch.cuda.current_device()}), "
-                         f"got {t.device}")
-    if t.dtype not in _dtypes()[kind]:
+    if t.get_device() != _current_device():
+        raise ValueError(f"{name}: must be on the current GPU (cuda:{_current_device()}), got {t.device}")
+    if t.dtype not in (_kinds or _dtypes())[kind]:
         raise TypeError(f"{name}: dtype {t.dtype} is not {kind} ({_dtypes()[kind]})")
     if not t.is_contiguous():
         raise ValueError(f"{name}: must be contiguous")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape and tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name}: shape {tuple(t.shape)} != {tuple(shape)}")
     if numel is not None and t.numel() != numel:
         raise ValueError(f"{name}: {t.numel()} elements, the layout needs {numel}")
@@ -235,7 +250,7 @@ class PackedWeight:
                 raise ValueError(f"PackedWeight.{name}: required by format {self.format}")
             if not isinstance(t, torch.Tensor) or not t.is_cuda:
                 raise ValueError(f"PackedWeight.{name}: must be a GPU tensor")
-            if t.get_device() != torch.cuda.current_device():
+            if t.get_device() != _current_device():
                 raise ValueError(f"PackedWeight.{name}: must be on the current GPU")
             if not t.is_contiguous():
                 raise ValueError(f"PackedWeight.{name}: must be contiguous")
@@ -488,8 +503,8 @@ def wq_quantize_mx(x) -> PackedWeight:
     if k <= 0 or k % 64:
         raise ValueError(f"wq_quantize_mx: k = {k} is not a positive multiple of 64")
     x = _need(x.contiguous(), "wq_quantize_mx x", kind)
-    codes = torch.empty((E, n, k // 2), dtype=torch.uint8, device=x.device)
-    scales = torch.empty((E, n, k // 32), dtype=torch.uint8, device=x.device)
+    codes = x.new_empty((E, n, k // 2), dtype=torch.uint8)
+    scales = x.new_empty((E, n, k // 32), dtype=torch.uint8)
     _check(lib().wq_quantize_mx(_ptr(x), vt, E * n, k, _ptr(codes), _ptr(scales), _stream()),
            "wq_quantize_mx")
     return PackedWeight(FMT_MXFP4, n, k, E, 32, codes=codes, qscale=scales)
@@ -517,7 +532,7 @@ def wq_gemm_mx(x, w: PackedWeight, y=None, dtype=None):
 
     _mx_rows(x, "wq_gemm_mx x", k=w.k)
     if y is None:
-        y = torch.empty((x.n, w.n), dtype=dtype or torch.bfloat16, device=x.codes.device)
+        y = x.codes.new_empty((x.n, w.n), dtype=dtype or torch.bfloat16)
     vt, kind = _value_type(y, "wq_gemm_mx y")
     _need(y, "wq_gemm_mx y", kind, shape=(x.n, w.n))
     _check(lib().wq_gemm_mx(_ptr(x.codes), _ptr(x.qscale), x.n, ctypes.byref(w.cstruct()), _ptr(y), vt,
@@ -535,7 +550,7 @@ def wq_moe_gate_up_mx(x, offsets, sorted_pairs, topk: int, gate: PackedWeight, u
     _need(offsets, "wq_moe_gate_up_mx offsets", "i32", numel=gate.experts + 1)
     _need(sorted_pairs, "wq_moe_gate_up_mx sorted_pairs", "i32", numel=t * topk)
     if h is None:
-        h = torch.empty((t * topk, gate.n), dtype=torch.bfloat16, device=x.codes.device)
+        h = x.codes.new_empty((t * topk, gate.n), dtype=torch.bfloat16)
     _need(h, "wq_moe_gate_up_mx h", "bf16", shape=(t * topk, gate.n))
     _check(lib().wq_moe_gate_up_mx(_ptr(x.codes), _ptr(x.qscale), t, _ptr(offsets), _ptr(sorted_pairs),
                                    topk, ctypes.byref(gate.cstruct()), ctypes.byref(up.cstruct()),
@@ -551,7 +566,7 @@ def wq_moe_down_mx(h, offsets, down: PackedWeight, d=None, dtype=None):
     _mx_rows(h, "wq_moe_down_mx h", k=down.k)
     _need(offsets, "wq_moe_down_mx offsets", "i32", numel=down.experts + 1)
     if d is None:
-        d = torch.empty((h.n, down.n), dtype=dtype or torch.bfloat16, device=h.codes.device)
+        d = h.codes.new_empty((h.n, down.n), dtype=dtype or torch.bfloat16)
     vt, kind = _value_type(d, "wq_moe_down_mx d")
     _need(d, "wq_moe_down_mx d", kind, shape=(h.n, down.n))
     _check(lib().wq_moe_down_mx(_ptr(h.codes), _ptr(h.qscale), h.n, _ptr(offsets),
@@ -566,8 +581,6 @@ def wq_moe_down_mx(h, offsets, down: PackedWeight, d=None, dtype=None):
 def wq_moe_positions(topk_ids, offsets, sorted_pairs, positions=None):
     """positions int32 [t, topk]: the row of every (token, slot) pair in expert order, -1 for a pair
     whose id is no expert's; offsets and sorted_pairs as wq_moe_route gave them for topk_ids."""
-    import torch
-
     if topk_ids.dim() != 2:
         raise ValueError("wq_moe_positions: topk_ids must be [t, topk]")
     t, topk = topk_ids.shape
@@ -575,7 +588,7 @@ def wq_moe_positions(topk_ids, offsets, sorted_pairs, positions=None):
     _need(offsets, "wq_moe_positions offsets", "i32")
     _need(sorted_pairs, "wq_moe_positions sorted_pairs", "i32", numel=t * topk)
     if positions is None:
-        positions = torch.empty((t, topk), dtype=torch.int32, device=topk_ids.device)
+        positions = topk_ids.new_empty((t, topk))
     _need(positions, "wq_moe_positions positions", "i32", shape=(t, topk))
     _check(lib().wq_moe_positions(_ptr(topk_ids), t, topk, offsets.numel() - 1, _ptr(offsets),
                                   _ptr(sorted_pairs), _ptr(positions), _stream()), "wq_moe_positions")
@@ -592,8 +605,6 @@ def _positions(positions, what):
 def wq_moe_permute(x, positions, rows=None):
     """rows [t*topk, hidden] in expert order: rows[positions[t, j]] = x[t] (bf16 or fp32).  Its
     gradient is wq_moe_unpermute(d_rows, positions)."""
-    import torch
-
     t, topk = _positions(positions, "wq_moe_permute")
     vt, kind = _value_type(x, "wq_moe_permute x")
     if x.dim() != 2:
@@ -601,7 +612,7 @@ def wq_moe_permute(x, positions, rows=None):
     hidden = x.shape[1]
     _need(x, "wq_moe_permute x", kind, shape=(t, hidden))
     if rows is None:
-        rows = torch.empty((t * topk, hidden), dtype=x.dtype, device=x.device)
+        rows = x.new_empty((t * topk, hidden))
     _need(rows, "wq_moe_permute rows", kind, shape=(t * topk, hidden))
     _check(lib().wq_moe_permute(_ptr(x), vt, t, topk, hidden, _ptr(positions), _ptr(rows), _stream()),
            "wq_moe_permute")
@@ -610,8 +621,6 @@ def wq_moe_permute(x, positions, rows=None):
 
 def wq_moe_unpermute(rows, positions, topk_weights=None, y=None):
     """y [t, hidden] = sum_j topk_weights[t, j] * rows[positions[t, j]] (weights None: 1)."""
-    import torch
-
     t, topk = _positions(positions, "wq_moe_unpermute")
     vt, kind = _value_type(rows, "wq_moe_unpermute rows")
     if rows.dim() != 2:
@@ -621,7 +630,7 @@ def wq_moe_unpermute(rows, positions, topk_weights=None, y=None):
     if topk_weights is not None:
         _need(topk_weights, "wq_moe_unpermute topk_weights", "f32", shape=(t, topk))
     if y is None:
-        y = torch.empty((t, hidden), dtype=rows.dtype, device=rows.device)
+        y = rows.new_empty((t, hidden))
     _need(y, "wq_moe_unpermute y", kind, shape=(t, hidden))
     _check(lib().wq_moe_unpermute(_ptr(rows), vt, _ptr(positions), _ptr(topk_weights), t, topk, hidden,
                                   _ptr(y), _stream()), "wq_moe_unpermute")
@@ -642,12 +651,12 @@ def wq_moe_unpermute_grad(dy, rows, positions, topk_weights=None, d_rows=None, d
     if topk_weights is not None:
         _need(topk_weights, "wq_moe_unpermute_grad topk_weights", "f32", shape=(t, topk))
     if d_rows is None:
-        d_rows = torch.empty((t * topk, hidden), dtype=dy.dtype, device=dy.device)
+        d_rows = dy.new_empty((t * topk, hidden))
     _need(d_rows, "wq_moe_unpermute_grad d_rows", kind, shape=(t * topk, hidden))
     if rows is not None:
         _need(rows, "wq_moe_unpermute_grad rows", kind, shape=(t * topk, hidden))
         if d_weights is None:
-            d_weights = torch.empty((t, topk), dtype=torch.float32, device=dy.device)
+            d_weights = dy.new_empty((t, topk), dtype=torch.float32)
     if d_weights is not None:
         _need(d_weights, "wq_moe_unpermute_grad d_weights", "f32", shape=(t, topk))
     _check(lib().wq_moe_unpermute_grad(_ptr(dy), vt, _ptr(rows), _ptr(positions), _ptr(topk_weights), t,
