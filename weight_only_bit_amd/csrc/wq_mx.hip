@@ -260,13 +260,17 @@ hipError_t launch_stream(const MxArgs& a, int64_t gy, int64_t gz, hipStream_t s)
 //     and a block of 32: slice s of a stage takes block 4 h + s, so a lane's four blocks are 64
 //     contiguous bytes and their scales one dword, of which slice s reads byte s (the instruction's
 //     byte select).  Any order of the k sum is the same product.
-//   * Codes pass through registers to LDS (16 bytes per lane, 8 lanes per row), which holds two
-//     stages; the registers hold a third, on its way.  Rows are 128 bytes, 16-byte piece p of row r
-//     in slot p ^ (r / 2 % 8), which keeps the fragment reads free of bank conflicts.  (Copies to
-//     LDS without registers have to wait for the buffer that they fill, so that all of a stage's
-//     are issued at once and its MFMAs wait behind them: measured 1.75 us per stage of 256 CUs
-//     where the copies alone and the rest alone take 0.95 each.)  Thread t carries the scales of
-//     rows t the same way.
+//   * Rows of a stage are 128 bytes in LDS, 16-byte piece p of row r in slot p ^ (r / 2 % 8), which
+//     keeps the fragment reads free of bank conflicts; 8 lanes load a row.  Thread t carries the
+//     scales of rows t through registers (rows of scale bytes are only 2-byte aligned).
+//   * Two buffers, one workgroup per CU (256 x 256): codes pass through registers, which hold a third
+//     stage on its way, so loads and LDS writes spread over the whole stage.  (Copies without
+//     registers have to wait for the buffer that they fill, so all of a stage's are issued at once
+//     and the MFMAs wait behind them: 1.75 us per stage of 256 CUs where the copies alone and the
+//     rest alone take 0.95 each, with codes of zero; this way 1.2.)
+//   * One buffer, two workgroups per CU (128 x 256): the next stage is copied without registers while
+//     the other workgroup multiplies, which also covers a tile's first loads and its stores.  Through
+//     registers: 176 us where this takes 165 (4096 x 8192, k 8192).
 //   * The next slice's fragments are read under the current slice's MFMAs; the last slice of a
 //     stage is multiplied after the barrier that ends the stage, over the next stage's first reads.
 // Results of rows behind a ragged tile's end and of columns behind N are not stored.
@@ -369,49 +373,65 @@ __device__ __forceinline__ void mx_tile(const MxArgs& a, const TileLds& lds, int
   // 32 products of at most 36 is zero in fp32.
   const int32_t behind = (int64_t)last * kStageBytes + piece * 16 >= half ? kStageBytes : 0;
 
-  // A stage's codes pass through NC registers of 16 bytes per lane, in four groups: fetch loads
-  // group q of stage g, put writes it to the buffers.
+  // Load i of stage g: do_load(i, resource, lane offset).
   constexpr int NX = 2 * WM, NC = 2 * WM + 2 * WN;
-  u32x4 held[NC];
-  auto fetch_to = [&](u32x4(&to)[NC], int32_t g, auto qc) __attribute__((always_inline)) {
-    constexpr int Q = decltype(qc)::value;
+  auto load_codes = [&](int32_t g, int i, auto do_load) __attribute__((always_inline)) {
     const int32_t gc = g < last ? g : last;  // stages behind the last one load it again
     // a lane's offset is never below zero: what it does not go back it goes on from the stage before
     const uint32_t on = kStageBytes - (gc == last ? (uint32_t)behind : 0u);
     const int32_t at = (gc - 1) * kStageBytes;
     auto load = [&](const uint8_t* base, int32_t bytes, uint32_t lane_off) __attribute__((always_inline)) {
       const int32_t left = bytes - at;  // ranges are below 2^31 - 128 (checked on the host)
-      const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
-          const_cast<uint8_t*>(base + at), (short)0, left > 0 ? left : 0, 0x00020000);
-      return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, (int)(lane_off + on), 0, 0));
+      do_load(__builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(base + at), (short)0, left > 0 ? left : 0,
+                                                0x00020000),
+              (int)(lane_off + on));
     };
-#pragma unroll
-    for (int i = NC * Q / 4; i < NC * (Q + 1) / 4; ++i) {
-      if (i < NX) {
-        if constexpr (MODE == MODE_GATEUP)
-          to[i] = load(a.x_codes, (int32_t)(a.M / a.topk * half), xoff[i < NX ? i : 0]);
-        else
-          to[i] = load(a.x_codes + (row0 + 32 * i) * half, (int32_t)((rows - 32 * i) * half), off);
-      } else {
-        // rows 32 (i - NX) .. + 31 of the stage: block (i - NX) % WN of wave column (i - NX) / WN
-        const int c = (i - NX) / WN, j = (i - NX) % WN;
-        const bool up = MODE == MODE_GATEUP && j >= NJ;
-        const int64_t n = n0 + 32 * (c * NJ + (up ? j - NJ : j));
-        to[i] = load((up ? a.w1_codes : a.w0_codes) + (e * N + n) * half, (int32_t)((N - n) * half), off);
-      }
+    if (i < NX) {
+      if constexpr (MODE == MODE_GATEUP)
+        load(a.x_codes, (int32_t)(a.M / a.topk * half), xoff[i < NX ? i : 0]);
+      else
+        load(a.x_codes + (row0 + 32 * i) * half, (int32_t)((rows - 32 * i) * half), off);
+    } else {
+      // rows 32 (i - NX) .. + 31 of the stage: block (i - NX) % WN of wave column (i - NX) / WN
+      const int c = (i - NX) / WN, j = (i - NX) % WN;
+      const bool up = MODE == MODE_GATEUP && j >= NJ;
+      const int64_t n = n0 + 32 * (c * NJ + (up ? j - NJ : j));
+      load((up ? a.w1_codes : a.w0_codes) + (e * N + n) * half, (int32_t)((N - n) * half), off);
     }
+  };
+  auto stage_rows = [&](int i, auto stc) __attribute__((always_inline)) {  // where load i's rows go
+    constexpr int ST = decltype(stc)::value;
+    return i < NX ? lds.x[ST] + (32 * i + 8 * wave) * kStageBytes
+                  : lds.w[ST] + (32 * (i - NX) + 8 * wave) * kStageBytes;
+  };
+  // Two buffers: a stage's codes pass through NC registers of 16 bytes per lane, in four groups: fetch
+  // loads group q of stage g, put writes it to a buffer.
+  u32x4 held[BUFS == 2 ? NC : 1];
+  auto fetch_to = [&](u32x4* to, int32_t g, auto qc) __attribute__((always_inline)) {
+    constexpr int Q = decltype(qc)::value;
+#pragma unroll
+    for (int i = NC * Q / 4; i < NC * (Q + 1) / 4; ++i)
+      load_codes(g, i, [&](__amdgpu_buffer_rsrc_t r, int at) __attribute__((always_inline)) {
+        to[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, at, 0, 0));
+      });
+  };
+  auto put_from = [&](const u32x4* from, auto qc, auto stc) __attribute__((always_inline)) {
+    constexpr int Q = decltype(qc)::value;
+#pragma unroll
+    for (int i = NC * Q / 4; i < NC * (Q + 1) / 4; ++i)
+      *reinterpret_cast<u32x4*>(stage_rows(i, stc) + lane * 16) = from[i];
   };
   auto fetch = [&](int32_t g, auto qc) __attribute__((always_inline)) { fetch_to(held, g, qc); };
-  auto put_from = [&](const u32x4(&from)[NC], auto qc, auto stc) __attribute__((always_inline)) {
-    constexpr int Q = decltype(qc)::value, ST = decltype(stc)::value;
-#pragma unroll
-    for (int i = NC * Q / 4; i < NC * (Q + 1) / 4; ++i) {
-      uint8_t* const to = i < NX ? lds.x[ST] + (32 * i + 8 * wave) * kStageBytes
-                                 : lds.w[ST] + (32 * (i - NX) + 8 * wave) * kStageBytes;
-      *reinterpret_cast<u32x4*>(to + lane * 16) = from[i];
-    }
-  };
   auto put = [&](auto qc, auto stc) __attribute__((always_inline)) { put_from(held, qc, stc); };
+  // One buffer: copied to LDS without registers.
+  auto copy = [&](int32_t g) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < NC; ++i)
+      load_codes(g, i, [&](__amdgpu_buffer_rsrc_t r, int at) __attribute__((always_inline)) {
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(
+            r, (__attribute__((address_space(3))) void*)stage_rows(i, std::integral_constant<int, 0>{}), 16, at, 0, 0, 0);
+      });
+  };
   // The stage's 8 scale bytes of a row.  The last, partial stage reads the row's last 8 bytes and
   // moves the ones it needs down (k >= 256: a row has 8); blocks behind k get byte 0, a finite scale.
   struct Scales {
@@ -506,21 +526,10 @@ __device__ __forceinline__ void mx_tile(const MxArgs& a, const TileLds& lds, int
     read(X, 0, c0);
   } else {
     scales = load_scales(0);
-    fetch(0, c0);
-    fetch(0, c1);
-    fetch(0, c2);
-    fetch(0, c3);
+    copy(0);
     put_scales(scales, 0, c0);
-    put(c0, c0);
-    put(c1, c0);
-    put(c2, c0);
-    put(c3, c0);
     scales = load_scales(1);
-    fetch(1, c0);
-    fetch(1, c1);
-    fetch(1, c2);
-    fetch(1, c3);
-    __builtin_amdgcn_s_waitcnt(0xC07F);
+    __builtin_amdgcn_s_waitcnt(0);
     __builtin_amdgcn_s_barrier();
   }
 
@@ -579,44 +588,42 @@ __device__ __forceinline__ void mx_tile(const MxArgs& a, const TileLds& lds, int
     mma(Y, c3, stc);
     interleave(std::integral_constant<int, NR>{});
   };
-  // One buffer: the stage's last slice is multiplied over the writes of the next stage and the loads
-  // of the one after; the CU's second workgroup fills what the reads and the two barriers leave
-  // idle.  A wave has 256 registers, so each slice's fragments are read when the last one's are used.
+  // One buffer: once every wave's fragments of the last slice are in registers the next stage is
+  // copied over it; the CU's second workgroup multiplies meanwhile.
   auto stage1 = [&](int32_t g) __attribute__((always_inline)) {
     constexpr int NF = WM * WN;
+    constexpr int NR = WM + WN;
+    Frag Y;
+    auto reads = [&]() __attribute__((always_inline)) {
+#pragma unroll
+      for (int i = 0; i < NF; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        if (i < NR) __builtin_amdgcn_sched_group_barrier(0x100, NF >= NR ? 1 : NR, 0);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    };
     __builtin_amdgcn_sched_barrier(0);
     read_scales(c0);
     read(X, 0, c0);
+    __builtin_amdgcn_sched_barrier(0);
+    read(Y, 1, c0);
     mma(X, c0, c0);
-    __builtin_amdgcn_sched_barrier(0);
-    read(X, 1, c0);
-    mma(X, c1, c0);
-    __builtin_amdgcn_sched_barrier(0);
+    reads();
     read(X, 2, c0);
+    mma(Y, c1, c0);
+    reads();
+    read(Y, 3, c0);
     mma(X, c2, c0);
-    __builtin_amdgcn_sched_barrier(0);
-    read(X, 3, c0);
+    reads();
     __builtin_amdgcn_s_waitcnt(0xC07F);  // this wave's reads of the stage have returned
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
     put_scales(scales, g + 1, c0);
-    put(c0, c0);
-    put(c1, c0);
-    put(c2, c0);
-    put(c3, c0);
     scales = load_scales(g + 2);
-    fetch(g + 2, c0);
-    fetch(g + 2, c1);
-    fetch(g + 2, c2);
-    fetch(g + 2, c3);
-    mma(X, c3, c0);
-#pragma unroll
-    for (int i = 0; i < NF; ++i) {
-      __builtin_amdgcn_sched_group_barrier(0x200, (NC + 2 + NF - 1) / NF, 0);
-      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-      __builtin_amdgcn_sched_group_barrier(0x020, (NC + 2 + NF - 1) / NF, 0);
-    }
-    __builtin_amdgcn_s_waitcnt(0xC07F);  // the next stage is written
+    copy(g + 1);
+    __builtin_amdgcn_sched_barrier(0);
+    mma(Y, c3, c0);
+    __builtin_amdgcn_s_waitcnt(0);  // the next stage is written
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
   };
@@ -691,55 +698,72 @@ __device__ __forceinline__ void mx_tile(const MxArgs& a, const TileLds& lds, int
   else store(std::integral_constant<int, 4>{});
 }
 
-// The tile of workgroup wg among `row_tiles` x `col_tiles`, in an order for the 8 XCDs (workgroup w
-// runs on XCD w % 8, each with an L2 of its own): an XCD takes a contiguous eighth of the list
-// [groups of 4 row tiles][column tiles][row tiles of the group], so the tiles that it computes at a
-// time share 4 row tiles' activations and a few column tiles' weights.  false: no tile.
-__device__ __forceinline__ bool xcd_tile(int64_t wg, int64_t row_tiles, int64_t col_tiles, int64_t& r, int64_t& c) {
-  const uint32_t total = (uint32_t)(row_tiles * col_tiles), share = (total + 7) / 8;  // a grid: below 2^31
-  const uint32_t t = ((uint32_t)wg & 7) * share + ((uint32_t)wg >> 3);
-  if (((uint32_t)wg >> 3) >= share || t >= total) return false;
-  const uint32_t group = t / (4 * (uint32_t)col_tiles), in = t % (4 * (uint32_t)col_tiles);
-  const uint32_t left = (uint32_t)row_tiles - 4 * group, here = left < 4 ? left : 4;
+// The tile of workgroup wg among row_tiles x col_tiles, in an order for the 8 XCDs (workgroup w runs
+// on XCD w % 8, each with an L2 of its own): an XCD takes a contiguous eighth of the list [groups of
+// 4 row tiles][column tiles][row tiles of the group], so the tiles that it computes at a time share
+// 4 row tiles' activations and a few column tiles' weights.  (Experts' tiles cost unequally; blocks
+// of 4 x 8 tiles going round the XCDs even that out, 843 us against 860 for 4096 tokens, but cost
+// the decode step of 32 tokens more: 372 against 332.)  false: no tile.
+__device__ __forceinline__ bool xcd_tile(uint32_t wg, uint32_t row_tiles, uint32_t col_tiles, int64_t& r,
+                                         int64_t& c) {
+  const uint32_t total = row_tiles * col_tiles, share = (total + 7) / 8;  // a grid: below 2^31
+  const uint32_t k = wg >> 3, t = (wg & 7) * share + k;
+  if (k >= share || t >= total) return false;
+  const uint32_t group = t / (4 * col_tiles), in = t % (4 * col_tiles);
+  const uint32_t left = row_tiles - 4 * group, here = left < 4 ? left : 4;
   c = in / here;
   r = 4 * group + in % here;
   return true;
 }
 
-// The rows of row tile `tile` of an MoE product: every expert's rows in tiles of `size`, experts in
-// order.  Every wave finds it by itself.  Returns the number of row tiles where tile < 0.
-__device__ __forceinline__ int64_t expert_tile(const int32_t* offsets, int32_t experts, int size, int64_t tile,
-                                               int64_t& e, int64_t& row0, int64_t& rows) {
-  const int lane = threadIdx.x & 63;
-  int64_t before = 0;
-  for (int32_t eb = 0; eb < experts; eb += 64) {
-    const int32_t ex = eb + lane;
-    const int32_t from = ex < experts ? offsets[ex] : 0;
-    const int32_t count = ex < experts ? offsets[ex + 1] - from : 0;
-    const int32_t nt = count > 0 ? (count + size - 1) / size : 0;
-    int32_t incl = nt;
+// The row tiles of an MoE product: every expert's rows in tiles of `size`, experts in order.  Every
+// wave counts and finds them by itself; lane l holds experts l, l + 64, ...
+struct ExpertTiles {
+  const int32_t* offsets;
+  int32_t experts, size;
+  int32_t from, count, incl, tiles;  // of the 64 experts from `base` on: first row, rows, tiles up to
+  int32_t base = -1;                 // and with this lane's, this lane's
+  __device__ __forceinline__ void load(int32_t eb) {
+    if (base == eb) return;
+    base = eb;
+    const int lane = threadIdx.x & 63, ex = eb + lane;
+    from = ex < experts ? offsets[ex] : 0;
+    count = ex < experts ? offsets[ex + 1] - from : 0;
+    tiles = count > 0 ? (count + size - 1) / size : 0;
+    incl = tiles;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
       const int32_t v = __shfl_up(incl, d);
       if (lane >= d) incl += v;
     }
-    const int64_t all = __builtin_amdgcn_readlane(incl, 63);
-    if (tile >= before && tile < before + all) {
-      const int64_t want = tile - before;
-      const uint64_t hit = __ballot(want >= incl - nt && want < incl);
-      const int src = __ffsll((unsigned long long)hit) - 1;
-      const int at = __builtin_amdgcn_readfirstlane(src);
-      const int32_t k = (int32_t)want - __builtin_amdgcn_readlane(incl - nt, at);
-      e = eb + at;
-      row0 = __builtin_amdgcn_readlane(from, at) + k * size;
-      const int32_t left = __builtin_amdgcn_readlane(count, at) - k * size;
-      rows = left < size ? left : size;
-      return 0;
-    }
-    before += all;
   }
-  return __builtin_amdgcn_readfirstlane((int)before);
-}
+  __device__ __forceinline__ int32_t total() {
+    int32_t sum = 0;
+    for (int32_t eb = 0; eb < experts; eb += 64) {
+      load(eb);
+      sum += __builtin_amdgcn_readlane(incl, 63);
+    }
+    return sum;
+  }
+  __device__ __forceinline__ void find(int32_t tile, int64_t& e, int64_t& row0, int64_t& rows) {
+    for (int32_t eb = 0; eb < experts; eb += 64) {
+      load(eb);
+      const int32_t all = __builtin_amdgcn_readlane(incl, 63);
+      if (tile < all) {
+        const uint64_t hit = __ballot(tile >= incl - tiles && tile < incl);
+        const int at = __builtin_amdgcn_readfirstlane(__ffsll((unsigned long long)hit) - 1);
+        const int32_t k = tile - __builtin_amdgcn_readlane(incl - tiles, at);
+        e = eb + at;
+        row0 = __builtin_amdgcn_readlane(from, at) + k * size;
+        const int32_t left = __builtin_amdgcn_readlane(count, at) - k * size;
+        rows = left < size ? left : size;
+        return;
+      }
+      tile -= all;
+    }
+    rows = 0;
+  }
+};
 
 // WM: the largest tile's; a tile with few rows left takes a smaller one.
 template <int MODE, int WM, int WN, int BUFS>
@@ -752,18 +776,19 @@ void mx_tiled_kernel(const MxArgs a, int32_t experts) {
   __shared__ __attribute__((aligned(16))) uint8_t w1[BUFS == 1 ? 16 : WR * kStageBytes];
   __shared__ __attribute__((aligned(16))) uint8_t s0[(XR + WR) * 8];
   __shared__ __attribute__((aligned(16))) uint8_t s1[BUFS == 1 ? 16 : (XR + WR) * 8];
+  // (two-buffer arrays apart: the compiler tells them apart, and waits for no write to the other)
   const TileLds lds{{codes0, x1}, {BUFS == 1 ? codes0 + XR * kStageBytes : w0, w1}, {s0, s1}};
   constexpr int64_t cols = MODE == MODE_GATEUP ? 32 * WN : 64 * WN;
   const int64_t col_tiles = (a.N + cols - 1) / cols;
   int64_t r, c, e = 0, row0, rows;
   if constexpr (MODE == MODE_DENSE) {
-    if (!xcd_tile(blockIdx.x, (a.M + XR - 1) / XR, col_tiles, r, c)) return;
+    if (!xcd_tile(blockIdx.x, (uint32_t)((a.M + XR - 1) / XR), (uint32_t)col_tiles, r, c)) return;
     row0 = r * XR;
     rows = a.M - row0 < XR ? a.M - row0 : XR;
   } else {
-    const int64_t row_tiles = expert_tile(a.offsets, experts, XR, -1, e, row0, rows);
-    if (!xcd_tile(blockIdx.x, row_tiles, col_tiles, r, c)) return;
-    expert_tile(a.offsets, experts, XR, r, e, row0, rows);
+    ExpertTiles tiles{a.offsets, experts, XR};
+    if (!xcd_tile(blockIdx.x, (uint32_t)tiles.total(), (uint32_t)col_tiles, r, c)) return;
+    tiles.find((int32_t)r, e, row0, rows);
   }
   if constexpr (WM == 4) {
     if (rows > 128) mx_tile<MODE, 4, WN, BUFS>(a, lds, e, row0, rows, c);
@@ -844,8 +869,9 @@ bool tiles_fit(int mode, const MxArgs& a) {
 hipError_t product_dense(const MxArgs& a, hipStream_t stream) {
   const auto tiles = [&](int64_t bm, int64_t bn) { return ceil_div(a.M, bm) * ceil_div(a.N, bn); };
   if (a.M > 32 && tiles_fit(MODE_DENSE, a)) {
-    if (tiles(256, 256) >= 192 && a.K >= 4096) return launch_tiles<MODE_DENSE, 4, 4, 2>(a, 1, stream);
-    if (tiles(128, 256) >= 256) return launch_tiles<MODE_DENSE, 2, 4, 1>(a, 1, stream);
+    if (tiles(256, 256) >= 192 && a.K > 2048) return launch_tiles<MODE_DENSE, 4, 4, 2>(a, 1, stream);
+    if (tiles(128, 256) >= 512) return launch_tiles<MODE_DENSE, 2, 4, 1>(a, 1, stream);
+    if (tiles(128, 256) >= 192) return launch_tiles<MODE_DENSE, 2, 4, 2>(a, 1, stream);
     if (tiles(128, 128) >= 128) return launch_tiles<MODE_DENSE, 2, 2, 2>(a, 1, stream);
     if (tiles(32, 16) >= 850) return launch_tiles<MODE_DENSE, 1, 1, 2>(a, 1, stream);
   }
@@ -870,7 +896,7 @@ hipError_t product_experts(const MxArgs& a, int64_t experts, hipStream_t stream)
     return rows <= 32.0 ? launch_stream<MODE, 1, 4>(a, experts, 1, stream)
                         : launch_tiles<MODE, 2, 2, 2>(a, experts, stream);
   if (rows < 128.0) return launch_tiles<MODE, 2, 4, 2>(a, experts, stream);
-  if (a.K < 4096 || (a.M / 256 + active) * cols < 512) return launch_tiles<MODE, 2, 4, 1>(a, experts, stream);
+  if (a.K <= 2048 || (a.M / 256 + active) * cols < 512) return launch_tiles<MODE, 2, 4, 1>(a, experts, stream);
   return launch_tiles<MODE, 4, 4, 2>(a, experts, stream);
 }
 
