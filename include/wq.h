@@ -146,7 +146,8 @@ wq_status wq_dequantize(const wq_weight* w, uint16_t* out, void* stream);
  * operator benchmarks).  x bf16 [m][k], y bf16 [m][n], w->experts must be 1.  m == 0 is a
  * no-op.  Small m (<= 32) runs the decode kernels that stream the packed weights once;
  * larger m runs the MFMA kernel with LDS-staged dequantized tiles, except group-64 INT8,
- * which runs the decode kernels at every m (in launches of at most 65535 x 32 rows). */
+ * which runs the decode kernels at every m (in launches of at most 65535 x 32 rows), and MXFP4,
+ * which runs them until the tiles fill the chip. */
 wq_status wq_gemm(const uint16_t* x, int64_t m, const wq_weight* w, uint16_t* y, void* stream);
 
 /* ---- Mixture-of-experts expert FFN --------------------------------------------------------

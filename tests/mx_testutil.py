@@ -73,7 +73,7 @@ def gate_up_bound(g, gm, u, um, k):
     |silu(g)| <= |g|), the exponential's argument (|g| 2^-23 relative in e^-g) and a few fp32
     roundings, then the output's rounding."""
     dg, du = k * 2.0 ** -23 * gm, k * 2.0 ** -23 * um
-    h = g / (1 + np.exp(-g)) * u
+    h = g / (1 + np.exp(-np.clip(g, -700, None))) * u
     err = 1.1 * dg * (np.abs(u) + du) + np.abs(g) * du + np.abs(h) * (8 + 2 * np.abs(g)) * 2.0 ** -23
     return h, err + HALF["bf16"] * (np.abs(h) + err) + 2.0 ** -126
 

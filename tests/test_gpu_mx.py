@@ -432,3 +432,92 @@ def test_mx_ffn_captured(wq, t):
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(y, want)
+
+
+# ---------------------------------------------------------------------------------------------
+# sizes that reach every kernel of the products: the references multiply in float64 on the GPU
+# ---------------------------------------------------------------------------------------------
+
+def _mm64(x, w):
+    """(x w^T, magnitudes) in fp64 of host values, multiplied on the GPU."""
+    import torch
+
+    a, b = torch.from_numpy(x).cuda(), torch.from_numpy(np.ascontiguousarray(w.T)).cuda()
+    return torch.mm(a, b).cpu().numpy(), torch.mm(a.abs(), b.abs()).cpu().numpy()
+
+
+# dense tiles of 64 x 64, 128 x 128, 128 x 256 (two buffers, one buffer), 256 x 256; k with a stage that
+# ends inside, n that no 16-byte piece divides
+BIG = [(513, 900, 1088), (1300, 1700, 448), (1500, 4100, 320), (4100, 4099, 256), (4111, 4096, 576), (3100, 4097, 2112)]
+
+
+@pytest.mark.parametrize("m,n,k", BIG)
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+def test_gemm_mx_every_tile(wq, m, n, k, out):
+    import torch
+
+    _say("gemm_mx big", m, n, k, out)
+    rng = np.random.default_rng(m)
+    code, byte = mx.encode(rng.standard_normal((n, k)) * np.exp2(rng.integers(-2, 3, (n, 1))))
+    xc, xb = mx.encode(mx.bf16(rng.standard_normal((m, k))))
+    y = torch.full((m + 1, n), 9.0, dtype=torch.bfloat16 if out == "bf16" else torch.float32, device="cuda")
+    wq.wq_gemm_mx(mx.weight(wq, xc[None], xb[None]), mx.weight(wq, code[None], byte[None]), y=y[:m])
+    assert bool((y[m] == 9.0).all()), "the row behind the last one was written"
+    ref, mag = _mm64(mx.values(xc, xb), mx.values(code, byte))
+    mx.assert_within(mx.to_host(y[:m]), ref, mx.sum_bound(ref, mag, k, out), f"{m} {n} {k}")
+
+
+@pytest.mark.parametrize("m,n,k", [(40, 28801, 192), (100, 17001, 64), (1400, 2000, 320), (2000, 1537, 448)])
+def test_gemm_bf16_activations_tiled(wq, m, n, k):
+    import torch
+
+    _say("gemm bf16 tiled", m, n, k)
+    rng = np.random.default_rng(m)
+    code, byte = mx.encode(rng.standard_normal((n, k)))
+    byte[n // 2, -1] = 255
+    x = mx.bf16(rng.standard_normal((m, k)))
+    y = wq.wq_gemm(_cuda(x, torch.bfloat16), mx.weight(wq, code[None], byte[None]))
+    ref, mag = _mm64(x, mx.values(code, byte))
+    mx.assert_within(mx.to_host(y), ref, mx.sum_bound(np.nan_to_num(ref), np.nan_to_num(mag), k, "bf16"), "tiled")
+
+
+# (t, topk, E, n, k, routing) of gate+up and of down: 128 x 256 tiles with two buffers, 128 x 128, 128 x 256
+# with one buffer, 256 x 256 with small tiles beside, more experts than a wave's lanes, none with a row
+MOE_BIG = [(40, 4, 8, 2100, 320, "any"), (200, 2, 4, 300, 320, "dropped"), (300, 2, 3, 2500, 448, "skewed"),
+           (700, 2, 2, 9500, 2112, "skewed"), (300, 4, 130, 700, 256, "any"), (60, 2, 4, 4000, 256, "none")]
+
+
+@pytest.mark.parametrize("t,topk,E,n,k,kind", MOE_BIG)
+def test_moe_mx_every_tile(wq, t, topk, E, n, k, kind):
+    import torch
+
+    _say("moe mx big", t, topk, E, n, k, kind)
+    rng = np.random.default_rng(t + n)
+    ids = np.full((t, topk), E, np.int32) if kind == "none" else _ids(rng, t, topk, E, kind)
+    off, order, _ = mx.route(ids, E)
+    offsets, pairs = wq.wq_moe_route(_cuda(ids), E)
+    g, u = (mx.encode(rng.standard_normal((E, n, k))) for _ in range(2))
+    P, live = t * topk, len(order)
+    gd, ud = mx.weight(wq, *g), mx.weight(wq, *u)
+    for rows, gate_up in ((t, True), (P, False)):
+        xc, xb = mx.encode(mx.bf16(rng.standard_normal((rows, k)) / k ** 0.5))
+        x, xd = mx.values(xc, xb), mx.weight(wq, xc[None], xb[None])
+        o = torch.full((P, n), 7.0, dtype=torch.bfloat16, device="cuda")
+        if gate_up:
+            wq.wq_moe_gate_up_mx(xd, offsets, pairs, topk, gd, ud, h=o)
+        else:
+            wq.wq_moe_down_mx(xd, offsets, gd, d=o)
+        got = mx.to_host(o)
+        assert np.all(got[live:] == 7.0), "rows behind the last expert's were written"
+        for e in range(E):
+            r = slice(off[e], off[e + 1])
+            if off[e] == off[e + 1]:
+                continue
+            xe = x[order[r] // topk] if gate_up else x[r]
+            a, am = _mm64(xe, mx.values(g[0][e], g[1][e]))
+            if gate_up:
+                b, bm = _mm64(xe, mx.values(u[0][e], u[1][e]))
+                ref, bound = mx.gate_up_bound(a, am, b, bm, k)
+            else:
+                ref, bound = a, mx.sum_bound(a, am, k, "bf16")
+            mx.assert_within(got[r], ref, bound, f"expert {e} gate_up {gate_up}")

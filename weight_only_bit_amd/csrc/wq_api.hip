@@ -187,6 +187,16 @@ MoeWs moe_layout(void* ws, int64_t t, int32_t topk, int32_t experts, int64_t hid
 constexpr int32_t kMaxExperts = 512;
 // Up to this many activation rows the decode-streaming kernels run; above it the tiled ones.
 constexpr int64_t kSkinnyMaxRows = 32;
+// MXFP4 decodes so cheaply (half an instruction per weight) that the decode-streaming kernels, which
+// decode again for every 32 rows, stay ahead until the tiled kernel's 256 x 256 tiles fill the chip:
+// they take about 2 m n k / 220 TFLOP/s, one round of tiles 1.6 us per 64 columns of k (0.67 with at
+// most 64 rows, 0.98 with 128).  Measured at k = 4096: 64 x 4096 11.7 us against 43, 512 x 4096 78
+// against 104, 1024 x 4096 154 against 104; 2000 x 515, k 2112: 20 against 57.
+bool mxfp4_streams(const wq_weight* w, int64_t m) {
+  const int64_t most = m <= 64 ? 1150000 : m <= 128 ? 1680000 : 2750000;
+  return w->format == WQ_FMT_MXFP4 && m * w->n < most;
+}
+
 // MoE layers whose experts average at least this many routed rows use the tiled kernels.
 constexpr double kMoeTiledRows = 32.0;
 // Largest grid z extent one launch uses.
@@ -279,7 +289,7 @@ wq_status wq_gemm(const uint16_t* x, int64_t m, const wq_weight* w, uint16_t* y,
   if (!aligned16(x) || !aligned16(y)) return fail(WQ_ERR_ALIGN, "wq_gemm: x or y not 16-byte aligned");
   if (m > (1ll << 31)) return fail(WQ_ERR_UNSUPPORTED, "wq_gemm: m must be below 2^31");
   hipStream_t s = static_cast<hipStream_t>(stream);
-  if (m > kSkinnyMaxRows && has_tiled(w)) {
+  if (m > kSkinnyMaxRows && has_tiled(w) && !mxfp4_streams(w, m)) {
     wq::TiledArgs t{};
     t.w0 = dev_weight(w);
     t.w1 = t.w0;

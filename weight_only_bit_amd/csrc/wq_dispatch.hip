@@ -192,30 +192,47 @@ __global__ __launch_bounds__(256) void unpermute_grad_kernel(const T* __restrict
     return;
   }
   const float w = weights ? weights[p] : 1.f;
-  const T* g = dy + p / topk * hidden;
+  const T* const g = dy + p / topk * hidden;
+  const T* const in = rows + (rows ? r * hidden : 0);
+  T* const out = d_rows + (d_rows ? r * hidden : 0);
   float dot = 0.f;
-  for (int64_t c = (int64_t)lane * E; c < hidden; c += 64 * E) {
-    if (c + E <= hidden) {
+  // U pieces a round, all loads before the first use
+  constexpr int U = 4;
+  const int64_t whole = hidden / E * E;
+  for (int64_t c0 = (int64_t)lane * E; c0 < whole; c0 += 64 * E * U) {
+    u32x4 gv[U], rv[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t c = c0 + 64 * E * u;
+      if (c < whole) {
+        gv[u] = load_piece(g + c);
+        if (d_weights) rv[u] = load_piece(in + c);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t c = c0 + 64 * E * u;
+      if (c >= whole) break;
       float f[E], o[E];
-      unpack(load_piece(g + c), f);
+      unpack(gv[u], f);
       if (d_weights) {
         float v[E];
-        unpack(load_piece(rows + r * hidden + c), v);
+        unpack(rv[u], v);
 #pragma unroll
         for (int i = 0; i < E; ++i) dot = __builtin_fmaf(f[i], v[i], dot);
       }
       if (d_rows) {
 #pragma unroll
         for (int i = 0; i < E; ++i) o[i] = w * f[i];
-        store_piece(d_rows + r * hidden + c, pack(o));
-      }
-    } else {
-      for (int64_t cc = c; cc < hidden; ++cc) {
-        const float f = to_f32(g[cc]);
-        if (d_weights) dot = __builtin_fmaf(f, to_f32(rows[r * hidden + cc]), dot);
-        if (d_rows) d_rows[r * hidden + cc] = from_f32<T>(w * f);
+        store_piece(out + c, pack(o));
       }
     }
+  }
+  const int64_t c = whole + lane;  // the row's last elements, fewer than E
+  if (c < hidden) {
+    const float f = to_f32(g[c]);
+    if (d_weights) dot = __builtin_fmaf(f, to_f32(in[c]), dot);
+    if (d_rows) out[c] = from_f32<T>(w * f);
   }
   if (d_weights) {
 #pragma unroll
