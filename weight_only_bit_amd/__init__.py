@@ -297,7 +297,8 @@ def wq_dequantize(w: PackedWeight, out=None):
 
     if out is None:
         out = torch.empty((w.experts, w.n, w.k), dtype=torch.int16, device=w.codes.device)
-    _need(out, "wq_dequantize out", "bf16", numel=w.experts * w.n * w.k)
+    else:
+        _need(out, "wq_dequantize out", "bf16", numel=w.experts * w.n * w.k)
     _check(lib().wq_dequantize(ctypes.byref(w.cstruct()), _ptr(out), _stream()), "wq_dequantize")
     return out
 
@@ -312,7 +313,8 @@ def wq_gemm(x, w: PackedWeight, y=None):
     _need(x, "wq_gemm x", "bf16", shape=(m, w.k))
     if y is None:
         y = torch.empty((m, w.n), dtype=torch.bfloat16, device=x.device)
-    _need(y, "wq_gemm y", "bf16", shape=(m, w.n))
+    else:
+        _need(y, "wq_gemm y", "bf16", shape=(m, w.n))
     _check(lib().wq_gemm(_ptr(x), m, ctypes.byref(w.cstruct()), _ptr(y), _stream()), "wq_gemm")
     return y
 
@@ -525,16 +527,24 @@ def _mx_rows(x, what, rows=None, k=None):
     return x
 
 
+def _product_out(y, dtype, like, shape, name):
+    """(wq_type, output): y checked, or a new tensor of `dtype` (bf16 by default)."""
+    import torch
+
+    if y is None:
+        y = like.new_empty(shape, dtype=dtype or torch.bfloat16)
+        return _value_type(y, name)[0], y
+    vt, kind = _value_type(y, name)
+    if dtype is not None and y.dtype != dtype:
+        raise TypeError(f"{name}: dtype {y.dtype} is not the {dtype} asked for")
+    return vt, _need(y, name, kind, shape=shape)
+
+
 def wq_gemm_mx(x, w: PackedWeight, y=None, dtype=None):
     """y = x @ W^T with both operands in MXFP4; x: wq_quantize_mx of the rows [m, k].  y is bf16, or
     fp32 with dtype=torch.float32 (or a y of that type)."""
-    import torch
-
     _mx_rows(x, "wq_gemm_mx x", k=w.k)
-    if y is None:
-        y = x.codes.new_empty((x.n, w.n), dtype=dtype or torch.bfloat16)
-    vt, kind = _value_type(y, "wq_gemm_mx y")
-    _need(y, "wq_gemm_mx y", kind, shape=(x.n, w.n))
+    vt, y = _product_out(y, dtype, x.codes, (x.n, w.n), "wq_gemm_mx y")
     _check(lib().wq_gemm_mx(_ptr(x.codes), _ptr(x.qscale), x.n, ctypes.byref(w.cstruct()), _ptr(y), vt,
                             _stream()), "wq_gemm_mx")
     return y
@@ -551,7 +561,8 @@ def wq_moe_gate_up_mx(x, offsets, sorted_pairs, topk: int, gate: PackedWeight, u
     _need(sorted_pairs, "wq_moe_gate_up_mx sorted_pairs", "i32", numel=t * topk)
     if h is None:
         h = x.codes.new_empty((t * topk, gate.n), dtype=torch.bfloat16)
-    _need(h, "wq_moe_gate_up_mx h", "bf16", shape=(t * topk, gate.n))
+    else:
+        _need(h, "wq_moe_gate_up_mx h", "bf16", shape=(t * topk, gate.n))
     _check(lib().wq_moe_gate_up_mx(_ptr(x.codes), _ptr(x.qscale), t, _ptr(offsets), _ptr(sorted_pairs),
                                    topk, ctypes.byref(gate.cstruct()), ctypes.byref(up.cstruct()),
                                    _ptr(h), _stream()), "wq_moe_gate_up_mx")
@@ -561,14 +572,9 @@ def wq_moe_gate_up_mx(x, offsets, sorted_pairs, topk: int, gate: PackedWeight, u
 def wq_moe_down_mx(h, offsets, down: PackedWeight, d=None, dtype=None):
     """d [npairs, hidden] = down h with both operands in MXFP4; h: wq_quantize_mx of the rows
     [npairs, inter] in expert order, the order d is in too.  bf16, or fp32 as in wq_gemm_mx."""
-    import torch
-
     _mx_rows(h, "wq_moe_down_mx h", k=down.k)
     _need(offsets, "wq_moe_down_mx offsets", "i32", numel=down.experts + 1)
-    if d is None:
-        d = h.codes.new_empty((h.n, down.n), dtype=dtype or torch.bfloat16)
-    vt, kind = _value_type(d, "wq_moe_down_mx d")
-    _need(d, "wq_moe_down_mx d", kind, shape=(h.n, down.n))
+    vt, d = _product_out(d, dtype, h.codes, (h.n, down.n), "wq_moe_down_mx d")
     _check(lib().wq_moe_down_mx(_ptr(h.codes), _ptr(h.qscale), h.n, _ptr(offsets),
                                 ctypes.byref(down.cstruct()), _ptr(d), vt, _stream()), "wq_moe_down_mx")
     return d
@@ -589,7 +595,8 @@ def wq_moe_positions(topk_ids, offsets, sorted_pairs, positions=None):
     _need(sorted_pairs, "wq_moe_positions sorted_pairs", "i32", numel=t * topk)
     if positions is None:
         positions = topk_ids.new_empty((t, topk))
-    _need(positions, "wq_moe_positions positions", "i32", shape=(t, topk))
+    else:
+        _need(positions, "wq_moe_positions positions", "i32", shape=(t, topk))
     _check(lib().wq_moe_positions(_ptr(topk_ids), t, topk, offsets.numel() - 1, _ptr(offsets),
                                   _ptr(sorted_pairs), _ptr(positions), _stream()), "wq_moe_positions")
     return positions
@@ -613,7 +620,8 @@ def wq_moe_permute(x, positions, rows=None):
     _need(x, "wq_moe_permute x", kind, shape=(t, hidden))
     if rows is None:
         rows = x.new_empty((t * topk, hidden))
-    _need(rows, "wq_moe_permute rows", kind, shape=(t * topk, hidden))
+    else:
+        _need(rows, "wq_moe_permute rows", kind, shape=(t * topk, hidden))
     _check(lib().wq_moe_permute(_ptr(x), vt, t, topk, hidden, _ptr(positions), _ptr(rows), _stream()),
            "wq_moe_permute")
     return rows
@@ -631,7 +639,8 @@ def wq_moe_unpermute(rows, positions, topk_weights=None, y=None):
         _need(topk_weights, "wq_moe_unpermute topk_weights", "f32", shape=(t, topk))
     if y is None:
         y = rows.new_empty((t, hidden))
-    _need(y, "wq_moe_unpermute y", kind, shape=(t, hidden))
+    else:
+        _need(y, "wq_moe_unpermute y", kind, shape=(t, hidden))
     _check(lib().wq_moe_unpermute(_ptr(rows), vt, _ptr(positions), _ptr(topk_weights), t, topk, hidden,
                                   _ptr(y), _stream()), "wq_moe_unpermute")
     return y
@@ -652,7 +661,8 @@ def wq_moe_unpermute_grad(dy, rows, positions, topk_weights=None, d_rows=None, d
         _need(topk_weights, "wq_moe_unpermute_grad topk_weights", "f32", shape=(t, topk))
     if d_rows is None:
         d_rows = dy.new_empty((t * topk, hidden))
-    _need(d_rows, "wq_moe_unpermute_grad d_rows", kind, shape=(t * topk, hidden))
+    else:
+        _need(d_rows, "wq_moe_unpermute_grad d_rows", kind, shape=(t * topk, hidden))
     if rows is not None:
         _need(rows, "wq_moe_unpermute_grad rows", kind, shape=(t * topk, hidden))
         if d_weights is None:
