@@ -80,11 +80,11 @@ struct Item {
   int64_t col;
 };
 template <int LPR, int E>
-__device__ __forceinline__ Item item(int64_t t, int64_t hidden) {
+__device__ __forceinline__ Item item(int64_t first, int64_t t, int64_t hidden) {
   const uint32_t slices = (uint32_t)((hidden + LPR * E - 1) / (LPR * E));
-  int64_t group = ((int64_t)blockIdx.x * 256 + threadIdx.x) / LPR;
+  int64_t group = ((first + blockIdx.x) * 256 + threadIdx.x) / LPR;
   if constexpr (LPR == 64)
-    group = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    group = (first + blockIdx.x) * 4 + __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   Item r;
   r.token = group / slices;
   r.col = ((group % slices) * LPR + (threadIdx.x & (LPR - 1))) * E;
@@ -95,9 +95,9 @@ __device__ __forceinline__ Item item(int64_t t, int64_t hidden) {
 template <typename T, int LPR>
 __global__ __launch_bounds__(256) void permute_kernel(const T* __restrict__ x, int64_t t, int32_t topk,
                                                       int64_t hidden, const int32_t* __restrict__ positions,
-                                                      T* __restrict__ rows) {
+                                                      T* __restrict__ rows, int64_t first) {
   constexpr int E = 16 / (int)sizeof(T);
-  const Item it = item<LPR, E>(t, hidden);
+  const Item it = item<LPR, E>(first, t, hidden);
   if (it.token >= t) return;
   const int64_t npairs = t * topk;
   const int32_t* pos = positions + it.token * topk;
@@ -124,9 +124,10 @@ template <typename T, int LPR>
 __global__ __launch_bounds__(256) void unpermute_kernel(const T* __restrict__ rows,
                                                         const int32_t* __restrict__ positions,
                                                         const float* __restrict__ weights, int64_t t,
-                                                        int32_t topk, int64_t hidden, T* __restrict__ y) {
+                                                        int32_t topk, int64_t hidden, T* __restrict__ y,
+                                                        int64_t first) {
   constexpr int E = 16 / (int)sizeof(T);
-  const Item it = item<LPR, E>(t, hidden);
+  const Item it = item<LPR, E>(first, t, hidden);
   if (it.token >= t) return;
   const int64_t npairs = t * topk;
   const int64_t p0 = it.token * topk;
@@ -181,10 +182,10 @@ __global__ __launch_bounds__(256) void unpermute_grad_kernel(const T* __restrict
                                                              const float* __restrict__ weights,
                                                              int64_t npairs, int32_t topk, int64_t hidden,
                                                              T* __restrict__ d_rows,
-                                                             float* __restrict__ d_weights) {
+                                                             float* __restrict__ d_weights, int64_t first) {
   constexpr int E = 16 / (int)sizeof(T);
   const int lane = threadIdx.x & 63;
-  const int64_t p = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const int64_t p = (first + blockIdx.x) * 4 + __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   if (p >= npairs) return;
   const int64_t r = positions[p];
   if (r < 0 || r >= npairs) {
@@ -264,13 +265,10 @@ static hipError_t permute_t(const T* x, int64_t t, int32_t topk, int64_t hidden,
                             T* rows, hipStream_t s) {
   constexpr int E = 16 / (int)sizeof(T);
   const int lpr = row_lanes(hidden, E);
-  const int64_t wgs = row_wgs(t, hidden, E, lpr);
-  if (wgs > 0x7FFFFFFF) return hipErrorInvalidValue;
-  const dim3 grid((unsigned)wgs), block(256);
-  if (lpr == 64) hipLaunchKernelGGL((permute_kernel<T, 64>), grid, block, 0, s, x, t, topk, hidden, positions, rows);
-  else if (lpr == 32) hipLaunchKernelGGL((permute_kernel<T, 32>), grid, block, 0, s, x, t, topk, hidden, positions, rows);
-  else hipLaunchKernelGGL((permute_kernel<T, 8>), grid, block, 0, s, x, t, topk, hidden, positions, rows);
-  return hipGetLastError();
+  return launch_in_parts(row_wgs(t, hidden, E, lpr), [&](int64_t first, dim3 grid) {
+    const auto kernel = lpr == 64 ? permute_kernel<T, 64> : lpr == 32 ? permute_kernel<T, 32> : permute_kernel<T, 8>;
+    hipLaunchKernelGGL(kernel, grid, dim3(256), 0, s, x, t, topk, hidden, positions, rows, first);
+  });
 }
 
 hipError_t launch_permute(const void* x, int f32, int64_t t, int32_t topk, int64_t hidden,
@@ -285,13 +283,10 @@ static hipError_t unpermute_t(const T* rows, const int32_t* positions, const flo
                               int32_t topk, int64_t hidden, T* y, hipStream_t s) {
   constexpr int E = 16 / (int)sizeof(T);
   const int lpr = row_lanes(hidden, E);
-  const int64_t wgs = row_wgs(t, hidden, E, lpr);
-  if (wgs > 0x7FFFFFFF) return hipErrorInvalidValue;
-  const dim3 grid((unsigned)wgs), block(256);
-  if (lpr == 64) hipLaunchKernelGGL((unpermute_kernel<T, 64>), grid, block, 0, s, rows, positions, weights, t, topk, hidden, y);
-  else if (lpr == 32) hipLaunchKernelGGL((unpermute_kernel<T, 32>), grid, block, 0, s, rows, positions, weights, t, topk, hidden, y);
-  else hipLaunchKernelGGL((unpermute_kernel<T, 8>), grid, block, 0, s, rows, positions, weights, t, topk, hidden, y);
-  return hipGetLastError();
+  return launch_in_parts(row_wgs(t, hidden, E, lpr), [&](int64_t first, dim3 grid) {
+    const auto kernel = lpr == 64 ? unpermute_kernel<T, 64> : lpr == 32 ? unpermute_kernel<T, 32> : unpermute_kernel<T, 8>;
+    hipLaunchKernelGGL(kernel, grid, dim3(256), 0, s, rows, positions, weights, t, topk, hidden, y, first);
+  });
 }
 
 hipError_t launch_unpermute(const void* rows, int f32, const int32_t* positions, const float* weights,
@@ -306,16 +301,16 @@ hipError_t launch_unpermute_grad(const void* dy, const void* rows, int f32, cons
                                  const float* weights, int64_t t, int32_t topk, int64_t hidden,
                                  void* d_rows, float* d_weights, hipStream_t stream) {
   const int64_t npairs = t * topk;
-  const dim3 grid((unsigned)((npairs + 3) / 4)), block(256);
-  if (f32)
-    hipLaunchKernelGGL(unpermute_grad_kernel<float>, grid, block, 0, stream, static_cast<const float*>(dy),
-                       static_cast<const float*>(rows), positions, weights, npairs, topk, hidden,
-                       static_cast<float*>(d_rows), d_weights);
-  else
-    hipLaunchKernelGGL(unpermute_grad_kernel<uint16_t>, grid, block, 0, stream,
-                       static_cast<const uint16_t*>(dy), static_cast<const uint16_t*>(rows), positions,
-                       weights, npairs, topk, hidden, static_cast<uint16_t*>(d_rows), d_weights);
-  return hipGetLastError();
+  return launch_in_parts((npairs + 3) / 4, [&](int64_t first, dim3 grid) {
+    if (f32)
+      hipLaunchKernelGGL(unpermute_grad_kernel<float>, grid, dim3(256), 0, stream,
+                         static_cast<const float*>(dy), static_cast<const float*>(rows), positions, weights,
+                         npairs, topk, hidden, static_cast<float*>(d_rows), d_weights, first);
+    else
+      hipLaunchKernelGGL(unpermute_grad_kernel<uint16_t>, grid, dim3(256), 0, stream,
+                         static_cast<const uint16_t*>(dy), static_cast<const uint16_t*>(rows), positions,
+                         weights, npairs, topk, hidden, static_cast<uint16_t*>(d_rows), d_weights, first);
+  });
 }
 
 }  // namespace wq

@@ -94,6 +94,19 @@ hipError_t launch_ccq_encode(const float* w, int64_t n, int64_t k, int32_t zp, i
                              uint8_t* codes, uint8_t* qscale, float* super_scale,
                              float* code_scale, float* code_zero, hipStream_t stream);
 
+// A launch holds below 2^32 threads: grids of `wgs` workgroups of 256 in as many launches as that
+// takes, launch(first workgroup, workgroups).
+template <class Launch>
+hipError_t launch_in_parts(int64_t wgs, Launch launch) {
+  constexpr int64_t most = (1ll << 24) - 1;
+  for (int64_t first = 0; first < wgs; first += most) {
+    launch(first, dim3((unsigned)(wgs - first < most ? wgs - first : most)));
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
 // MXFP4 quantisation of n rows of k values (bf16, or fp32 where f32 is set).
 hipError_t launch_mx_quantize(const void* x, int f32, int64_t n, int64_t k, uint8_t* codes,
                               uint8_t* scales, hipStream_t stream);

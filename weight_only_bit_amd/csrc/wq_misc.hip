@@ -73,8 +73,9 @@ __global__ __launch_bounds__(256) void dequant_kernel(const DevWeight w, int64_t
 // flat array, so rows play no part.
 __global__ __launch_bounds__(256) void dequant_mxfp4_kernel(const uint8_t* __restrict__ codes,
                                                             const uint8_t* __restrict__ scales,
-                                                            int64_t octets, uint16_t* __restrict__ out) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+                                                            int64_t octets, uint16_t* __restrict__ out,
+                                                            int64_t first) {
+  const int64_t i = (first + blockIdx.x) * 256 + threadIdx.x;
   if (i >= octets) return;
   uint32_t p[8];
   mxfp4_decode16(reinterpret_cast<const uint32_t*>(codes)[i], 0u, scales[i >> 2], p);
@@ -443,11 +444,10 @@ hipError_t launch_dequant(int fmt, const DevWeight& w, int64_t experts, uint16_t
   const int64_t rows = experts * w.n;
   if (fmt == FMT_MXFP4) {
     const int64_t octets = rows * (w.k / 8);
-    const int64_t wgs = (octets + 255) / 256;
-    if (wgs > 0x7FFFFFFF) return hipErrorInvalidValue;
-    hipLaunchKernelGGL(dequant_mxfp4_kernel, dim3((unsigned)wgs), dim3(256), 0, stream, w.codes,
-                       w.qscale, octets, out);
-    return hipGetLastError();
+    return launch_in_parts((octets + 255) / 256, [&](int64_t first, dim3 grid) {
+      hipLaunchKernelGGL(dequant_mxfp4_kernel, grid, dim3(256), 0, stream, w.codes, w.qscale, octets, out,
+                         first);
+    });
   }
   const int64_t threads = rows * (w.k / 16);
   const dim3 grid((unsigned)((threads + 255) / 256));

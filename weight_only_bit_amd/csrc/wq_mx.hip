@@ -40,8 +40,8 @@ __device__ __forceinline__ uint32_t umax(uint32_t a, uint32_t b) { return a > b 
 template <typename T>
 __global__ __launch_bounds__(256) void mx_quantize_kernel(const T* __restrict__ x, int64_t octets,
                                                           uint8_t* __restrict__ codes,
-                                                          uint8_t* __restrict__ scales) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;  // 8 values
+                                                          uint8_t* __restrict__ scales, int64_t first) {
+  const int64_t i = (first + blockIdx.x) * 256 + threadIdx.x;  // 8 values
   if (i >= octets) return;  // octets is a multiple of 8: quads stay whole
   uint32_t top = 0, c = 0;
   if constexpr (sizeof(T) == 2) {
@@ -819,15 +819,14 @@ hipError_t launch_tiles(const MxArgs& a, int64_t experts, hipStream_t s) {
 hipError_t launch_mx_quantize(const void* x, int f32, int64_t n, int64_t k, uint8_t* codes,
                               uint8_t* scales, hipStream_t stream) {
   const int64_t octets = n * (k / 8);
-  const int64_t wgs = (octets + 255) / 256;
-  if (wgs > 0x7FFFFFFF) return hipErrorInvalidValue;
-  if (f32)
-    hipLaunchKernelGGL(mx_quantize_kernel<float>, dim3((unsigned)wgs), dim3(256), 0, stream,
-                       static_cast<const float*>(x), octets, codes, scales);
-  else
-    hipLaunchKernelGGL(mx_quantize_kernel<uint16_t>, dim3((unsigned)wgs), dim3(256), 0, stream,
-                       static_cast<const uint16_t*>(x), octets, codes, scales);
-  return hipGetLastError();
+  return launch_in_parts((octets + 255) / 256, [&](int64_t first, dim3 grid) {
+    if (f32)
+      hipLaunchKernelGGL(mx_quantize_kernel<float>, grid, dim3(256), 0, stream,
+                         static_cast<const float*>(x), octets, codes, scales, first);
+    else
+      hipLaunchKernelGGL(mx_quantize_kernel<uint16_t>, grid, dim3(256), 0, stream,
+                         static_cast<const uint16_t*>(x), octets, codes, scales, first);
+  });
 }
 
 namespace {
