@@ -2,10 +2,11 @@
 // the permutation, the weighted way back, and the gradients of both.
 //
 // Everything is driven per token through positions[p], the row of pair p = token * topk + slot in
-// expert order (-1: dropped), so every output element is written by one thread that adds its
-// contributions in slot order: no atomics, the same bits every run.  All of it is bound by
-// memory: rows are read and written once in 16-byte pieces; a row of odd length starts at any
-// element, which these accesses allow, and its last pieces go element by element.
+// expert order (-1: dropped), so a thread adds all of an output element's contributions, in slot
+// order: no atomics, the same bits every run.  All of it is bound by memory (a copy of 2 GiB: 4.8 to
+// 5.3 TB/s); rows are read and written in 16-byte pieces, at any element's address, which a row of
+// odd length starts at.  4096 tokens x 8 of 8192 bf16 (32 tokens): positions 2 us (1.4), permutation
+// 115 us, 5.2 TB/s (4.2), way back 117 us, 5.2 TB/s (4.1), gradient 230 us, 5.0 TB/s (7.3).
 #include <hip/hip_runtime.h>
 
 #include "wq_kernels.hpp"
@@ -72,67 +73,68 @@ __global__ __launch_bounds__(256) void positions_kernel(const int32_t* __restric
   }
 }
 
-// One work item: a lane's piece of one token's row.  LPR lanes (a power of two, at most a wave)
-// take consecutive pieces of a row; a row needs `slices` such groups.  With LPR = 64 the token
-// is the same in the whole wave.
+// One work item: a lane's piece of one token's row.  kLanes neighbouring lanes take consecutive pieces
+// of a row.  More leave lanes idle behind short rows, fewer gain nothing on long ones (us for 65536
+// tokens x 4, way back, with 8, 32, 64 lanes: 64 values 6.9, 16, 29; 128 values 15, 18, 30; 512 values
+// 67, 68, 68; 4096 x 8, 8192 values: 122 each).  The last piece of a row ends with it, over some of the
+// values of the one before, which get the same bits twice (32 tokens x 8, 1027 values: 3.7 us; 8.0 with
+// a row's end value by value); a row shorter than a piece has a lane for each value.
+constexpr int kLanes = 8;
 struct Item {
   int64_t token;
   int64_t col;
 };
-template <int LPR, int E>
+template <int E>
 __device__ __forceinline__ Item item(int64_t first, int64_t t, int64_t hidden) {
-  const uint32_t slices = (uint32_t)((hidden + LPR * E - 1) / (LPR * E));
-  int64_t group = ((first + blockIdx.x) * 256 + threadIdx.x) / LPR;
-  if constexpr (LPR == 64)
-    group = (first + blockIdx.x) * 4 + __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const uint32_t slices = (uint32_t)((hidden + kLanes * E - 1) / (kLanes * E));
+  const int64_t group = ((first + blockIdx.x) * 256 + threadIdx.x) / kLanes;
   Item r;
   r.token = group / slices;
-  r.col = ((group % slices) * LPR + (threadIdx.x & (LPR - 1))) * E;
+  r.col = ((group % slices) * kLanes + (threadIdx.x & (kLanes - 1))) * (hidden < E ? 1 : E);
   if (r.col >= hidden) r.token = t;  // nothing to do
+  else if (hidden >= E && r.col + E > hidden) r.col = hidden - E;
   return r;
 }
 
-template <typename T, int LPR>
+template <typename T>
 __global__ __launch_bounds__(256) void permute_kernel(const T* __restrict__ x, int64_t t, int32_t topk,
                                                       int64_t hidden, const int32_t* __restrict__ positions,
                                                       T* __restrict__ rows, int64_t first) {
   constexpr int E = 16 / (int)sizeof(T);
-  const Item it = item<LPR, E>(first, t, hidden);
+  const Item it = item<E>(first, t, hidden);
   if (it.token >= t) return;
   const int64_t npairs = t * topk;
   const int32_t* pos = positions + it.token * topk;
   const T* src = x + it.token * hidden + it.col;
-  if (it.col + E <= hidden) {
+  if (hidden >= E) {
     const u32x4 v = load_piece(src);
     for (int j = 0; j < topk; ++j) {
       const int64_t r = pos[j];
       if (r >= 0 && r < npairs) store_piece(rows + r * hidden + it.col, v);
     }
   } else {
-    for (int64_t c = it.col; c < hidden; ++c) {
-      const T v = src[c - it.col];
-      for (int j = 0; j < topk; ++j) {
-        const int64_t r = pos[j];
-        if (r >= 0 && r < npairs) rows[r * hidden + c] = v;
-      }
+    const T v = *src;
+    for (int j = 0; j < topk; ++j) {
+      const int64_t r = pos[j];
+      if (r >= 0 && r < npairs) rows[r * hidden + it.col] = v;
     }
   }
 }
 
 // y[t] = sum_j w[t][j] rows[pos[t][j]] in fp32, j in order; w null: 1.
-template <typename T, int LPR>
+template <typename T>
 __global__ __launch_bounds__(256) void unpermute_kernel(const T* __restrict__ rows,
                                                         const int32_t* __restrict__ positions,
                                                         const float* __restrict__ weights, int64_t t,
                                                         int32_t topk, int64_t hidden, T* __restrict__ y,
                                                         int64_t first) {
   constexpr int E = 16 / (int)sizeof(T);
-  const Item it = item<LPR, E>(first, t, hidden);
+  const Item it = item<E>(first, t, hidden);
   if (it.token >= t) return;
   const int64_t npairs = t * topk;
   const int64_t p0 = it.token * topk;
   T* dst = y + it.token * hidden + it.col;
-  if (it.col + E <= hidden) {
+  if (hidden >= E) {
     float acc[E];
 #pragma unroll
     for (int i = 0; i < E; ++i) acc[i] = 0.f;
@@ -161,15 +163,13 @@ __global__ __launch_bounds__(256) void unpermute_kernel(const T* __restrict__ ro
     }
     store_piece(dst, pack(acc));
   } else {
-    for (int64_t c = it.col; c < hidden; ++c) {
-      float acc = 0.f;
-      for (int j = 0; j < topk; ++j) {
-        const int64_t r = positions[p0 + j];
-        if (r >= 0 && r < npairs)
-          acc = __builtin_fmaf(weights ? weights[p0 + j] : 1.f, to_f32(rows[r * hidden + c]), acc);
-      }
-      dst[c - it.col] = from_f32<T>(acc);
+    float acc = 0.f;
+    for (int j = 0; j < topk; ++j) {
+      const int64_t r = positions[p0 + j];
+      if (r >= 0 && r < npairs)
+        acc = __builtin_fmaf(weights ? weights[p0 + j] : 1.f, to_f32(rows[r * hidden + it.col]), acc);
     }
+    *dst = from_f32<T>(acc);
   }
 }
 
@@ -197,7 +197,8 @@ __global__ __launch_bounds__(256) void unpermute_grad_kernel(const T* __restrict
   const T* const in = rows + (rows ? r * hidden : 0);
   T* const out = d_rows + (d_rows ? r * hidden : 0);
   float dot = 0.f;
-  // U pieces a round, all loads before the first use
+  // U pieces a round, all loads before the first use (32 tokens x 8 of 8192 bf16: 7.9 us with one, 6.5
+  // with four)
   constexpr int U = 4;
   const int64_t whole = hidden / E * E;
   for (int64_t c0 = (int64_t)lane * E; c0 < whole; c0 += 64 * E * U) {
@@ -242,14 +243,11 @@ __global__ __launch_bounds__(256) void unpermute_grad_kernel(const T* __restrict
   }
 }
 
-// Workgroups for t rows of `hidden` elements, E per lane and LPR lanes per slice.
-int64_t row_wgs(int64_t t, int64_t hidden, int E, int LPR) {
-  const int64_t groups = t * ((hidden + (int64_t)LPR * E - 1) / ((int64_t)LPR * E));
-  return (groups * LPR + 255) / 256;
+// Workgroups for t rows of `hidden` elements, E per lane.
+int64_t row_wgs(int64_t t, int64_t hidden, int E) {
+  const int64_t slices = (hidden + (int64_t)kLanes * E - 1) / ((int64_t)kLanes * E);
+  return (t * slices * kLanes + 255) / 256;
 }
-
-// Lanes per row slice: a whole wave, fewer for rows shorter than a wave's pieces.
-int row_lanes(int64_t hidden, int E) { return hidden > 32 * E ? 64 : hidden > 8 * E ? 32 : 8; }
 
 }  // namespace
 
@@ -264,10 +262,8 @@ template <typename T>
 static hipError_t permute_t(const T* x, int64_t t, int32_t topk, int64_t hidden, const int32_t* positions,
                             T* rows, hipStream_t s) {
   constexpr int E = 16 / (int)sizeof(T);
-  const int lpr = row_lanes(hidden, E);
-  return launch_in_parts(row_wgs(t, hidden, E, lpr), [&](int64_t first, dim3 grid) {
-    const auto kernel = lpr == 64 ? permute_kernel<T, 64> : lpr == 32 ? permute_kernel<T, 32> : permute_kernel<T, 8>;
-    hipLaunchKernelGGL(kernel, grid, dim3(256), 0, s, x, t, topk, hidden, positions, rows, first);
+  return launch_in_parts(row_wgs(t, hidden, E), [&](int64_t first, dim3 grid) {
+    hipLaunchKernelGGL(permute_kernel<T>, grid, dim3(256), 0, s, x, t, topk, hidden, positions, rows, first);
   });
 }
 
@@ -282,10 +278,8 @@ template <typename T>
 static hipError_t unpermute_t(const T* rows, const int32_t* positions, const float* weights, int64_t t,
                               int32_t topk, int64_t hidden, T* y, hipStream_t s) {
   constexpr int E = 16 / (int)sizeof(T);
-  const int lpr = row_lanes(hidden, E);
-  return launch_in_parts(row_wgs(t, hidden, E, lpr), [&](int64_t first, dim3 grid) {
-    const auto kernel = lpr == 64 ? unpermute_kernel<T, 64> : lpr == 32 ? unpermute_kernel<T, 32> : unpermute_kernel<T, 8>;
-    hipLaunchKernelGGL(kernel, grid, dim3(256), 0, s, rows, positions, weights, t, topk, hidden, y, first);
+  return launch_in_parts(row_wgs(t, hidden, E), [&](int64_t first, dim3 grid) {
+    hipLaunchKernelGGL(unpermute_kernel<T>, grid, dim3(256), 0, s, rows, positions, weights, t, topk, hidden, y, first);
   });
 }
 
