@@ -303,7 +303,8 @@ wq_status wq_moe_down_mx(const uint8_t* h_codes, const uint8_t* h_scales, int64_
  * wq_moe_route sorts the pairs; the calls below move rows.  positions i32[t][topk] holds the row
  * of every pair p = t*topk + j in expert order, -1 for a dropped pair (id outside [0, experts)):
  * a dropped pair contributes nothing, and nothing is written for it.  Rows, tokens and their
- * gradients are of one type; sums are fp32, slots in order, rounded once. */
+ * gradients are of one type; sums are fp32, slots in order, rounded once.  Outputs overlap no input
+ * (WQ_ERR_ARG where rows or tokens would). */
 
 /* positions from what wq_moe_route was given and gave: positions[sorted_pairs[r]] = r. */
 wq_status wq_moe_positions(const int32_t* topk_ids, int64_t t, int32_t topk, int32_t experts,

@@ -666,6 +666,14 @@ wq_status check_pairs(int64_t t, int32_t topk, int64_t hidden, const char* what)
   return WQ_OK;
 }
 
+// Whether arrays of na and nb elements of `type` share memory (a null one shares none).  Rows move
+// while others are still read, so no output of the dispatch may lie in an input.
+bool overlap(const void* a, int64_t na, const void* b, int64_t nb, int32_t type) {
+  const uint64_t size = type == WQ_TYPE_F32 ? 4 : 2;
+  const uint64_t pa = (uint64_t)(uintptr_t)a, pb = (uint64_t)(uintptr_t)b;
+  return a && b && pa < pb + (uint64_t)nb * size && pb < pa + (uint64_t)na * size;
+}
+
 wq::MxArgs mx_args(const wq_weight* w, const wq_weight* up, const uint8_t* codes, const uint8_t* scales,
                    int64_t rows, void* out) {
   wq::MxArgs a{};
@@ -789,6 +797,8 @@ wq_status wq_moe_permute(const void* x, int32_t type, int64_t t, int32_t topk, i
   if (!x || !positions || !rows) return fail(WQ_ERR_ARG, "wq_moe_permute: null pointer");
   if (!aligned16(x) || !aligned16(rows))
     return fail(WQ_ERR_ALIGN, "wq_moe_permute: x and rows must be 16-byte aligned");
+  if (overlap(x, t * hidden, rows, t * topk * hidden, type))
+    return fail(WQ_ERR_ARG, "wq_moe_permute: x and rows overlap");
   return hip_status(wq::launch_permute(x, type == WQ_TYPE_F32, t, topk, hidden, positions, rows,
                                        static_cast<hipStream_t>(stream)),
                     "wq_moe_permute launch");
@@ -804,6 +814,8 @@ wq_status wq_moe_unpermute(const void* rows, int32_t type, const int32_t* positi
   if (!rows || !positions || !y) return fail(WQ_ERR_ARG, "wq_moe_unpermute: null pointer");
   if (!aligned16(rows) || !aligned16(y))
     return fail(WQ_ERR_ALIGN, "wq_moe_unpermute: rows and y must be 16-byte aligned");
+  if (overlap(rows, t * topk * hidden, y, t * hidden, type))
+    return fail(WQ_ERR_ARG, "wq_moe_unpermute: rows and y overlap");
   return hip_status(wq::launch_unpermute(rows, type == WQ_TYPE_F32, positions, topk_weights, t, topk,
                                          hidden, y, static_cast<hipStream_t>(stream)),
                     "wq_moe_unpermute launch");
@@ -821,6 +833,9 @@ wq_status wq_moe_unpermute_grad(const void* dy, int32_t type, const void* rows,
     return fail(WQ_ERR_ARG, "wq_moe_unpermute_grad: null pointer");
   if (!aligned16(dy) || !aligned16(rows) || !aligned16(d_rows))
     return fail(WQ_ERR_ALIGN, "wq_moe_unpermute_grad: dy, rows and d_rows must be 16-byte aligned");
+  if (overlap(d_rows, t * topk * hidden, dy, t * hidden, type) ||
+      overlap(d_rows, t * topk * hidden, rows, t * topk * hidden, type))
+    return fail(WQ_ERR_ARG, "wq_moe_unpermute_grad: d_rows overlaps dy or rows");
   return hip_status(wq::launch_unpermute_grad(dy, rows, type == WQ_TYPE_F32, positions, topk_weights, t,
                                               topk, hidden, d_rows, d_weights,
                                               static_cast<hipStream_t>(stream)),
