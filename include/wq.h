@@ -311,9 +311,12 @@ wq_status wq_moe_positions(const int32_t* topk_ids, int64_t t, int32_t topk, int
                            const int32_t* expert_offsets, const int32_t* sorted_pairs,
                            int32_t* positions, void* stream);
 
-/* rows[positions[t][j]] = x[t]: x [t][hidden], rows [t*topk][hidden] of `type`; rows that no pair
- * has are left as they were.  Its gradient is wq_moe_unpermute without weights.  positions must
- * not hold a row twice. */
+/* Added to the type of wq_moe_permute and wq_moe_unpermute_grad: rows (d_rows) that no pair has are
+ * set to zero, the gradient of what no token reads; without it they are left as they were. */
+enum { WQ_CLEAR_ROWS = 0x100 };
+
+/* rows[positions[t][j]] = x[t]: x [t][hidden], rows [t*topk][hidden] of `type` (WQ_CLEAR_ROWS may be
+ * added).  Its gradient is wq_moe_unpermute without weights.  positions must not hold a row twice. */
 wq_status wq_moe_permute(const void* x, int32_t type, int64_t t, int32_t topk, int64_t hidden,
                          const int32_t* positions, void* rows, void* stream);
 
@@ -324,7 +327,7 @@ wq_status wq_moe_unpermute(const void* rows, int32_t type, const int32_t* positi
                            void* y, void* stream);
 
 /* Gradients of wq_moe_unpermute for dy [t][hidden]:
- *   d_rows[positions[t][j]] = topk_weights[t][j] * dy[t]      (rows of no pair left as they were)
+ *   d_rows[positions[t][j]] = topk_weights[t][j] * dy[t]      (rows of no pair: WQ_CLEAR_ROWS)
  *   d_weights[t][j] = <dy[t], rows[positions[t][j]]>           (0 for a dropped pair)
  * Either output may be NULL and is then not computed; rows may be NULL when d_weights is.
  * topk_weights NULL: every weight 1.  positions must not hold a row twice. */

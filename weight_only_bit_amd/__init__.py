@@ -33,6 +33,7 @@ FMT_INT4, FMT_INT2_AFFINE, FMT_CCQ2, FMT_CCQ432, FMT_CCQ_HYBRID, FMT_INT8 = 1, 2
 FMT_MXFP4 = 7
 
 TYPE_BF16, TYPE_F32 = 0, 1  # wq_type
+_CLEAR_ROWS = 0x100         # WQ_CLEAR_ROWS, for the arrays that a call allocates itself
 
 # Every symbol include/wq.h declares.
 EXPORTS = ("wq_dequantize", "wq_gemm", "wq_moe_workspace_bytes", "wq_moe_route_workspace_bytes",
@@ -610,8 +611,9 @@ def _positions(positions, what):
 
 
 def wq_moe_permute(x, positions, rows=None):
-    """rows [t*topk, hidden] in expert order: rows[positions[t, j]] = x[t] (bf16 or fp32).  Its
-    gradient is wq_moe_unpermute(d_rows, positions)."""
+    """rows [t*topk, hidden] in expert order: rows[positions[t, j]] = x[t] (bf16 or fp32).  Rows that
+    no pair has (dropped pairs leave some) are zeros; in a `rows` of the caller's they stay as they
+    were.  Its gradient is wq_moe_unpermute(d_rows, positions)."""
     t, topk = _positions(positions, "wq_moe_permute")
     vt, kind = _value_type(x, "wq_moe_permute x")
     if x.dim() != 2:
@@ -620,6 +622,7 @@ def wq_moe_permute(x, positions, rows=None):
     _need(x, "wq_moe_permute x", kind, shape=(t, hidden))
     if rows is None:
         rows = x.new_empty((t * topk, hidden))
+        vt |= _CLEAR_ROWS
     else:
         _need(rows, "wq_moe_permute rows", kind, shape=(t * topk, hidden))
     _check(lib().wq_moe_permute(_ptr(x), vt, t, topk, hidden, _ptr(positions), _ptr(rows), _stream()),
@@ -648,7 +651,8 @@ def wq_moe_unpermute(rows, positions, topk_weights=None, y=None):
 
 def wq_moe_unpermute_grad(dy, rows, positions, topk_weights=None, d_rows=None, d_weights=None):
     """(d_rows [t*topk, hidden], d_weights f32 [t, topk]) of wq_moe_unpermute for dy [t, hidden].
-    rows None: only d_rows is computed, and d_weights is None."""
+    Rows that no pair has get a gradient of zero; in a `d_rows` of the caller's they stay as they
+    were.  rows None: only d_rows is computed, and d_weights is None."""
     import torch
 
     t, topk = _positions(positions, "wq_moe_unpermute_grad")
@@ -661,6 +665,7 @@ def wq_moe_unpermute_grad(dy, rows, positions, topk_weights=None, d_rows=None, d
         _need(topk_weights, "wq_moe_unpermute_grad topk_weights", "f32", shape=(t, topk))
     if d_rows is None:
         d_rows = dy.new_empty((t * topk, hidden))
+        vt |= _CLEAR_ROWS
     else:
         _need(d_rows, "wq_moe_unpermute_grad d_rows", kind, shape=(t * topk, hidden))
     if rows is not None:

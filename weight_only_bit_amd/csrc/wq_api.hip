@@ -790,6 +790,8 @@ wq_status wq_moe_positions(const int32_t* topk_ids, int64_t t, int32_t topk, int
 
 wq_status wq_moe_permute(const void* x, int32_t type, int64_t t, int32_t topk, int64_t hidden,
                          const int32_t* positions, void* rows, void* stream) {
+  const int clear = type & WQ_CLEAR_ROWS;
+  type &= ~WQ_CLEAR_ROWS;
   wq_status st = check_type(type, "wq_moe_permute");
   if (st != WQ_OK) return st;
   if ((st = check_pairs(t, topk, hidden, "wq_moe_permute")) != WQ_OK) return st;
@@ -799,7 +801,7 @@ wq_status wq_moe_permute(const void* x, int32_t type, int64_t t, int32_t topk, i
     return fail(WQ_ERR_ALIGN, "wq_moe_permute: x and rows must be 16-byte aligned");
   if (overlap(x, t * hidden, rows, t * topk * hidden, type))
     return fail(WQ_ERR_ARG, "wq_moe_permute: x and rows overlap");
-  return hip_status(wq::launch_permute(x, type == WQ_TYPE_F32, t, topk, hidden, positions, rows,
+  return hip_status(wq::launch_permute(x, type == WQ_TYPE_F32, t, topk, hidden, positions, rows, clear,
                                        static_cast<hipStream_t>(stream)),
                     "wq_moe_permute launch");
 }
@@ -825,6 +827,8 @@ wq_status wq_moe_unpermute_grad(const void* dy, int32_t type, const void* rows,
                                 const int32_t* positions, const float* topk_weights, int64_t t,
                                 int32_t topk, int64_t hidden, void* d_rows, float* d_weights,
                                 void* stream) {
+  const int clear = type & WQ_CLEAR_ROWS;
+  type &= ~WQ_CLEAR_ROWS;
   wq_status st = check_type(type, "wq_moe_unpermute_grad");
   if (st != WQ_OK) return st;
   if ((st = check_pairs(t, topk, hidden, "wq_moe_unpermute_grad")) != WQ_OK) return st;
@@ -837,7 +841,7 @@ wq_status wq_moe_unpermute_grad(const void* dy, int32_t type, const void* rows,
       overlap(d_rows, t * topk * hidden, rows, t * topk * hidden, type))
     return fail(WQ_ERR_ARG, "wq_moe_unpermute_grad: d_rows overlaps dy or rows");
   return hip_status(wq::launch_unpermute_grad(dy, rows, type == WQ_TYPE_F32, positions, topk_weights, t,
-                                              topk, hidden, d_rows, d_weights,
+                                              topk, hidden, d_rows, d_weights, clear,
                                               static_cast<hipStream_t>(stream)),
                     "wq_moe_unpermute_grad launch");
 }

@@ -96,12 +96,80 @@ __device__ __forceinline__ Item item(int64_t first, int64_t t, int64_t hidden) {
   return r;
 }
 
+// Rows that no pair has become zero: workgroup c of a launch's first W = 2^log2_wgs takes the rows c,
+// c + W, c + 2 W, ... (dropped pairs leave the last ones, which so fall to all of them).  It reads all
+// positions, marks its rows in LDS, and writes those without a mark: no scratch, no order among the
+// workgroups, and where nothing was dropped only the reads, beside the other workgroups' copies.
+constexpr int kClearRows = 65536;  // of one workgroup at most
+struct Clear {
+  int32_t wgs, log2_wgs;  // wgs 0: nothing to do
+};
+struct __attribute__((packed, aligned(4))) Positions4 {
+  int32_t v[4];
+};
+template <typename T>
+__device__ __forceinline__ void clear_rows(const int32_t* __restrict__ positions, int64_t npairs,
+                                           int64_t hidden, T* __restrict__ out, uint32_t wg, Clear clear) {
+  constexpr int E = 16 / (int)sizeof(T);
+  __shared__ uint32_t used[kClearRows / 32];
+  const int tid = threadIdx.x;
+  const uint32_t n = ((uint32_t)npairs - wg + (uint32_t)clear.wgs - 1) >> clear.log2_wgs;  // rows, wg < npairs
+  for (uint32_t i = tid; i < (n + 31) / 32; i += 256) used[i] = 0;
+  __syncthreads();
+  auto mark = [&](int32_t p) __attribute__((always_inline)) {
+    const uint32_t i = (uint32_t)p >> clear.log2_wgs;
+    if (((uint32_t)p & (uint32_t)(clear.wgs - 1)) == wg && i < n) atomicOr(&used[i >> 5], 1u << (i & 31));
+  };
+  const int64_t quads = npairs / 4;
+  constexpr int U = 8;  // loads of a thread before the first use
+  for (int64_t i0 = tid; i0 < quads; i0 += 256 * U) {
+    Positions4 v[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t i = i0 + 256 * u;
+      v[u] = reinterpret_cast<const Positions4*>(positions)[i < quads ? i : i0];
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) mark(v[u].v[j]);
+  }
+  if (tid < (int)(npairs & 3)) mark(positions[4 * quads + tid]);
+  __syncthreads();
+  const int lane = tid & 63;
+  const uint32_t mine = 0x11111111u << __builtin_amdgcn_readfirstlane(tid >> 6);  // a wave's of 32 rows
+  for (uint32_t b = 0; b < n; b += 32) {
+    uint32_t free = ~used[b >> 5] & mine;
+    if (n - b < 32) free &= (1u << (n - b)) - 1u;
+    for (; free; free &= free - 1) {
+      const int64_t r = ((int64_t)(b + __builtin_ctz(free)) << clear.log2_wgs) + wg;
+      T* const row = out + r * hidden;
+      for (int64_t c = (int64_t)lane * E; c + E <= hidden; c += 64 * E)
+        store_piece(row + c, (u32x4){0, 0, 0, 0});
+      const int64_t c = hidden / E * E + lane;
+      if (c < hidden) row[c] = T(0);
+    }
+  }
+}
+
+// Zeros in `pieces` pieces of 16 bytes and then `rest` 2-byte units.
+__global__ __launch_bounds__(256) void fill_kernel(u32x4* __restrict__ out, int64_t pieces, int32_t rest,
+                                                   int64_t first) {
+  const int64_t i = (first + blockIdx.x) * 256 + threadIdx.x;
+  if (i < pieces) out[i] = (u32x4){0, 0, 0, 0};
+  else if (i < pieces + rest) reinterpret_cast<uint16_t*>(out + pieces)[i - pieces] = 0;
+}
+
 template <typename T>
 __global__ __launch_bounds__(256) void permute_kernel(const T* __restrict__ x, int64_t t, int32_t topk,
                                                       int64_t hidden, const int32_t* __restrict__ positions,
-                                                      T* __restrict__ rows, int64_t first) {
+                                                      T* __restrict__ rows, Clear clear, int64_t first) {
   constexpr int E = 16 / (int)sizeof(T);
-  const Item it = item<E>(first, t, hidden);
+  if (first + blockIdx.x < clear.wgs) {  // all of them in the first launch
+    clear_rows(positions, t * topk, hidden, rows, blockIdx.x, clear);
+    return;
+  }
+  const Item it = item<E>(first - clear.wgs, t, hidden);
   if (it.token >= t) return;
   const int64_t npairs = t * topk;
   const int32_t* pos = positions + it.token * topk;
@@ -182,10 +250,16 @@ __global__ __launch_bounds__(256) void unpermute_grad_kernel(const T* __restrict
                                                              const float* __restrict__ weights,
                                                              int64_t npairs, int32_t topk, int64_t hidden,
                                                              T* __restrict__ d_rows,
-                                                             float* __restrict__ d_weights, int64_t first) {
+                                                             float* __restrict__ d_weights, Clear clear,
+                                                             int64_t first) {
   constexpr int E = 16 / (int)sizeof(T);
   const int lane = threadIdx.x & 63;
-  const int64_t p = (first + blockIdx.x) * 4 + __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const int64_t wg = first + blockIdx.x - clear.wgs;
+  if (wg < 0) {  // all of them in the first launch
+    clear_rows(positions, npairs, hidden, d_rows, blockIdx.x, clear);
+    return;
+  }
+  const int64_t p = wg * 4 + __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   if (p >= npairs) return;
   const int64_t r = positions[p];
   if (r < 0 || r >= npairs) {
@@ -249,6 +323,33 @@ int64_t row_wgs(int64_t t, int64_t hidden, int E) {
   return (t * slices * kLanes + 255) / 256;
 }
 
+// How rows that no pair has become zero: by a launch's first workgroups, or by a fill before the launch
+// (wgs 0).  8 rows a workgroup spread the writes of a small call; many pairs take fewer workgroups, for
+// each reads all of the positions, 0.2 ns a pair beside the copies.  So the fill serves rows below `fill`
+// bytes of 32768 pairs or more (us beyond the permutation's own, first workgroups and fill: 32768 pairs
+// of 256 bytes 3.3 to 4.4 and 4.1 to 4.3, of 2 KiB 0.8 to 2.1 and 10.2; 262144 of 1 KiB 29 to 55 and 32
+// to 38; 16384 of 128 bytes 1.2 to 1.5 and 1.9 to 2.0), and rows that are fewer bytes than all those
+// reads once marks for 65536 rows ask for more workgroups.  The gradient takes longer a pair and hides
+// the reads at every length (262144 pairs of 256 bytes: 2 to 7 and 10).
+template <typename T>
+hipError_t plan_clear(T* rows, int64_t npairs, int64_t hidden, int64_t fill, Clear* c, hipStream_t s) {
+  int log2_wgs = 8;
+  while (log2_wgs > 0 && npairs < (8ll << log2_wgs)) --log2_wgs;
+  while (log2_wgs > 6 && npairs << log2_wgs > 1ll << 23) --log2_wgs;
+  while ((int64_t)kClearRows << log2_wgs < npairs) {
+    ++log2_wgs;
+    if (fill < 4ll << log2_wgs) fill = 4ll << log2_wgs;
+  }
+  *c = Clear{1 << log2_wgs, log2_wgs};
+  if (npairs < 32768 || hidden * (int64_t)sizeof(T) >= fill) return hipSuccess;
+  *c = Clear{0, 0};
+  const int64_t units = npairs * hidden * (int64_t)sizeof(T) / 2, pieces = units / 8;
+  return launch_in_parts((pieces + units % 8 + 255) / 256, [&](int64_t first, dim3 grid) {
+    hipLaunchKernelGGL(fill_kernel, grid, dim3(256), 0, s, reinterpret_cast<u32x4*>(rows), pieces,
+                       (int32_t)(units % 8), first);
+  });
+}
+
 }  // namespace
 
 hipError_t launch_positions(const int32_t* ids, int64_t npairs, int32_t experts, const int32_t* offsets,
@@ -260,18 +361,24 @@ hipError_t launch_positions(const int32_t* ids, int64_t npairs, int32_t experts,
 
 template <typename T>
 static hipError_t permute_t(const T* x, int64_t t, int32_t topk, int64_t hidden, const int32_t* positions,
-                            T* rows, hipStream_t s) {
+                            T* rows, int clear, hipStream_t s) {
   constexpr int E = 16 / (int)sizeof(T);
-  return launch_in_parts(row_wgs(t, hidden, E), [&](int64_t first, dim3 grid) {
-    hipLaunchKernelGGL(permute_kernel<T>, grid, dim3(256), 0, s, x, t, topk, hidden, positions, rows, first);
+  Clear c{0, 0};
+  if (clear) {
+    const hipError_t e = plan_clear(rows, t * topk, hidden, 1024, &c, s);
+    if (e != hipSuccess) return e;
+  }
+  return launch_in_parts(c.wgs + row_wgs(t, hidden, E), [&](int64_t first, dim3 grid) {
+    hipLaunchKernelGGL(permute_kernel<T>, grid, dim3(256), 0, s, x, t, topk, hidden, positions, rows, c, first);
   });
 }
 
 hipError_t launch_permute(const void* x, int f32, int64_t t, int32_t topk, int64_t hidden,
-                          const int32_t* positions, void* rows, hipStream_t stream) {
-  return f32 ? permute_t(static_cast<const float*>(x), t, topk, hidden, positions, static_cast<float*>(rows), stream)
+                          const int32_t* positions, void* rows, int clear, hipStream_t stream) {
+  return f32 ? permute_t(static_cast<const float*>(x), t, topk, hidden, positions, static_cast<float*>(rows),
+                         clear, stream)
              : permute_t(static_cast<const uint16_t*>(x), t, topk, hidden, positions,
-                         static_cast<uint16_t*>(rows), stream);
+                         static_cast<uint16_t*>(rows), clear, stream);
 }
 
 template <typename T>
@@ -291,20 +398,30 @@ hipError_t launch_unpermute(const void* rows, int f32, const int32_t* positions,
                            static_cast<uint16_t*>(y), stream);
 }
 
+template <typename T>
+static hipError_t unpermute_grad_t(const T* dy, const T* rows, const int32_t* positions, const float* weights,
+                                   int64_t t, int32_t topk, int64_t hidden, T* d_rows, float* d_weights,
+                                   int clear, hipStream_t s) {
+  const int64_t npairs = t * topk;
+  Clear c{0, 0};
+  if (clear && d_rows) {
+    const hipError_t e = plan_clear(d_rows, npairs, hidden, 0, &c, s);
+    if (e != hipSuccess) return e;
+  }
+  return launch_in_parts(c.wgs + (npairs + 3) / 4, [&](int64_t first, dim3 grid) {
+    hipLaunchKernelGGL(unpermute_grad_kernel<T>, grid, dim3(256), 0, s, dy, rows, positions, weights, npairs,
+                       topk, hidden, d_rows, d_weights, c, first);
+  });
+}
+
 hipError_t launch_unpermute_grad(const void* dy, const void* rows, int f32, const int32_t* positions,
                                  const float* weights, int64_t t, int32_t topk, int64_t hidden,
-                                 void* d_rows, float* d_weights, hipStream_t stream) {
-  const int64_t npairs = t * topk;
-  return launch_in_parts((npairs + 3) / 4, [&](int64_t first, dim3 grid) {
-    if (f32)
-      hipLaunchKernelGGL(unpermute_grad_kernel<float>, grid, dim3(256), 0, stream,
-                         static_cast<const float*>(dy), static_cast<const float*>(rows), positions, weights,
-                         npairs, topk, hidden, static_cast<float*>(d_rows), d_weights, first);
-    else
-      hipLaunchKernelGGL(unpermute_grad_kernel<uint16_t>, grid, dim3(256), 0, stream,
-                         static_cast<const uint16_t*>(dy), static_cast<const uint16_t*>(rows), positions,
-                         weights, npairs, topk, hidden, static_cast<uint16_t*>(d_rows), d_weights, first);
-  });
+                                 void* d_rows, float* d_weights, int clear, hipStream_t stream) {
+  return f32 ? unpermute_grad_t(static_cast<const float*>(dy), static_cast<const float*>(rows), positions,
+                                weights, t, topk, hidden, static_cast<float*>(d_rows), d_weights, clear, stream)
+             : unpermute_grad_t(static_cast<const uint16_t*>(dy), static_cast<const uint16_t*>(rows), positions,
+                                weights, t, topk, hidden, static_cast<uint16_t*>(d_rows), d_weights, clear,
+                                stream);
 }
 
 }  // namespace wq

@@ -127,16 +127,16 @@ struct MxArgs {
 };
 hipError_t launch_mx_product(int mode, const MxArgs& args, int64_t experts, hipStream_t stream);
 
-// Token dispatch (rows bf16, or fp32 where f32 is set).
+// Token dispatch (rows bf16, or fp32 where f32 is set; clear: rows that no pair has become zero).
 hipError_t launch_positions(const int32_t* ids, int64_t npairs, int32_t experts, const int32_t* offsets,
                             const int32_t* sorted_pairs, int32_t* positions, hipStream_t stream);
 hipError_t launch_permute(const void* x, int f32, int64_t t, int32_t topk, int64_t hidden,
-                          const int32_t* positions, void* rows, hipStream_t stream);
+                          const int32_t* positions, void* rows, int clear, hipStream_t stream);
 hipError_t launch_unpermute(const void* rows, int f32, const int32_t* positions, const float* weights,
                             int64_t t, int32_t topk, int64_t hidden, void* y, hipStream_t stream);
 hipError_t launch_unpermute_grad(const void* dy, const void* rows, int f32, const int32_t* positions,
                                  const float* weights, int64_t t, int32_t topk, int64_t hidden,
-                                 void* d_rows, float* d_weights, hipStream_t stream);
+                                 void* d_rows, float* d_weights, int clear, hipStream_t stream);
 
 // Rows of one tile of the tiled kernel.
 int tiled_rows();
