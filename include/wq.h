@@ -266,7 +266,8 @@ wq_status wq_quantize_ccq(const float* w, int64_t n, int64_t k, int32_t zp, int3
 /* ---- Microscaled 4-bit floating point (MXFP4) -----------------------------------------------
  * WQ_FMT_MXFP4 weights are taken by every call above with bf16 activations.  The calls below
  * quantise, and multiply MXFP4 activations with MXFP4 weights: every product of two codes is
- * exact, each pair of blocks' sum is scaled by both blocks' scales, and the sums are fp32. */
+ * exact, each pair of blocks' sum is scaled by both blocks' scales, and the sums are fp32.  Outputs
+ * overlap no input and no other output (WQ_ERR_ARG). */
 
 /* n rows of k values (x_type; device) to MXFP4: codes u8[n][k/2], scales u8[n][k/32].  Per block
  * of 32 with largest magnitude a:
@@ -304,7 +305,7 @@ wq_status wq_moe_down_mx(const uint8_t* h_codes, const uint8_t* h_scales, int64_
  * of every pair p = t*topk + j in expert order, -1 for a dropped pair (id outside [0, experts)):
  * a dropped pair contributes nothing, and nothing is written for it.  Rows, tokens and their
  * gradients are of one type; sums are fp32, slots in order, rounded once.  Outputs overlap no input
- * (WQ_ERR_ARG where rows or tokens would). */
+ * and no other output (WQ_ERR_ARG). */
 
 /* positions from what wq_moe_route was given and gave: positions[sorted_pairs[r]] = r. */
 wq_status wq_moe_positions(const int32_t* topk_ids, int64_t t, int32_t topk, int32_t experts,

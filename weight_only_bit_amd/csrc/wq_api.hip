@@ -7,6 +7,7 @@
 #include <cstdint>
 #include <cstdio>
 #include <cstring>
+#include <initializer_list>
 #include <string>
 
 #include "../../include/wq.h"
@@ -666,13 +667,28 @@ wq_status check_pairs(int64_t t, int32_t topk, int64_t hidden, const char* what)
   return WQ_OK;
 }
 
-// Whether arrays of na and nb elements of `type` share memory (a null one shares none).  Rows move
-// while others are still read, so no output of the dispatch may lie in an input.
-bool overlap(const void* a, int64_t na, const void* b, int64_t nb, int32_t type) {
-  const uint64_t size = type == WQ_TYPE_F32 ? 4 : 2;
-  const uint64_t pa = (uint64_t)(uintptr_t)a, pb = (uint64_t)(uintptr_t)b;
-  return a && b && pa < pb + (uint64_t)nb * size && pb < pa + (uint64_t)na * size;
+// An array that a call reads or writes.
+struct Span {
+  const void* p;
+  uint64_t bytes;
+  Span(const void* at, int64_t count, int size) : p(at), bytes((uint64_t)count * (uint64_t)size) {}
+};
+int type_size(int32_t type) { return type == WQ_TYPE_F32 ? 4 : 2; }
+
+// Whether `out` shares memory with one of the others (a null one shares none).  Workgroups write while
+// others still read, so no output of the calls below may lie in an input or in another output.
+bool overlaps(const Span& out, std::initializer_list<Span> others) {
+  const uint64_t a = (uint64_t)(uintptr_t)out.p;
+  for (const Span& o : others) {
+    const uint64_t b = (uint64_t)(uintptr_t)o.p;
+    if (a && b && a < b + o.bytes && b < a + out.bytes) return true;
+  }
+  return false;
 }
+
+// The arrays of an MXFP4 weight (checked: one expert's codes lie below 2^31 bytes).
+Span mx_codes(const wq_weight* w) { return Span(w->codes, w->experts * w->n * (w->k / 2), 1); }
+Span mx_scales(const wq_weight* w) { return Span(w->qscale, w->experts * w->n * (w->k / 32), 1); }
 
 wq::MxArgs mx_args(const wq_weight* w, const wq_weight* up, const uint8_t* codes, const uint8_t* scales,
                    int64_t rows, void* out) {
@@ -708,6 +724,9 @@ wq_status wq_quantize_mx(const void* x, int32_t x_type, int64_t n, int64_t k, ui
   if (!x || !codes || !scales) return fail(WQ_ERR_ARG, "wq_quantize_mx: null pointer");
   if (!aligned16(x) || !aligned16(codes) || !aligned16(scales))
     return fail(WQ_ERR_ALIGN, "wq_quantize_mx: x, codes and scales must be 16-byte aligned");
+  const Span in(x, n * k, type_size(x_type)), sc(scales, n * (k / 32), 1);
+  if (overlaps(Span(codes, n * (k / 2), 1), {in, sc}) || overlaps(sc, {in}))
+    return fail(WQ_ERR_ARG, "wq_quantize_mx: codes or scales overlap x or each other");
   return hip_status(wq::launch_mx_quantize(x, x_type == WQ_TYPE_F32, n, k, codes, scales,
                                            static_cast<hipStream_t>(stream)),
                     "wq_quantize_mx launch");
@@ -725,6 +744,9 @@ wq_status wq_gemm_mx(const uint8_t* x_codes, const uint8_t* x_scales, int64_t m,
   if (!aligned16(x_codes) || !aligned16(x_scales) || !aligned16(y))
     return fail(WQ_ERR_ALIGN, "wq_gemm_mx: x or y not 16-byte aligned");
   if (m > (1ll << 31)) return fail(WQ_ERR_UNSUPPORTED, "wq_gemm_mx: m must not exceed 2^31");
+  if (overlaps(Span(y, m * w->n, type_size(y_type)),
+               {Span(x_codes, m * (w->k / 2), 1), Span(x_scales, m * (w->k / 32), 1), mx_codes(w), mx_scales(w)}))
+    return fail(WQ_ERR_ARG, "wq_gemm_mx: y overlaps x or the weight");
   wq::MxArgs a = mx_args(w, w, x_codes, x_scales, m, y);
   a.out_f32 = y_type == WQ_TYPE_F32;
   return hip_status(wq::launch_mx_product(wq::MODE_DENSE, a, 1, static_cast<hipStream_t>(stream)),
@@ -745,6 +767,11 @@ wq_status wq_moe_gate_up_mx(const uint8_t* x_codes, const uint8_t* x_scales, int
     return fail(WQ_ERR_ARG, "wq_moe_gate_up_mx: null pointer");
   if (!aligned16(x_codes) || !aligned16(x_scales) || !aligned16(h))
     return fail(WQ_ERR_ALIGN, "wq_moe_gate_up_mx: x and h must be 16-byte aligned");
+  if (overlaps(Span(h, t * topk * gate->n, 2),
+               {Span(x_codes, t * (gate->k / 2), 1), Span(x_scales, t * (gate->k / 32), 1), mx_codes(gate),
+                mx_scales(gate), mx_codes(up), mx_scales(up), Span(expert_offsets, gate->experts + 1, 4),
+                Span(sorted_pairs, t * topk, 4)}))
+    return fail(WQ_ERR_ARG, "wq_moe_gate_up_mx: h overlaps an input");
   wq::MxArgs a = mx_args(gate, up, x_codes, x_scales, t * topk, h);
   a.offsets = expert_offsets;
   a.sorted_pairs = sorted_pairs;
@@ -766,6 +793,10 @@ wq_status wq_moe_down_mx(const uint8_t* h_codes, const uint8_t* h_scales, int64_
   if (!h_codes || !h_scales || !expert_offsets || !d) return fail(WQ_ERR_ARG, "wq_moe_down_mx: null pointer");
   if (!aligned16(h_codes) || !aligned16(h_scales) || !aligned16(d))
     return fail(WQ_ERR_ALIGN, "wq_moe_down_mx: h and d must be 16-byte aligned");
+  if (overlaps(Span(d, npairs * down->n, type_size(d_type)),
+               {Span(h_codes, npairs * (down->k / 2), 1), Span(h_scales, npairs * (down->k / 32), 1),
+                mx_codes(down), mx_scales(down), Span(expert_offsets, down->experts + 1, 4)}))
+    return fail(WQ_ERR_ARG, "wq_moe_down_mx: d overlaps an input");
   wq::MxArgs a = mx_args(down, down, h_codes, h_scales, npairs, d);
   a.offsets = expert_offsets;
   a.out_f32 = d_type == WQ_TYPE_F32;
@@ -783,6 +814,9 @@ wq_status wq_moe_positions(const int32_t* topk_ids, int64_t t, int32_t topk, int
   if (t == 0) return WQ_OK;
   if (!topk_ids || !expert_offsets || !sorted_pairs || !positions)
     return fail(WQ_ERR_ARG, "wq_moe_positions: null pointer");
+  if (overlaps(Span(positions, t * topk, 4), {Span(topk_ids, t * topk, 4), Span(expert_offsets, experts + 1, 4),
+                                              Span(sorted_pairs, t * topk, 4)}))
+    return fail(WQ_ERR_ARG, "wq_moe_positions: positions overlaps an input");
   return hip_status(wq::launch_positions(topk_ids, t * topk, experts, expert_offsets, sorted_pairs,
                                          positions, static_cast<hipStream_t>(stream)),
                     "wq_moe_positions launch");
@@ -799,8 +833,9 @@ wq_status wq_moe_permute(const void* x, int32_t type, int64_t t, int32_t topk, i
   if (!x || !positions || !rows) return fail(WQ_ERR_ARG, "wq_moe_permute: null pointer");
   if (!aligned16(x) || !aligned16(rows))
     return fail(WQ_ERR_ALIGN, "wq_moe_permute: x and rows must be 16-byte aligned");
-  if (overlap(x, t * hidden, rows, t * topk * hidden, type))
-    return fail(WQ_ERR_ARG, "wq_moe_permute: x and rows overlap");
+  if (overlaps(Span(rows, t * topk * hidden, type_size(type)),
+               {Span(x, t * hidden, type_size(type)), Span(positions, t * topk, 4)}))
+    return fail(WQ_ERR_ARG, "wq_moe_permute: rows overlaps x or positions");
   return hip_status(wq::launch_permute(x, type == WQ_TYPE_F32, t, topk, hidden, positions, rows, clear,
                                        static_cast<hipStream_t>(stream)),
                     "wq_moe_permute launch");
@@ -816,8 +851,10 @@ wq_status wq_moe_unpermute(const void* rows, int32_t type, const int32_t* positi
   if (!rows || !positions || !y) return fail(WQ_ERR_ARG, "wq_moe_unpermute: null pointer");
   if (!aligned16(rows) || !aligned16(y))
     return fail(WQ_ERR_ALIGN, "wq_moe_unpermute: rows and y must be 16-byte aligned");
-  if (overlap(rows, t * topk * hidden, y, t * hidden, type))
-    return fail(WQ_ERR_ARG, "wq_moe_unpermute: rows and y overlap");
+  if (overlaps(Span(y, t * hidden, type_size(type)),
+               {Span(rows, t * topk * hidden, type_size(type)), Span(positions, t * topk, 4),
+                Span(topk_weights, t * topk, 4)}))
+    return fail(WQ_ERR_ARG, "wq_moe_unpermute: y overlaps rows, positions or topk_weights");
   return hip_status(wq::launch_unpermute(rows, type == WQ_TYPE_F32, positions, topk_weights, t, topk,
                                          hidden, y, static_cast<hipStream_t>(stream)),
                     "wq_moe_unpermute launch");
@@ -837,9 +874,11 @@ wq_status wq_moe_unpermute_grad(const void* dy, int32_t type, const void* rows,
     return fail(WQ_ERR_ARG, "wq_moe_unpermute_grad: null pointer");
   if (!aligned16(dy) || !aligned16(rows) || !aligned16(d_rows))
     return fail(WQ_ERR_ALIGN, "wq_moe_unpermute_grad: dy, rows and d_rows must be 16-byte aligned");
-  if (overlap(d_rows, t * topk * hidden, dy, t * hidden, type) ||
-      overlap(d_rows, t * topk * hidden, rows, t * topk * hidden, type))
-    return fail(WQ_ERR_ARG, "wq_moe_unpermute_grad: d_rows overlaps dy or rows");
+  const Span g(dy, t * hidden, type_size(type)), in(rows, t * topk * hidden, type_size(type));
+  const Span pos(positions, t * topk, 4), w(topk_weights, t * topk, 4), dw(d_weights, t * topk, 4);
+  if (overlaps(Span(d_rows, t * topk * hidden, type_size(type)), {g, in, pos, w, dw}) ||
+      overlaps(dw, {g, in, pos, w}))
+    return fail(WQ_ERR_ARG, "wq_moe_unpermute_grad: d_rows or d_weights overlaps an input or the other");
   return hip_status(wq::launch_unpermute_grad(dy, rows, type == WQ_TYPE_F32, positions, topk_weights, t,
                                               topk, hidden, d_rows, d_weights, clear,
                                               static_cast<hipStream_t>(stream)),
