@@ -11,6 +11,7 @@
 #include <type_traits>
 
 #include "wq_kernels.hpp"
+#include "wq_mx_select.hpp"
 
 namespace wq {
 namespace {
@@ -846,8 +847,6 @@ hipError_t launch_mx_quantize(const void* x, int f32, int64_t n, int64_t k, uint
 
 namespace {
 
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
-
 // Dense products: rows in passes of 16 MT; the grid's z extent is 16 bits, so more rows take further
 // launches.
 template <int MT>
@@ -859,59 +858,33 @@ hipError_t stream_dense(const MxArgs& a, hipStream_t stream) {
     b.x_scales = a.x_scales + r0 * (a.K / 32);
     b.out = static_cast<uint8_t*>(a.out) + r0 * a.out_stride * (a.out_f32 ? 4 : 2);
     b.M = a.M - r0 < chunk ? a.M - r0 : chunk;
-    const hipError_t e = launch_stream<MODE_DENSE, MT, 4>(b, 1, ceil_div(b.M, 16 * MT), stream);
+    const hipError_t e = launch_stream<MODE_DENSE, MT, 4>(b, 1, mx_ceil_div(b.M, 16 * MT), stream);
     if (e != hipSuccess) return e;
   }
   return hipSuccess;
 }
 
-// The tiles' 32-bit ranges: one expert's codes, a tile's rows (k below 2^23) and, gathered, all tokens'
-// codes, each below 2^31 less a stage's bytes.  A stage needs 256 columns.
-bool tiles_fit(int mode, const MxArgs& a) {
-  constexpr int64_t most = (1ll << 31) - 1024;
-  if (a.K < 256 || a.K >= (1ll << 23) || a.N * (a.K / 2) > most) return false;
-  return mode != MODE_GATEUP || a.M / a.topk * (a.K / 2) <= most;
-}
-
-// Which kernel, by what was measured on both sides of each border (us, in a graph):
-//   256 x 256 tiles, one workgroup per CU, for long k; 128 x 256 with one buffer, two per CU, whose
-//   neighbour covers a tile's start and end, for short k:
-//     4096 x 8192, k 8192: 145 and 170;  8192 x 8192, k 1024: 77 and 58
-//   128 x 128 where 128 x 256 would leave CUs without a tile: 3000 x 2048, k 1024: 10.5 and 11.7
-//   64 x 64 where 128 x 128 would: 128 x 4096, k 4096: 10.4 and 13.8
-//   streaming where few workgroups of 32 x 16 suffice: 48 x 4096, k 4096: 8.9 against 10
 hipError_t product_dense(const MxArgs& a, hipStream_t stream) {
-  const auto tiles = [&](int64_t bm, int64_t bn) { return ceil_div(a.M, bm) * ceil_div(a.N, bn); };
-  if (a.M > 32 && tiles_fit(MODE_DENSE, a)) {
-    if (tiles(256, 256) >= 192 && a.K > 2048) return launch_tiles<MODE_DENSE, 4, 4, 2>(a, 1, stream);
-    if (tiles(128, 256) >= 512) return launch_tiles<MODE_DENSE, 2, 4, 1>(a, 1, stream);
-    if (tiles(128, 256) >= 192) return launch_tiles<MODE_DENSE, 2, 4, 2>(a, 1, stream);
-    if (tiles(128, 128) >= 128) return launch_tiles<MODE_DENSE, 2, 2, 2>(a, 1, stream);
-    if (tiles(32, 16) >= 850) return launch_tiles<MODE_DENSE, 1, 1, 2>(a, 1, stream);
+  switch (mx_dense_kernel(a.M, a.N, a.K)) {
+    case MX_TILES_256: return launch_tiles<MODE_DENSE, 4, 4, 2>(a, 1, stream);
+    case MX_TILES_128x256_ONE: return launch_tiles<MODE_DENSE, 2, 4, 1>(a, 1, stream);
+    case MX_TILES_128x256: return launch_tiles<MODE_DENSE, 2, 4, 2>(a, 1, stream);
+    case MX_TILES_128: return launch_tiles<MODE_DENSE, 2, 2, 2>(a, 1, stream);
+    case MX_TILES_64: return launch_tiles<MODE_DENSE, 1, 1, 2>(a, 1, stream);
+    case MX_STREAM_32: return stream_dense<2>(a, stream);
+    default: return stream_dense<1>(a, stream);
   }
-  // 16 rows a workgroup where 32 would leave CUs without one: 64 x 1024, k 8192: 7.3 against 9.8
-  return a.M > 16 && tiles(32, 16) >= 256 ? stream_dense<2>(a, stream) : stream_dense<1>(a, stream);
 }
 
-// The same for experts, by the rows that an expert has on average (gate+up / down, 64 experts,
-// hidden 8192, inter 3584 unless said otherwise):
-//   streaming for few: 2 rows: 319 / 181 against 363 / 188 in tiles; 4 rows: 368 / 217 against
-//   339 / 195; with few tiles for more rows: 8 experts, 1024 x 1024, 16 rows: 4.6 against 5.9
-//   128 x 256 tiles (64 rows where an expert has no more) up to 128 rows: 64 rows: 490 against 503
-//   256 x 256 for long k: 512 rows: 1311 against 1545;  128 x 256 with one buffer for short k (16
-//   experts, 250 rows, 1000 x 2048: 23.2 against 27.1 with two)
 template <int MODE>
 hipError_t product_experts(const MxArgs& a, int64_t experts, hipStream_t stream) {
-  const int64_t active = a.M < experts ? a.M : experts;  // at most
-  const double rows = (double)a.M / (double)experts;
-  const int64_t cols = ceil_div(MODE == MODE_GATEUP ? 2 * a.N : a.N, 256);
-  if (!tiles_fit(MODE, a) || rows < 3.0) return launch_stream<MODE, 1, 4>(a, experts, 1, stream);
-  if ((a.M / 128 + active) * cols < 128)
-    return rows <= 32.0 ? launch_stream<MODE, 1, 4>(a, experts, 1, stream)
-                        : launch_tiles<MODE, 2, 2, 2>(a, experts, stream);
-  if (rows < 128.0) return launch_tiles<MODE, 2, 4, 2>(a, experts, stream);
-  if (a.K <= 2048 || (a.M / 256 + active) * cols < 512) return launch_tiles<MODE, 2, 4, 1>(a, experts, stream);
-  return launch_tiles<MODE, 4, 4, 2>(a, experts, stream);
+  switch (mx_experts_kernel(MODE == MODE_GATEUP ? a.M / a.topk : 0, a.M, a.N, a.K, experts)) {
+    case MX_TILES_256: return launch_tiles<MODE, 4, 4, 2>(a, experts, stream);
+    case MX_TILES_128x256_ONE: return launch_tiles<MODE, 2, 4, 1>(a, experts, stream);
+    case MX_TILES_128x256: return launch_tiles<MODE, 2, 4, 2>(a, experts, stream);
+    case MX_TILES_128: return launch_tiles<MODE, 2, 2, 2>(a, experts, stream);
+    default: return launch_stream<MODE, 1, 4>(a, experts, 1, stream);
+  }
 }
 
 }  // namespace

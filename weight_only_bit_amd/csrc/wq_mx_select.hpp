@@ -1,0 +1,69 @@
+// wq_mx_select.hpp -- which kernel of wq_mx.hip a product of two MXFP4 operands takes.  Plain host C++: the
+// rules hold no device code, so their borders can be looked at without a GPU.
+#pragma once
+
+#include <cstdint>
+
+namespace wq {
+
+// Rows x columns of a workgroup's outputs.
+enum MxKernel : int32_t {
+  MX_STREAM_16 = 0,  // 16 x 16, weights straight from memory
+  MX_STREAM_32,      // 32 x 16
+  MX_TILES_64,       // 64 x 64, two buffers
+  MX_TILES_128,      // 128 x 128, two buffers
+  MX_TILES_128x256,  // two buffers
+  MX_TILES_128x256_ONE,  // one buffer, two workgroups per CU
+  MX_TILES_256       // 256 x 256, two buffers
+};
+
+inline int64_t mx_ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// The tiles' 32-bit ranges: one expert's codes, a tile's rows (k below 2^23) and, gathered, the codes of
+// `gathered` tokens (0: rows are not gathered), each below 2^31 less a stage's bytes.  A stage needs 256
+// columns.
+inline bool mx_tiles_fit(int64_t gathered, int64_t N, int64_t K) {
+  constexpr int64_t most = (1ll << 31) - 1024;
+  if (K < 256 || K >= (1ll << 23) || N * (K / 2) > most) return false;
+  return gathered * (K / 2) <= most;
+}
+
+// By what was measured on both sides of each border (us, in a graph):
+//   256 x 256 tiles, one workgroup per CU, for long k; 128 x 256 with one buffer, two per CU, whose
+//   neighbour covers a tile's start and end, for short k:
+//     4096 x 8192, k 8192: 145 and 170;  8192 x 8192, k 1024: 77 and 58
+//   128 x 128 where 128 x 256 would leave CUs without a tile: 3000 x 2048, k 1024: 10.5 and 11.7
+//   64 x 64 where 128 x 128 would: 128 x 4096, k 4096: 10.4 and 13.8
+//   streaming where few workgroups of 32 x 16 suffice: 48 x 4096, k 4096: 8.9 against 10
+inline MxKernel mx_dense_kernel(int64_t M, int64_t N, int64_t K) {
+  const auto tiles = [&](int64_t bm, int64_t bn) { return mx_ceil_div(M, bm) * mx_ceil_div(N, bn); };
+  if (M > 32 && mx_tiles_fit(0, N, K)) {
+    if (tiles(256, 256) >= 192 && K > 2048) return MX_TILES_256;
+    if (tiles(128, 256) >= 512) return MX_TILES_128x256_ONE;
+    if (tiles(128, 256) >= 192) return MX_TILES_128x256;
+    if (tiles(128, 128) >= 128) return MX_TILES_128;
+    if (tiles(32, 16) >= 850) return MX_TILES_64;
+  }
+  // 16 rows a workgroup where 32 would leave CUs without one: 64 x 1024, k 8192: 7.3 against 9.8
+  return M > 16 && tiles(32, 16) >= 256 ? MX_STREAM_32 : MX_STREAM_16;
+}
+
+// The same for experts, `pairs` rows in all, gate+up of `gathered` tokens (down: 0), by the rows that an
+// expert has on average (gate+up / down, 64 experts, hidden 8192, inter 3584 unless said otherwise):
+//   streaming for few: 2 rows: 319 / 181 against 363 / 188 in tiles; 4 rows: 368 / 217 against
+//   339 / 195; with few tiles for more rows: 8 experts, 1024 x 1024, 16 rows: 4.6 against 5.9
+//   128 x 256 tiles (64 rows where an expert has no more) up to 128 rows: 64 rows: 490 against 503
+//   256 x 256 for long k: 512 rows: 1311 against 1545;  128 x 256 with one buffer for short k (16
+//   experts, 250 rows, 1000 x 2048: 23.2 against 27.1 with two)
+inline MxKernel mx_experts_kernel(int64_t gathered, int64_t pairs, int64_t N, int64_t K, int64_t experts) {
+  const int64_t active = pairs < experts ? pairs : experts;  // at most
+  const double rows = (double)pairs / (double)experts;
+  const int64_t cols = mx_ceil_div(gathered ? 2 * N : N, 256);
+  if (!mx_tiles_fit(gathered, N, K) || rows < 3.0) return MX_STREAM_16;
+  if ((pairs / 128 + active) * cols < 128) return rows <= 32.0 ? MX_STREAM_16 : MX_TILES_128;
+  if (rows < 128.0) return MX_TILES_128x256;
+  if (K <= 2048 || (pairs / 256 + active) * cols < 512) return MX_TILES_128x256_ONE;
+  return MX_TILES_256;
+}
+
+}  // namespace wq
