@@ -280,13 +280,17 @@ wq_status wq_quantize_mx(const void* x, int32_t x_type, int64_t n, int64_t k, ui
                          uint8_t* scales, void* stream);
 
 /* y[m][n] = x W^T with x in MXFP4 (x_codes u8[m][k/2], x_scales u8[m][k/32]) and w in
- * WQ_FMT_MXFP4, experts == 1; y of y_type.  m == 0 is a no-op. */
+ * WQ_FMT_MXFP4, experts == 1; y of y_type.  m == 0 is a no-op.  Many rows run tiles; k below 256 or
+ * from 2^23 on, or more than 2^31 - 1024 bytes of an expert's codes (here and in the two calls below),
+ * runs the kernel for few rows at every m, several times slower where m is large. */
 wq_status wq_gemm_mx(const uint8_t* x_codes, const uint8_t* x_scales, int64_t m,
                      const wq_weight* w, void* y, int32_t y_type, void* stream);
 
 /* wq_moe_gate_up with x in MXFP4 (x_codes u8[t][hidden/2], x_scales u8[t][hidden/32]): the
  * product gathers the tokens' rows itself.  h bf16 [t*topk][inter], rows in expert order; rows of
- * dropped pairs (behind expert_offsets[experts]) are left as they were. */
+ * dropped pairs (behind expert_offsets[experts]) are left as they were.  The tiles reach tokens whose
+ * codes together take at most 2^31 - 1024 bytes (524287 tokens of hidden 8192); more run the kernel for
+ * few rows, many times slower: route and multiply such batches in parts. */
 wq_status wq_moe_gate_up_mx(const uint8_t* x_codes, const uint8_t* x_scales, int64_t t,
                             const int32_t* expert_offsets, const int32_t* sorted_pairs,
                             int32_t topk, const wq_weight* gate, const wq_weight* up, uint16_t* h,

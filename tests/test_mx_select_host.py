@@ -69,6 +69,14 @@ def test_experts_cases_take_their_kernels(lib):
             assert set().union(*(rows_of_last_tiles(c.counts, height) for c in some if c.kernel == kernel)) == classes
 
 
+def test_limit_of_gathered_tokens(lib):
+    """gate+up's tiles address all tokens' codes with 32 bits: 524287 tokens of hidden 8192 at most.  Down's
+    rows are addressed tile by tile and have no such limit."""
+    for t, kernel in ((524287, "MX_TILES_256"), (524288, "MX_STREAM_16")):
+        assert _experts(lib, t, 8 * t, 3584, 8192, 64) == kernel
+        assert _experts(lib, 0, 8 * t, 8192, 3584, 64) == "MX_TILES_256"
+
+
 def test_limits_of_the_tiles(lib):
     assert _dense(lib, 4096, 8192, 256).startswith("MX_TILES") and _dense(lib, 4096, 8192, 192) == "MX_STREAM_32"
     assert _dense(lib, 33, 1 << 20, 2048).startswith("MX_TILES")

@@ -20,8 +20,9 @@ enum MxKernel : int32_t {
 inline int64_t mx_ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // The tiles' 32-bit ranges: one expert's codes, a tile's rows (k below 2^23) and, gathered, the codes of
-// `gathered` tokens (0: rows are not gathered), each below 2^31 less a stage's bytes.  A stage needs 256
-// columns.
+// `gathered` tokens (0: rows are not gathered), each below 2^31 less a stage's bytes: gathered rows lie
+// anywhere, so one range covers them all, and from 524288 tokens of hidden 8192 on gate+up streams 16 rows
+// at a time.  A stage needs 256 columns: k below that streams at every number of rows.
 inline bool mx_tiles_fit(int64_t gathered, int64_t N, int64_t K) {
   constexpr int64_t most = (1ll << 31) - 1024;
   if (K < 256 || K >= (1ll << 23) || N * (K / 2) > most) return false;
