@@ -170,3 +170,37 @@ def test_many_pairs(wq):
     _poison(torch, P, hidden, torch.bfloat16)
     d_rows = wq.wq_moe_unpermute_grad(x, None, pos.view(t, topk))[0]
     assert torch.equal(d_rows.float().sum(1), sums) and not bool(d_rows[free].any())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_rows_beyond_4_gib(wq, dtype):
+    """Permutation, way back and gradients over rows of 8.6 GB, a fifth of the pairs dropped."""
+    import torch
+
+    t, topk, hidden = (1 << 16) + 3, 8, 8192 if dtype == "bf16" else 4096
+    P, dt = t * topk, getattr(torch, TYPES[dtype][0])
+    print("rows beyond 4 GiB", P, hidden, dtype, flush=True)
+    g = torch.Generator(device="cuda").manual_seed(2)
+    drop = torch.rand(P, generator=g, device="cuda") < 0.2
+    kept = int((~drop).sum())
+    pos = torch.full((P,), -1, dtype=torch.int32, device="cuda")
+    pos[~drop] = torch.randperm(kept, generator=g, device="cuda").to(torch.int32)
+    x = torch.randint(-8, 9, (t, hidden), generator=g, device="cuda", dtype=torch.int8).to(dt)
+    pos = pos.view(t, topk)
+    rows = wq.wq_moe_permute(x, pos)
+    owner = torch.full((P,), -1, dtype=torch.int64, device="cuda")  # the token of every row
+    owner[pos.view(-1)[~drop].long()] = (torch.arange(P, device="cuda") // topk)[~drop]
+    assert not bool(rows[kept:].any())
+    for r in (slice(0, 500), slice(kept // 2, kept // 2 + 500), slice(kept - 500, kept)):
+        assert torch.equal(rows[r], x[owner[r]])
+    # whole numbers: a token's kept rows are copies of it
+    n = (pos >= 0).sum(1, keepdim=True).float()
+    y = wq.wq_moe_unpermute(rows, pos)
+    for s in (slice(0, 300), slice(t - 300, t)):
+        assert torch.equal(y[s].float(), x[s].float() * n[s])
+    d_rows, d_w = wq.wq_moe_unpermute_grad(x, rows, pos)
+    assert not bool(d_rows[kept:].any())
+    for r in (slice(0, 500), slice(kept - 500, kept)):
+        assert torch.equal(d_rows[r], x[owner[r]])
+    for s in (slice(0, 300), slice(t - 300, t)):
+        assert torch.equal(d_w[s], (pos[s] >= 0).float() * (x[s].float() ** 2).sum(1, keepdim=True))
