@@ -8,6 +8,9 @@ Names follow the C ABI: ``wq_dequantize``, ``wq_gemm``, ``wq_moe_route``, ``wq_m
 ``wq_moe_workspace_bytes``, ``wq_pack_int4``, ``wq_unpack_int4``, ``wq_packed_size``; MXFP4:
 ``wq_quantize_mx``, ``wq_gemm_mx``, ``wq_moe_gate_up_mx``, ``wq_moe_down_mx``; the token dispatch:
 ``wq_moe_positions``, ``wq_moe_permute``, ``wq_moe_unpermute``, ``wq_moe_unpermute_grad``.
+
+The calls stand outside autograd: results carry no graph, also where an input requires a gradient.  For
+training, call them in the forward and the backward of a ``torch.autograd.Function``.
 """
 from __future__ import annotations
 
@@ -553,7 +556,8 @@ def wq_gemm_mx(x, w: PackedWeight, y=None, dtype=None):
 
 def wq_moe_gate_up_mx(x, offsets, sorted_pairs, topk: int, gate: PackedWeight, up: PackedWeight, h=None):
     """wq_moe_gate_up with both operands in MXFP4; x: wq_quantize_mx of the tokens [t, hidden].
-    h [t*topk, inter] bf16, rows in expert order."""
+    h [t*topk, inter] bf16, rows in expert order; rows behind offsets[-1] (dropped pairs leave some) are
+    not written."""
     import torch
 
     _mx_rows(x, "wq_moe_gate_up_mx x", k=gate.k)
@@ -572,7 +576,8 @@ def wq_moe_gate_up_mx(x, offsets, sorted_pairs, topk: int, gate: PackedWeight, u
 
 def wq_moe_down_mx(h, offsets, down: PackedWeight, d=None, dtype=None):
     """d [npairs, hidden] = down h with both operands in MXFP4; h: wq_quantize_mx of the rows
-    [npairs, inter] in expert order, the order d is in too.  bf16, or fp32 as in wq_gemm_mx."""
+    [npairs, inter] in expert order, the order d is in too; rows behind offsets[-1] are not written.
+    bf16 (one more rounding before the weighted sum), or fp32 as in wq_gemm_mx."""
     _mx_rows(h, "wq_moe_down_mx h", k=down.k)
     _need(offsets, "wq_moe_down_mx offsets", "i32", numel=down.experts + 1)
     vt, d = _product_out(d, dtype, h.codes, (h.n, down.n), "wq_moe_down_mx d")
@@ -631,7 +636,8 @@ def wq_moe_permute(x, positions, rows=None):
 
 
 def wq_moe_unpermute(rows, positions, topk_weights=None, y=None):
-    """y [t, hidden] = sum_j topk_weights[t, j] * rows[positions[t, j]] (weights None: 1)."""
+    """y [t, hidden] = sum_j topk_weights[t, j] * rows[positions[t, j]] (weights None: 1), of the rows'
+    type."""
     t, topk = _positions(positions, "wq_moe_unpermute")
     vt, kind = _value_type(rows, "wq_moe_unpermute rows")
     if rows.dim() != 2:

@@ -198,7 +198,8 @@ bool mxfp4_streams(const wq_weight* w, int64_t m) {
   return w->format == WQ_FMT_MXFP4 && m * w->n < most;
 }
 
-// MoE layers whose experts average at least this many routed rows use the tiled kernels.
+// MoE layers whose experts average at least this many routed rows use the tiled kernels (MXFP4, 31 rows and
+// 32: 64 experts, gate+up 3584 x 8192 891 and 714 us; 8 experts, 1024 x 1024 11.4 and 14.3).
 constexpr double kMoeTiledRows = 32.0;
 // Largest grid z extent one launch uses.
 constexpr int64_t kMaxGridZ = 65535;

@@ -5,8 +5,9 @@
 // expert order (-1: dropped), so a thread adds all of an output element's contributions, in slot
 // order: no atomics, the same bits every run.  All of it is bound by memory (a copy of 2 GiB: 4.8 to
 // 5.3 TB/s); rows are read and written in 16-byte pieces, at any element's address, which a row of
-// odd length starts at.  4096 tokens x 8 of 8192 bf16 (32 tokens): positions 2 us (1.4), permutation
-// 115 us, 5.2 TB/s (4.2), way back 117 us, 5.2 TB/s (4.1), gradient 230 us, 5.0 TB/s (7.3).
+// odd length starts at.  4096 tokens x 8 of 8192 bf16 (32 tokens): positions 2 to 5 us (1.4), permutation
+// 102 to 121 us, 5.0 to 5.9 TB/s (4.2), way back 117 us, 5.2 TB/s (4.1), gradient 214 to 237 us, 4.8 to
+// 5.3 TB/s (7.3).
 #include <hip/hip_runtime.h>
 
 #include "wq_kernels.hpp"

@@ -26,8 +26,9 @@ typedef int i32x8 __attribute__((ext_vector_type(8)));
 // patterns, and a NaN or infinity is at least 0x7F800000) gives the scale byte
 //   E - 2 for a maximum with exponent field E (never below 0): floor(log2 max) - 2 + 127,
 // and v_cvt_scalef32_pk_fp4_* divides by the scale, rounds half to even and saturates at 6.
-// Bound by memory: 8192 x 8192 fp32 45 to 48 us (6.4 to 6.7 TB/s read and written), bf16 25.5 us (6.6
-// TB/s); 17 x 4096 bf16 2.5 us, of which an empty kernel takes 1.6.
+// Bound by memory: 8192 x 8192 fp32 45 to 48 us (6.4 to 6.7 TB/s read and written; 61 right after another
+// kernel has written 134 MB), bf16 25.5 us (6.6 TB/s); 17 x 4096 bf16 2.3 us, of which an empty kernel
+// takes 1.6.
 // ---------------------------------------------------------------------------------------------
 
 // Maximum over the quad of lanes 4 i .. 4 i + 3.
