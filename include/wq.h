@@ -341,6 +341,96 @@ wq_status wq_moe_unpermute_grad(const void* dy, int32_t type, const void* rows,
                                 int32_t topk, int64_t hidden, void* d_rows, float* d_weights,
                                 void* stream);
 
+/* ---- Products in 8-bit integers, the norm in front of them, and the routing's balance loss ---------
+ * Activations in int8 have an fp32 scale per row, weights are WQ_FMT_INT8 with a scale per channel
+ * (group 0), the same arrays that the products with bf16 activations take.  Sums are exact (int32), so
+ * k is at most 131008.  Outputs overlap no input and no other output (WQ_ERR_ARG) unless a call says so.
+ * Row scales and loss scalars need their type's alignment only. */
+
+/* n rows of k values (x_type; device) to codes i8[n][k] and a scale per row, with a = max_j |x_j|:
+ *   WQ_TYPE_F32 scales (activations)         scale = f32(a / 127), code = rint(127 x / a)
+ *   WQ_TYPE_BF16 scales (weights' channels)  scale = bf16(f32(a / 127)),
+ *                                            code = rint(x / scale), at most 127 in magnitude
+ * half way to the even code.  A row of zeros has scale 0; one that holds an infinity or a NaN becomes NaN
+ * (codes 0, scale NaN).  An MoE tensor is n = experts x rows.  n == 0 is a no-op. */
+wq_status wq_quantize_i8(const void* x, int32_t x_type, int64_t n, int64_t k, int8_t* codes,
+                         void* scales, int32_t scales_type, void* stream);
+
+/* y[m][n] = (f32(sum_k x_codes[m][k] w_codes[n][k]) * x_scales[m]) * w_scales[n], of y_type; w has
+ * experts == 1.  m == 0 is a no-op. */
+wq_status wq_gemm_i8(const int8_t* x_codes, const float* x_scales, int64_t m, const wq_weight* w,
+                     void* y, int32_t y_type, void* stream);
+
+/* wq_moe_gate_up with x in int8 (x_codes i8[t][hidden], x_scales f32[t]): the product gathers the tokens'
+ * rows itself.  h bf16 [t*topk][inter], rows in expert order; rows of dropped pairs (behind
+ * expert_offsets[experts]) are left as they were.  The tiles reach tokens whose codes together take at
+ * most 2^31 - 1024 bytes (262143 tokens of hidden 8192); more run the kernel for few rows, many times
+ * slower: route and multiply such batches in parts. */
+wq_status wq_moe_gate_up_i8(const int8_t* x_codes, const float* x_scales, int64_t t,
+                            const int32_t* expert_offsets, const int32_t* sorted_pairs,
+                            int32_t topk, const wq_weight* gate, const wq_weight* up, uint16_t* h,
+                            void* stream);
+
+/* d[r] = W_down[e] h[r] for every row r in expert order (h_codes i8[npairs][inter], h_scales f32[npairs]);
+ * d of d_type [npairs][hidden], rows in expert order as well (wq_moe_unpermute brings them back); rows
+ * behind expert_offsets[experts] are left as they were. */
+wq_status wq_moe_down_i8(const int8_t* h_codes, const float* h_scales, int64_t npairs,
+                         const int32_t* expert_offsets, const wq_weight* down, void* d,
+                         int32_t d_type, void* stream);
+
+/* Root-mean-square norm of n rows of k values, all arrays of `type`:
+ *   r = x + residual, rounded to `type` and written to sum;  inv = 1 / sqrt(mean_j r_j^2 + eps)
+ *   y_j = r_j inv weight_j
+ * residual and sum may both be NULL: r = x.  sum may be x or residual itself (the same address).
+ * n == 0 is a no-op. */
+wq_status wq_rms_norm(const void* x, int32_t type, const void* residual, const void* weight,
+                      float eps, int64_t n, int64_t k, void* sum, void* y, void* stream);
+
+/* The same with y in int8, as the products take it: with v_j = r_j weight_j (unrounded) and a = max_j |v_j|,
+ *   scales = f32(a inv / 127), codes = rint(127 v / a)
+ * (rows of zeros, infinities and NaN as in wq_quantize_i8). */
+wq_status wq_rms_norm_i8(const void* x, int32_t type, const void* residual, const void* weight,
+                         float eps, int64_t n, int64_t k, void* sum, int8_t* codes, float* scales,
+                         void* stream);
+
+/* Bytes of device workspace wq_rms_norm_grad needs for d_weight (sums of parts of the rows); 0 where it
+ * needs none, or for invalid sizes. */
+size_t wq_rms_norm_grad_workspace_bytes(int64_t n, int64_t k, int32_t type);
+
+/* Gradients of wq_rms_norm for dy [n][k], with sum = r (x where there was no residual) and d_sum [n][k] the
+ * gradient that reaches r from elsewhere (NULL: none):
+ *   g_j = dy_j weight_j;  dx_j = inv (g_j - r_j inv^2 mean_i g_i r_i) + d_sum_j   (of x and of residual)
+ *   d_weight_j = sum over the rows of dy_j r_j inv                                (f32; NULL: not computed)
+ * dx may be d_sum itself.  ws: wq_rms_norm_grad_workspace_bytes bytes (caller-owned, nothing in it needs
+ * to be initialized; may be NULL where d_weight is).  n == 0 sets d_weight to zero. */
+wq_status wq_rms_norm_grad(const void* dy, int32_t type, const void* d_sum, const void* sum,
+                           const void* weight, float eps, int64_t n, int64_t k, void* dx,
+                           float* d_weight, void* ws, size_t ws_bytes, void* stream);
+
+/* Bytes of device workspace wq_moe_balance_loss needs; 0 where it needs none, or for invalid sizes. */
+size_t wq_moe_balance_loss_workspace_bytes(int64_t t, int32_t experts);
+
+/* The loss that keeps the experts evenly loaded: with p = softmax(logits) (logits of `type` [t][experts]),
+ * c_e the pairs of topk_ids whose id is e, and T the tokens that have a pair,
+ *   loss = coefficient * sum_e (experts c_e / sum_i c_i) * (sum_t p_te / T)      (f32, one value)
+ *   counts[e] = c_e, counts[experts] = T                                         (int32 [experts + 1])
+ * Tokens whose ids all lie outside [0, experts) are padding: they count nowhere and their logits are not
+ * used.  Without any token the loss is 0.  A row of -inf has no probability anywhere.  ws: as in
+ * wq_rms_norm_grad.  At most 512 experts and 2^30 pairs. */
+wq_status wq_moe_balance_loss(const void* logits, int32_t type, const int32_t* topk_ids, int64_t t,
+                              int32_t topk, int32_t experts, float coefficient, float* loss,
+                              int32_t* counts, void* ws, size_t ws_bytes, void* stream);
+
+/* d_logits [t][experts] of wq_moe_balance_loss for d_loss (f32, one value in device memory; NULL: 1), with
+ * the counts that it gave, or the sums of several calls' counts where the loss is over all of their tokens
+ * (the shares are no function of the logits):
+ *   share_e = experts c_e / sum_i c_i
+ *   d_logits_te = d_loss * coefficient / T * p_te (share_e - sum_j share_j p_tj)   (0 for padding) */
+wq_status wq_moe_balance_loss_grad(const void* logits, int32_t type, const int32_t* topk_ids,
+                                   int64_t t, int32_t topk, int32_t experts, float coefficient,
+                                   const int32_t* counts, const float* d_loss, void* d_logits,
+                                   void* stream);
+
 /* Host helpers for the INT4 storage format (lesson E6.4, "Do it in code"); host memory.
  * wq_pack_int4: two codes per byte, the first in the low nibble, an odd count padded with 0;
  *   out must hold (n+1)/2 bytes; WQ_ERR_RANGE (nothing written) for a code outside -8..7.

@@ -7,7 +7,10 @@ built, importing works but every call raises (there is no CPU fallback).
 Names follow the C ABI: ``wq_dequantize``, ``wq_gemm``, ``wq_moe_route``, ``wq_moe_ffn``,
 ``wq_moe_workspace_bytes``, ``wq_pack_int4``, ``wq_unpack_int4``, ``wq_packed_size``; MXFP4:
 ``wq_quantize_mx``, ``wq_gemm_mx``, ``wq_moe_gate_up_mx``, ``wq_moe_down_mx``; the token dispatch:
-``wq_moe_positions``, ``wq_moe_permute``, ``wq_moe_unpermute``, ``wq_moe_unpermute_grad``.
+``wq_moe_positions``, ``wq_moe_permute``, ``wq_moe_unpermute``, ``wq_moe_unpermute_grad``; products in
+8-bit integers: ``wq_quantize_i8``, ``wq_quantize_i8_weight``, ``wq_gemm_i8``, ``wq_moe_gate_up_i8``,
+``wq_moe_down_i8``; the norm: ``wq_rms_norm``, ``wq_rms_norm_i8``, ``wq_rms_norm_grad``; the routing's loss:
+``wq_moe_balance_loss``, ``wq_moe_balance_loss_grad``.
 
 The calls stand outside autograd: results carry no graph, also where an input requires a gradient.  For
 training, call them in the forward and the backward of a ``torch.autograd.Function``.
@@ -18,6 +21,7 @@ import ctypes
 import functools
 import os
 from dataclasses import dataclass, field
+from typing import NamedTuple
 
 import numpy as np
 
@@ -44,7 +48,10 @@ EXPORTS = ("wq_dequantize", "wq_gemm", "wq_moe_workspace_bytes", "wq_moe_route_w
            "wq_moe_gate_up", "wq_moe_down", "wq_moe_combine", "wq_pack_int4", "wq_unpack_int4",
            "wq_packed_size", "wq_status_string", "wq_last_error", "wq_last_error_detail", "wq_quantize_ccq",
            "wq_moe_ffn_noalloc", "wq_quantize_mx", "wq_gemm_mx", "wq_moe_gate_up_mx", "wq_moe_down_mx",
-           "wq_moe_positions", "wq_moe_permute", "wq_moe_unpermute", "wq_moe_unpermute_grad")
+           "wq_moe_positions", "wq_moe_permute", "wq_moe_unpermute", "wq_moe_unpermute_grad",
+           "wq_quantize_i8", "wq_gemm_i8", "wq_moe_gate_up_i8", "wq_moe_down_i8", "wq_rms_norm", "wq_rms_norm_i8",
+           "wq_rms_norm_grad_workspace_bytes", "wq_rms_norm_grad", "wq_moe_balance_loss_workspace_bytes",
+           "wq_moe_balance_loss", "wq_moe_balance_loss_grad")
 
 
 class WqError(RuntimeError):
@@ -80,6 +87,7 @@ def lib() -> ctypes.CDLL:
             raise WqError(f"{LIB_PATH} is missing: build it with weight_only_bit_amd/build.py")
         L = ctypes.CDLL(LIB_PATH)
         vp, i64, i32, sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t
+        f32 = ctypes.c_float
         W = ctypes.POINTER(_CWeight)
         sig = {
             "wq_dequantize": (i32, [W, vp, vp]),
@@ -101,6 +109,17 @@ def lib() -> ctypes.CDLL:
             "wq_moe_permute": (i32, [vp, i32, i64, i32, i64, vp, vp, vp]),
             "wq_moe_unpermute": (i32, [vp, i32, vp, vp, i64, i32, i64, vp, vp]),
             "wq_moe_unpermute_grad": (i32, [vp, i32, vp, vp, vp, i64, i32, i64, vp, vp, vp]),
+            "wq_quantize_i8": (i32, [vp, i32, i64, i64, vp, vp, i32, vp]),
+            "wq_gemm_i8": (i32, [vp, vp, i64, W, vp, i32, vp]),
+            "wq_moe_gate_up_i8": (i32, [vp, vp, i64, vp, vp, i32, W, W, vp, vp]),
+            "wq_moe_down_i8": (i32, [vp, vp, i64, vp, W, vp, i32, vp]),
+            "wq_rms_norm": (i32, [vp, i32, vp, vp, f32, i64, i64, vp, vp, vp]),
+            "wq_rms_norm_i8": (i32, [vp, i32, vp, vp, f32, i64, i64, vp, vp, vp, vp]),
+            "wq_rms_norm_grad_workspace_bytes": (sz, [i64, i64, i32]),
+            "wq_rms_norm_grad": (i32, [vp, i32, vp, vp, vp, f32, i64, i64, vp, vp, vp, sz, vp]),
+            "wq_moe_balance_loss_workspace_bytes": (sz, [i64, i32]),
+            "wq_moe_balance_loss": (i32, [vp, i32, vp, i64, i32, i32, f32, vp, vp, vp, sz, vp]),
+            "wq_moe_balance_loss_grad": (i32, [vp, i32, vp, i64, i32, i32, f32, vp, vp, vp, vp]),
             "wq_pack_int4": (i32, [vp, i64, vp]),
             "wq_unpack_int4": (i32, [vp, i64, vp]),
             "wq_packed_size": (i64, [i64, i32]),
@@ -174,7 +193,7 @@ def _dtypes():
         import torch
 
         _kinds = {"bf16": (torch.bfloat16, torch.int16), "i32": (torch.int32,), "f32": (torch.float32,),
-                  "u8": (torch.uint8, torch.int8)}
+                  "u8": (torch.uint8, torch.int8), "i8": (torch.int8,)}
     return _kinds
 
 
@@ -684,6 +703,259 @@ def wq_moe_unpermute_grad(dy, rows, positions, topk_weights=None, d_rows=None, d
                                        topk, hidden, _ptr(d_rows), _ptr(d_weights), _stream()),
            "wq_moe_unpermute_grad")
     return d_rows, d_weights
+
+
+# ---------------------------------------------------------------------------------------------
+# Rows in int8, the products of two int8 operands, and the norm that writes such rows
+# ---------------------------------------------------------------------------------------------
+
+class Int8Rows(NamedTuple):
+    """Rows in int8: the value of codes[i, j] is codes[i, j] * scales[i]."""
+    codes: object   # int8 [n, k]
+    scales: object  # f32 [n]
+
+
+def wq_quantize_i8(x) -> Int8Rows:
+    """bf16 or fp32 rows [n, k] to int8 with a scale per row (include/wq.h): the activations of the products
+    below."""
+    import torch
+
+    vt, kind = _value_type(x, "wq_quantize_i8 x")
+    if x.dim() != 2 or x.shape[1] == 0:
+        raise ValueError(f"wq_quantize_i8: x must be [n, k], got shape {tuple(x.shape)}")
+    n, k = x.shape
+    x = _need(x.contiguous(), "wq_quantize_i8 x", kind)
+    rows = Int8Rows(x.new_empty((n, k), dtype=torch.int8), x.new_empty(n, dtype=torch.float32))
+    _check(lib().wq_quantize_i8(_ptr(x), vt, n, k, _ptr(rows.codes), _ptr(rows.scales), TYPE_F32, _stream()),
+           "wq_quantize_i8")
+    return rows
+
+
+def wq_quantize_i8_weight(w) -> PackedWeight:
+    """bf16 or fp32 weights [n, k] or [E, n, k] to FMT_INT8 with a bf16 scale per output channel."""
+    import torch
+
+    vt, kind = _value_type(w, "wq_quantize_i8_weight w")
+    if w.dim() not in (2, 3):
+        raise ValueError("wq_quantize_i8_weight: w must be [n, k] or [E, n, k]")
+    E, n, k = w.shape if w.dim() == 3 else (1, *w.shape)
+    if k <= 0 or k % 64:
+        raise ValueError(f"wq_quantize_i8_weight: k = {k} is not a positive multiple of 64")
+    w = _need(w.contiguous(), "wq_quantize_i8_weight w", kind)
+    codes = w.new_empty((E, n, k), dtype=torch.int8)
+    scales = w.new_empty((E, n), dtype=torch.bfloat16)
+    _check(lib().wq_quantize_i8(_ptr(w), vt, E * n, k, _ptr(codes), _ptr(scales), TYPE_BF16, _stream()),
+           "wq_quantize_i8_weight")
+    return PackedWeight(FMT_INT8, n, k, E, 0, codes=codes, scales=scales)
+
+
+def _i8_rows(x, what, k):
+    """(rows, codes) of x, which wq_quantize_i8 or wq_rms_norm_i8 gave, of length k."""
+    if not isinstance(x, tuple) or len(x) != 2:
+        raise TypeError(f"{what}: expected Int8Rows, got {type(x).__name__}")
+    codes, scales = x
+    _need(codes, f"{what} codes", "i8")
+    if codes.dim() != 2 or codes.shape[1] != k:
+        raise ValueError(f"{what}: codes must be [rows, {k}], got shape {tuple(codes.shape)}")
+    _need(scales, f"{what} scales", "f32", numel=codes.shape[0])
+    return codes.shape[0], codes, scales
+
+
+def wq_gemm_i8(x, w: PackedWeight, y=None, dtype=None):
+    """y = x @ W^T with x in int8 (Int8Rows [m, k]) and w in FMT_INT8 with a scale per channel (group 0).  y
+    is bf16, or fp32 with dtype=torch.float32 (or a y of that type)."""
+    m, codes, scales = _i8_rows(x, "wq_gemm_i8 x", w.k)
+    vt, y = _product_out(y, dtype, codes, (m, w.n), "wq_gemm_i8 y")
+    _check(lib().wq_gemm_i8(_ptr(codes), _ptr(scales), m, ctypes.byref(w.cstruct()), _ptr(y), vt, _stream()),
+           "wq_gemm_i8")
+    return y
+
+
+def wq_moe_gate_up_i8(x, offsets, sorted_pairs, topk: int, gate: PackedWeight, up: PackedWeight, h=None):
+    """wq_moe_gate_up with both operands in int8; x: Int8Rows of the tokens [t, hidden].  h [t*topk, inter]
+    bf16, rows in expert order; rows behind offsets[-1] (dropped pairs leave some) are not written."""
+    import torch
+
+    t, codes, scales = _i8_rows(x, "wq_moe_gate_up_i8 x", gate.k)
+    _need(offsets, "wq_moe_gate_up_i8 offsets", "i32", numel=gate.experts + 1)
+    _need(sorted_pairs, "wq_moe_gate_up_i8 sorted_pairs", "i32", numel=t * topk)
+    if h is None:
+        h = codes.new_empty((t * topk, gate.n), dtype=torch.bfloat16)
+    else:
+        _need(h, "wq_moe_gate_up_i8 h", "bf16", shape=(t * topk, gate.n))
+    _check(lib().wq_moe_gate_up_i8(_ptr(codes), _ptr(scales), t, _ptr(offsets), _ptr(sorted_pairs), topk,
+                                   ctypes.byref(gate.cstruct()), ctypes.byref(up.cstruct()), _ptr(h), _stream()),
+           "wq_moe_gate_up_i8")
+    return h
+
+
+def wq_moe_down_i8(h, offsets, down: PackedWeight, d=None, dtype=None):
+    """d [npairs, hidden] = down h with both operands in int8; h: Int8Rows [npairs, inter] in expert order,
+    the order d is in too; rows behind offsets[-1] are not written.  bf16, or fp32 as in wq_gemm_i8."""
+    npairs, codes, scales = _i8_rows(h, "wq_moe_down_i8 h", down.k)
+    _need(offsets, "wq_moe_down_i8 offsets", "i32", numel=down.experts + 1)
+    vt, d = _product_out(d, dtype, codes, (npairs, down.n), "wq_moe_down_i8 d")
+    _check(lib().wq_moe_down_i8(_ptr(codes), _ptr(scales), npairs, _ptr(offsets), ctypes.byref(down.cstruct()),
+                                _ptr(d), vt, _stream()), "wq_moe_down_i8")
+    return d
+
+
+def _norm_inputs(x, weight, residual, sum, what):
+    """(wq_type, _need kind, n, k, sum) of a norm's inputs; sum: the caller's array, a new one, or None where
+    there is no residual."""
+    vt, kind = _value_type(x, f"{what} x")
+    if x.dim() != 2 or x.shape[1] == 0:
+        raise ValueError(f"{what}: x must be [n, k], got shape {tuple(x.shape)}")
+    _need(x, f"{what} x", kind)
+    n, k = x.shape
+    _need(weight, f"{what} weight", kind, shape=(k,))
+    if residual is None:
+        if sum is not None:
+            raise ValueError(f"{what}: a sum without a residual")
+        return vt, kind, n, k, None
+    _need(residual, f"{what} residual", kind, shape=(n, k))
+    if sum is None:
+        sum = x.new_empty((n, k))
+    else:
+        _need(sum, f"{what} sum", kind, shape=(n, k))
+    return vt, kind, n, k, sum
+
+
+def wq_rms_norm(x, weight, residual=None, eps: float = 1e-6, y=None, sum=None):
+    """(y, sum): sum = x + residual rounded to their type (x itself without a residual) and its
+    root-mean-square norm times weight [k]; all bf16 or all fp32, rows [n, k].  sum may be the residual's or
+    x's own tensor."""
+    vt, kind, n, k, total = _norm_inputs(x, weight, residual, sum, "wq_rms_norm")
+    if y is None:
+        y = x.new_empty((n, k))
+    else:
+        _need(y, "wq_rms_norm y", kind, shape=(n, k))
+    _check(lib().wq_rms_norm(_ptr(x), vt, _ptr(residual), _ptr(weight), eps, n, k, _ptr(total), _ptr(y), _stream()),
+           "wq_rms_norm")
+    return y, x if total is None else total
+
+
+def wq_rms_norm_i8(x, weight, residual=None, eps: float = 1e-6, rows=None, sum=None):
+    """(Int8Rows, sum): wq_rms_norm with the normed rows in int8, a scale each, as the int8 products take
+    them."""
+    import torch
+
+    vt, kind, n, k, total = _norm_inputs(x, weight, residual, sum, "wq_rms_norm_i8")
+    if rows is None:
+        rows = Int8Rows(x.new_empty((n, k), dtype=torch.int8), x.new_empty(n, dtype=torch.float32))
+    else:
+        if not isinstance(rows, tuple) or len(rows) != 2:
+            raise TypeError(f"wq_rms_norm_i8 rows: expected Int8Rows, got {type(rows).__name__}")
+        rows = Int8Rows(*rows)
+        _need(rows.codes, "wq_rms_norm_i8 rows' codes", "i8", shape=(n, k))
+        _need(rows.scales, "wq_rms_norm_i8 rows' scales", "f32", numel=n)
+    _check(lib().wq_rms_norm_i8(_ptr(x), vt, _ptr(residual), _ptr(weight), eps, n, k, _ptr(total), _ptr(rows.codes),
+                                _ptr(rows.scales), _stream()), "wq_rms_norm_i8")
+    return rows, x if total is None else total
+
+
+def wq_rms_norm_grad(dy, sum, weight, d_sum=None, eps: float = 1e-6, dx=None, d_weight=None, weight_grad: bool = True,
+                     ws=None):
+    """(dx, d_weight f32 [k]) of wq_rms_norm for dy [n, k]; sum as wq_rms_norm gave it, d_sum: the gradient
+    that reaches the sum from elsewhere.  dx is the gradient of x and of the residual alike, and may be d_sum's
+    own tensor.  weight_grad False: d_weight is not computed and None.  ws: a uint8 tensor of
+    wq_rms_norm_grad_workspace_bytes, allocated by the call if None."""
+    import torch
+
+    vt, kind = _value_type(dy, "wq_rms_norm_grad dy")
+    if dy.dim() != 2 or dy.shape[1] == 0:
+        raise ValueError(f"wq_rms_norm_grad: dy must be [n, k], got shape {tuple(dy.shape)}")
+    n, k = dy.shape
+    _need(dy, "wq_rms_norm_grad dy", kind)
+    _need(sum, "wq_rms_norm_grad sum", kind, shape=(n, k))
+    _need(weight, "wq_rms_norm_grad weight", kind, shape=(k,))
+    if d_sum is not None:
+        _need(d_sum, "wq_rms_norm_grad d_sum", kind, shape=(n, k))
+    if dx is None:
+        dx = dy.new_empty((n, k))
+    else:
+        _need(dx, "wq_rms_norm_grad dx", kind, shape=(n, k))
+    if not weight_grad:
+        if d_weight is not None:
+            raise ValueError("wq_rms_norm_grad: a d_weight without weight_grad")
+    elif d_weight is None:
+        d_weight = dy.new_empty(k, dtype=torch.float32)
+    else:
+        _need(d_weight, "wq_rms_norm_grad d_weight", "f32", shape=(k,))
+    ws = _workspace(ws, wq_rms_norm_grad_workspace_bytes(n, k, vt) if weight_grad else 0, dy, "wq_rms_norm_grad")
+    _check(lib().wq_rms_norm_grad(_ptr(dy), vt, _ptr(d_sum), _ptr(sum), _ptr(weight), eps, n, k, _ptr(dx),
+                                  _ptr(d_weight), _ptr(ws), 0 if ws is None else ws.numel(), _stream()),
+           "wq_rms_norm_grad")
+    return dx, d_weight
+
+
+def wq_rms_norm_grad_workspace_bytes(n: int, k: int, value_type: int) -> int:
+    return int(lib().wq_rms_norm_grad_workspace_bytes(n, k, value_type))
+
+
+def _workspace(ws, need, like, what):
+    """The caller's workspace checked, a new one, or None where none is needed."""
+    import torch
+
+    if ws is None:
+        return like.new_empty(need, dtype=torch.uint8) if need else None
+    return _need(ws, f"{what} ws", "u8") if ws.numel() else None
+
+
+# ---------------------------------------------------------------------------------------------
+# The routing's balance loss
+# ---------------------------------------------------------------------------------------------
+
+def wq_moe_balance_loss_workspace_bytes(t: int, experts: int) -> int:
+    return int(lib().wq_moe_balance_loss_workspace_bytes(t, experts))
+
+
+def _balance_inputs(logits, topk_ids, what):
+    vt, kind = _value_type(logits, f"{what} logits")
+    if logits.dim() != 2 or topk_ids.dim() != 2:
+        raise ValueError(f"{what}: logits must be [t, experts] and topk_ids [t, topk]")
+    _need(logits, f"{what} logits", kind)
+    _need(topk_ids, f"{what} topk_ids", "i32", shape=(logits.shape[0], topk_ids.shape[1]))
+    return vt, kind, logits.shape[0], topk_ids.shape[1], logits.shape[1]
+
+
+def wq_moe_balance_loss(logits, topk_ids, coefficient: float = 1.0, loss=None, counts=None, ws=None):
+    """(loss f32 [], counts int32 [experts + 1]): the balance loss (include/wq.h) of the router's logits
+    [t, experts], bf16 or fp32, and the ids that it chose; counts holds every expert's pairs and, last, the
+    tokens that have a pair (padding, all of whose ids are no expert's, counts nowhere)."""
+    import torch
+
+    vt, _, t, topk, experts = _balance_inputs(logits, topk_ids, "wq_moe_balance_loss")
+    if loss is None:
+        loss = logits.new_empty((), dtype=torch.float32)
+    else:
+        _need(loss, "wq_moe_balance_loss loss", "f32", numel=1)
+    if counts is None:
+        counts = topk_ids.new_empty(experts + 1)
+    else:
+        _need(counts, "wq_moe_balance_loss counts", "i32", numel=experts + 1)
+    ws = _workspace(ws, wq_moe_balance_loss_workspace_bytes(t, experts), logits, "wq_moe_balance_loss")
+    _check(lib().wq_moe_balance_loss(_ptr(logits), vt, _ptr(topk_ids), t, topk, experts, coefficient, _ptr(loss),
+                                     _ptr(counts), _ptr(ws), 0 if ws is None else ws.numel(), _stream()),
+           "wq_moe_balance_loss")
+    return loss, counts
+
+
+def wq_moe_balance_loss_grad(logits, topk_ids, counts, coefficient: float = 1.0, d_loss=None, d_logits=None):
+    """d_logits [t, experts] of wq_moe_balance_loss; counts as it gave them (or the sum of several calls'),
+    d_loss: an fp32 tensor of one value (None: 1)."""
+    vt, kind, t, topk, experts = _balance_inputs(logits, topk_ids, "wq_moe_balance_loss_grad")
+    _need(counts, "wq_moe_balance_loss_grad counts", "i32", numel=experts + 1)
+    if d_loss is not None:
+        _need(d_loss, "wq_moe_balance_loss_grad d_loss", "f32", numel=1)
+    if d_logits is None:
+        d_logits = logits.new_empty((t, experts))
+    else:
+        _need(d_logits, "wq_moe_balance_loss_grad d_logits", kind, shape=(t, experts))
+    _check(lib().wq_moe_balance_loss_grad(_ptr(logits), vt, _ptr(topk_ids), t, topk, experts, coefficient,
+                                          _ptr(counts), _ptr(d_loss), _ptr(d_logits), _stream()),
+           "wq_moe_balance_loss_grad")
+    return d_logits
 
 
 # ---------------------------------------------------------------------------------------------

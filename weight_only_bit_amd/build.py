@@ -10,7 +10,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "libwq.so")
 SOURCES = ["wq_api.hip", "wq_misc.hip", "wq_skinny.hip", "wq_tiled.hip", "wq_encode.hip",
-           "wq_mx.hip", "wq_dispatch.hip"]
+           "wq_mx.hip", "wq_dispatch.hip", "wq_i8.hip", "wq_norm.hip", "wq_balance.hip"]
 ARCH = os.environ.get("WQ_OFFLOAD_ARCH", "gfx950")
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

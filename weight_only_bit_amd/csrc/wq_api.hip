@@ -11,6 +11,7 @@
 #include <string>
 
 #include "../../include/wq.h"
+#include "wq_i8_select.hpp"
 #include "wq_kernels.hpp"
 
 namespace {
@@ -884,6 +885,261 @@ wq_status wq_moe_unpermute_grad(const void* dy, int32_t type, const void* rows,
                                               topk, hidden, d_rows, d_weights, clear,
                                               static_cast<hipStream_t>(stream)),
                     "wq_moe_unpermute_grad launch");
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------------------------
+// Rows in int8 with a scale each, the products of two int8 operands, the root-mean-square norm, and the
+// routing's balance loss.
+// ---------------------------------------------------------------------------------------------
+namespace {
+
+// n rows of k values.
+wq_status check_rows(int64_t n, int64_t k, const char* what) {
+  if (n < 0 || k <= 0) return fail(WQ_ERR_ARG, "%s: bad sizes", what);
+  if (k > (1ll << 31) || n > (1ll << 42) / k) return fail(WQ_ERR_UNSUPPORTED, "%s: more than 2^42 values", what);
+  return WQ_OK;
+}
+
+wq_status check_i8_weight(const wq_weight* w, const char* what) {
+  wq_status st = check_weight(w, what);
+  if (st != WQ_OK) return st;
+  if (w->format != WQ_FMT_INT8 || w->group != 0)
+    return fail(WQ_ERR_UNSUPPORTED, "%s: the weight must be WQ_FMT_INT8 with a scale per channel (group 0)", what);
+  if (w->k > wq::kI8MaxK)
+    return fail(WQ_ERR_UNSUPPORTED, "%s: k = %lld above %lld, where a sum could leave int32", what, (long long)w->k,
+                (long long)wq::kI8MaxK);
+  return check_product_zp(w, what);
+}
+
+// The arrays of such a weight.
+Span i8_codes(const wq_weight* w) { return Span(w->codes, w->experts * w->n * w->k, 1); }
+Span i8_scales(const wq_weight* w) { return Span(w->scales, w->experts * w->n, 2); }
+
+wq::I8Args i8_args(const wq_weight* w, const wq_weight* up, const int8_t* codes, const float* scales, int64_t rows,
+                   void* out) {
+  wq::I8Args a{};
+  a.w0_codes = reinterpret_cast<const int8_t*>(w->codes);
+  a.w0_scales = w->scales;
+  a.w1_codes = reinterpret_cast<const int8_t*>(up->codes);
+  a.w1_scales = up->scales;
+  a.x_codes = codes;
+  a.x_scales = scales;
+  a.out = out;
+  a.topk = 1;
+  a.M = rows;
+  a.N = w->n;
+  a.K = w->k;
+  return a;
+}
+
+// The norm with either output (y, or codes and scales).
+wq_status norm_in(const char* what, const void* x, int32_t type, const void* residual, const void* weight, float eps,
+                  int64_t n, int64_t k, void* sum, void* y, int8_t* codes, float* scales, bool i8, void* stream) {
+  wq_status st = check_type(type, what);
+  if (st != WQ_OK) return st;
+  if ((st = check_rows(n, k, what)) != WQ_OK) return st;
+  if (!(eps >= 0.f) || eps > 3.4e38f) return fail(WQ_ERR_ARG, "%s: eps must be finite and not negative", what);
+  if (n == 0) return WQ_OK;
+  if (!x || !weight || (i8 ? !codes || !scales : !y)) return fail(WQ_ERR_ARG, "%s: null pointer", what);
+  if (!residual != !sum) return fail(WQ_ERR_ARG, "%s: residual and sum come together", what);
+  if (!aligned16(x) || !aligned16(residual) || !aligned16(weight) || !aligned16(sum) || !aligned16(y) || !aligned16(codes))
+    return fail(WQ_ERR_ALIGN, "%s: a row array is not 16-byte aligned", what);
+  const int size = type_size(type);
+  const Span in(x, n * k, size), res(residual, n * k, size), w(weight, k, size), total(sum, n * k, size);
+  const Span out(i8 ? static_cast<const void*>(codes) : y, n * k, i8 ? 1 : size), sc(i8 ? scales : nullptr, n, 4);
+  // the sum may take the place of x or of the residual: a thread reads an element before it writes it
+  if (overlaps(out, {in, res, w, total, sc}) || overlaps(sc, {in, res, w, total}) || overlaps(total, {w}) ||
+      (sum != x && overlaps(total, {in})) || (sum != residual && overlaps(total, {res})))
+    return fail(WQ_ERR_ARG, "%s: outputs overlap inputs or each other", what);
+  return hip_status(wq::launch_norm(x, type == WQ_TYPE_F32, residual, weight, eps, n, k, sum, y, i8 ? codes : nullptr,
+                                    scales, static_cast<hipStream_t>(stream)),
+                    what);
+}
+
+wq_status check_balance(int32_t type, int64_t t, int32_t topk, int32_t experts, const char* what) {
+  wq_status st = check_type(type, what);
+  if (st != WQ_OK) return st;
+  if ((st = check_pairs(t, topk, experts, what)) != WQ_OK) return st;
+  if (experts > kMaxExperts) return fail(WQ_ERR_UNSUPPORTED, "%s: at most %d experts", what, kMaxExperts);
+  return WQ_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+wq_status wq_quantize_i8(const void* x, int32_t x_type, int64_t n, int64_t k, int8_t* codes, void* scales,
+                         int32_t scales_type, void* stream) {
+  wq_status st = check_type(x_type, "wq_quantize_i8");
+  if (st != WQ_OK) return st;
+  if ((st = check_type(scales_type, "wq_quantize_i8 scales")) != WQ_OK) return st;
+  if ((st = check_rows(n, k, "wq_quantize_i8")) != WQ_OK) return st;
+  if (n == 0) return WQ_OK;
+  if (!x || !codes || !scales) return fail(WQ_ERR_ARG, "wq_quantize_i8: null pointer");
+  if (!aligned16(x) || !aligned16(codes))
+    return fail(WQ_ERR_ALIGN, "wq_quantize_i8: x and codes must be 16-byte aligned");
+  const Span in(x, n * k, type_size(x_type)), sc(scales, n, type_size(scales_type));
+  if (overlaps(Span(codes, n * k, 1), {in, sc}) || overlaps(sc, {in}))
+    return fail(WQ_ERR_ARG, "wq_quantize_i8: codes or scales overlap x or each other");
+  return hip_status(wq::launch_quantize_i8(x, x_type == WQ_TYPE_F32, n, k, codes, scales, scales_type == WQ_TYPE_F32,
+                                           static_cast<hipStream_t>(stream)),
+                    "wq_quantize_i8 launch");
+}
+
+wq_status wq_gemm_i8(const int8_t* x_codes, const float* x_scales, int64_t m, const wq_weight* w, void* y,
+                     int32_t y_type, void* stream) {
+  wq_status st = check_i8_weight(w, "wq_gemm_i8");
+  if (st != WQ_OK) return st;
+  if ((st = check_type(y_type, "wq_gemm_i8")) != WQ_OK) return st;
+  if (m < 0) return fail(WQ_ERR_ARG, "wq_gemm_i8: negative m");
+  if (w->experts != 1) return fail(WQ_ERR_ARG, "wq_gemm_i8: a dense weight has experts == 1");
+  if (m == 0) return WQ_OK;
+  if (!x_codes || !x_scales || !y) return fail(WQ_ERR_ARG, "wq_gemm_i8: null x or y");
+  if (!aligned16(x_codes) || !aligned16(y)) return fail(WQ_ERR_ALIGN, "wq_gemm_i8: x or y not 16-byte aligned");
+  if (m > (1ll << 31)) return fail(WQ_ERR_UNSUPPORTED, "wq_gemm_i8: m must not exceed 2^31");
+  if (overlaps(Span(y, m * w->n, type_size(y_type)),
+               {Span(x_codes, m * w->k, 1), Span(x_scales, m, 4), i8_codes(w), i8_scales(w)}))
+    return fail(WQ_ERR_ARG, "wq_gemm_i8: y overlaps x or the weight");
+  wq::I8Args a = i8_args(w, w, x_codes, x_scales, m, y);
+  a.out_f32 = y_type == WQ_TYPE_F32;
+  return hip_status(wq::launch_i8_product(wq::MODE_DENSE, a, 1, static_cast<hipStream_t>(stream)),
+                    "wq_gemm_i8 launch");
+}
+
+wq_status wq_moe_gate_up_i8(const int8_t* x_codes, const float* x_scales, int64_t t, const int32_t* expert_offsets,
+                            const int32_t* sorted_pairs, int32_t topk, const wq_weight* gate, const wq_weight* up,
+                            uint16_t* h, void* stream) {
+  if (!gate || !up) return fail(WQ_ERR_ARG, "wq_moe_gate_up_i8: null descriptor");
+  wq_status st = check_moe_weights(gate, up, nullptr, "wq_moe_gate_up_i8");
+  if (st != WQ_OK) return st;
+  if ((st = check_i8_weight(gate, "wq_moe_gate_up_i8")) != WQ_OK) return st;
+  if ((st = check_pairs(t, topk, gate->n, "wq_moe_gate_up_i8")) != WQ_OK) return st;
+  if (t == 0) return WQ_OK;
+  if (!x_codes || !x_scales || !expert_offsets || !sorted_pairs || !h)
+    return fail(WQ_ERR_ARG, "wq_moe_gate_up_i8: null pointer");
+  if (!aligned16(x_codes) || !aligned16(h))
+    return fail(WQ_ERR_ALIGN, "wq_moe_gate_up_i8: x and h must be 16-byte aligned");
+  if (overlaps(Span(h, t * topk * gate->n, 2),
+               {Span(x_codes, t * gate->k, 1), Span(x_scales, t, 4), i8_codes(gate), i8_scales(gate), i8_codes(up),
+                i8_scales(up), Span(expert_offsets, gate->experts + 1, 4), Span(sorted_pairs, t * topk, 4)}))
+    return fail(WQ_ERR_ARG, "wq_moe_gate_up_i8: h overlaps an input");
+  wq::I8Args a = i8_args(gate, up, x_codes, x_scales, t * topk, h);
+  a.offsets = expert_offsets;
+  a.sorted_pairs = sorted_pairs;
+  a.topk = topk;
+  return hip_status(wq::launch_i8_product(wq::MODE_GATEUP, a, gate->experts, static_cast<hipStream_t>(stream)),
+                    "wq_moe_gate_up_i8 launch");
+}
+
+wq_status wq_moe_down_i8(const int8_t* h_codes, const float* h_scales, int64_t npairs, const int32_t* expert_offsets,
+                         const wq_weight* down, void* d, int32_t d_type, void* stream) {
+  if (!down) return fail(WQ_ERR_ARG, "wq_moe_down_i8: null descriptor");
+  wq_status st = check_moe_weights(nullptr, nullptr, down, "wq_moe_down_i8");
+  if (st != WQ_OK) return st;
+  if ((st = check_i8_weight(down, "wq_moe_down_i8")) != WQ_OK) return st;
+  if ((st = check_type(d_type, "wq_moe_down_i8")) != WQ_OK) return st;
+  if ((st = check_pairs(npairs, 1, down->n, "wq_moe_down_i8")) != WQ_OK) return st;
+  if (npairs == 0) return WQ_OK;
+  if (!h_codes || !h_scales || !expert_offsets || !d) return fail(WQ_ERR_ARG, "wq_moe_down_i8: null pointer");
+  if (!aligned16(h_codes) || !aligned16(d))
+    return fail(WQ_ERR_ALIGN, "wq_moe_down_i8: h and d must be 16-byte aligned");
+  if (overlaps(Span(d, npairs * down->n, type_size(d_type)),
+               {Span(h_codes, npairs * down->k, 1), Span(h_scales, npairs, 4), i8_codes(down), i8_scales(down),
+                Span(expert_offsets, down->experts + 1, 4)}))
+    return fail(WQ_ERR_ARG, "wq_moe_down_i8: d overlaps an input");
+  wq::I8Args a = i8_args(down, down, h_codes, h_scales, npairs, d);
+  a.offsets = expert_offsets;
+  a.out_f32 = d_type == WQ_TYPE_F32;
+  return hip_status(wq::launch_i8_product(wq::MODE_DOWN, a, down->experts, static_cast<hipStream_t>(stream)),
+                    "wq_moe_down_i8 launch");
+}
+
+wq_status wq_rms_norm(const void* x, int32_t type, const void* residual, const void* weight, float eps, int64_t n,
+                      int64_t k, void* sum, void* y, void* stream) {
+  return norm_in("wq_rms_norm", x, type, residual, weight, eps, n, k, sum, y, nullptr, nullptr, false, stream);
+}
+
+wq_status wq_rms_norm_i8(const void* x, int32_t type, const void* residual, const void* weight, float eps, int64_t n,
+                         int64_t k, void* sum, int8_t* codes, float* scales, void* stream) {
+  return norm_in("wq_rms_norm_i8", x, type, residual, weight, eps, n, k, sum, nullptr, codes, scales, true, stream);
+}
+
+size_t wq_rms_norm_grad_workspace_bytes(int64_t n, int64_t k, int32_t type) {
+  if (n <= 0 || k <= 0 || k > (1ll << 31) || n > (1ll << 42) / k || (type != WQ_TYPE_BF16 && type != WQ_TYPE_F32)) return 0;
+  return sizeof(float) * (size_t)wq::norm_grad_parts(n, k, type == WQ_TYPE_F32) * (size_t)k;
+}
+
+wq_status wq_rms_norm_grad(const void* dy, int32_t type, const void* d_sum, const void* sum, const void* weight,
+                           float eps, int64_t n, int64_t k, void* dx, float* d_weight, void* ws, size_t ws_bytes,
+                           void* stream) {
+  wq_status st = check_type(type, "wq_rms_norm_grad");
+  if (st != WQ_OK) return st;
+  if (!ws && ws_bytes) return fail(WQ_ERR_ARG, "wq_rms_norm_grad: a workspace size without a workspace");
+  if ((st = check_rows(n, k, "wq_rms_norm_grad")) != WQ_OK) return st;
+  if (!(eps >= 0.f) || eps > 3.4e38f) return fail(WQ_ERR_ARG, "wq_rms_norm_grad: eps must be finite and not negative");
+  if (n > 0 && (!dy || !sum || !weight || !dx)) return fail(WQ_ERR_ARG, "wq_rms_norm_grad: null pointer");
+  if (!aligned16(dy) || !aligned16(d_sum) || !aligned16(sum) || !aligned16(weight) || !aligned16(dx) ||
+      !aligned16(d_weight) || !aligned16(ws))
+    return fail(WQ_ERR_ALIGN, "wq_rms_norm_grad: an array is not 16-byte aligned");
+  const size_t need = d_weight ? wq_rms_norm_grad_workspace_bytes(n, k, type) : 0;
+  if (ws_bytes < need) return fail(WQ_ERR_WORKSPACE, "wq_rms_norm_grad: workspace %zu < %zu bytes", ws_bytes, need);
+  const int size = type_size(type);
+  const Span g(dy, n * k, size), ds(d_sum, n * k, size), r(sum, n * k, size), w(weight, k, size), x(dx, n * k, size);
+  const Span dw(d_weight, k, 4), tmp(need ? ws : nullptr, (int64_t)need, 1);
+  // dx may take d_sum's place: a thread reads an element before it writes it
+  if (overlaps(x, {g, r, w, dw, tmp}) || (dx != d_sum && overlaps(x, {ds})) || overlaps(dw, {g, ds, r, w, tmp}) ||
+      overlaps(tmp, {g, ds, r, w}))
+    return fail(WQ_ERR_ARG, "wq_rms_norm_grad: outputs or the workspace overlap inputs or each other");
+  return hip_status(wq::launch_norm_grad(dy, type == WQ_TYPE_F32, d_sum, sum, weight, eps, n, k, dx, d_weight,
+                                         static_cast<float*>(ws), static_cast<hipStream_t>(stream)),
+                    "wq_rms_norm_grad launch");
+}
+
+size_t wq_moe_balance_loss_workspace_bytes(int64_t t, int32_t experts) {
+  if (t <= 0 || experts <= 0 || experts > kMaxExperts || t > (1ll << 30)) return 0;
+  const int64_t wgs = wq::balance_workgroups(t, experts);
+  return wgs > 1 ? (size_t)wgs * (2 * (size_t)experts + 1) * 4 : 0;
+}
+
+wq_status wq_moe_balance_loss(const void* logits, int32_t type, const int32_t* topk_ids, int64_t t, int32_t topk,
+                              int32_t experts, float coefficient, float* loss, int32_t* counts, void* ws,
+                              size_t ws_bytes, void* stream) {
+  wq_status st = check_balance(type, t, topk, experts, "wq_moe_balance_loss");
+  if (st != WQ_OK) return st;
+  if (!ws && ws_bytes) return fail(WQ_ERR_ARG, "wq_moe_balance_loss: a workspace size without a workspace");
+  if (!loss || !counts || (t > 0 && (!logits || !topk_ids)))
+    return fail(WQ_ERR_ARG, "wq_moe_balance_loss: null pointer");
+  if (!aligned16(logits) || !aligned16(ws))
+    return fail(WQ_ERR_ALIGN, "wq_moe_balance_loss: logits and ws must be 16-byte aligned");
+  const size_t need = wq_moe_balance_loss_workspace_bytes(t, experts);
+  if (ws_bytes < need) return fail(WQ_ERR_WORKSPACE, "wq_moe_balance_loss: workspace %zu < %zu bytes", ws_bytes, need);
+  const Span z(logits, t * experts, type_size(type)), ids(topk_ids, t * topk, 4), l(loss, 1, 4);
+  const Span c(counts, experts + 1, 4), tmp(need ? ws : nullptr, (int64_t)need, 1);
+  if (overlaps(l, {z, ids, c, tmp}) || overlaps(c, {z, ids, tmp}) || overlaps(tmp, {z, ids}))
+    return fail(WQ_ERR_ARG, "wq_moe_balance_loss: outputs or the workspace overlap inputs or each other");
+  return hip_status(wq::launch_balance_loss(logits, type == WQ_TYPE_F32, topk_ids, t, topk, experts, coefficient, loss,
+                                            counts, ws, static_cast<hipStream_t>(stream)),
+                    "wq_moe_balance_loss launch");
+}
+
+wq_status wq_moe_balance_loss_grad(const void* logits, int32_t type, const int32_t* topk_ids, int64_t t, int32_t topk,
+                                   int32_t experts, float coefficient, const int32_t* counts, const float* d_loss,
+                                   void* d_logits, void* stream) {
+  wq_status st = check_balance(type, t, topk, experts, "wq_moe_balance_loss_grad");
+  if (st != WQ_OK) return st;
+  if (t == 0) return WQ_OK;
+  if (!logits || !topk_ids || !counts || !d_logits) return fail(WQ_ERR_ARG, "wq_moe_balance_loss_grad: null pointer");
+  if (!aligned16(logits) || !aligned16(d_logits))
+    return fail(WQ_ERR_ALIGN, "wq_moe_balance_loss_grad: logits and d_logits must be 16-byte aligned");
+  if (overlaps(Span(d_logits, t * experts, type_size(type)),
+               {Span(logits, t * experts, type_size(type)), Span(topk_ids, t * topk, 4), Span(counts, experts + 1, 4),
+                Span(d_loss, 1, 4)}))
+    return fail(WQ_ERR_ARG, "wq_moe_balance_loss_grad: d_logits overlaps an input");
+  return hip_status(wq::launch_balance_loss_grad(logits, type == WQ_TYPE_F32, topk_ids, t, topk, experts, coefficient,
+                                                 counts, d_loss, d_logits, static_cast<hipStream_t>(stream)),
+                    "wq_moe_balance_loss_grad launch");
 }
 
 }  // extern "C"

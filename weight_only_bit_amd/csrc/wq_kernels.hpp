@@ -94,11 +94,11 @@ hipError_t launch_ccq_encode(const float* w, int64_t n, int64_t k, int32_t zp, i
                              uint8_t* codes, uint8_t* qscale, float* super_scale,
                              float* code_scale, float* code_zero, hipStream_t stream);
 
-// A launch holds below 2^32 threads: grids of `wgs` workgroups of 256 in as many launches as that
+// A launch holds below 2^32 threads: grids of `wgs` workgroups of `threads` in as many launches as that
 // takes, launch(first workgroup, workgroups).
 template <class Launch>
-hipError_t launch_in_parts(int64_t wgs, Launch launch) {
-  constexpr int64_t most = (1ll << 24) - 1;
+hipError_t launch_in_parts(int64_t wgs, Launch launch, int threads = 256) {
+  const int64_t most = (1ll << 32) / threads - 1;
   for (int64_t first = 0; first < wgs; first += most) {
     launch(first, dim3((unsigned)(wgs - first < most ? wgs - first : most)));
     const hipError_t e = hipGetLastError();
@@ -127,6 +127,24 @@ struct MxArgs {
 };
 hipError_t launch_mx_product(int mode, const MxArgs& args, int64_t experts, hipStream_t stream);
 
+// Arguments of the products of two int8 operands.
+struct I8Args {
+  const int8_t* w0_codes;     // dense W / MoE gate / MoE down [experts][N][K]
+  const uint16_t* w0_scales;  // bf16 [experts][N]
+  const int8_t* w1_codes;     // MoE up (gate+up mode only)
+  const uint16_t* w1_scales;
+  const int8_t* x_codes;      // rows: dense x; gate+up: tokens; down: h in expert order
+  const float* x_scales;      // one per row
+  void* out;                  // dense y [M][N]; MoE [pairs][N] in expert order
+  int32_t out_f32;            // fp32 output instead of bf16 (not gate+up)
+  int32_t topk;
+  int64_t M;                  // dense rows; MoE: the largest number of pairs
+  int64_t N, K;
+  const int32_t* offsets;       // MoE: expert_offsets [experts + 1]
+  const int32_t* sorted_pairs;  // gate+up
+};
+hipError_t launch_i8_product(int mode, const I8Args& args, int64_t experts, hipStream_t stream);
+
 // Token dispatch (rows bf16, or fp32 where f32 is set; clear: rows that no pair has become zero).
 hipError_t launch_positions(const int32_t* ids, int64_t npairs, int32_t experts, const int32_t* offsets,
                             const int32_t* sorted_pairs, int32_t* positions, hipStream_t stream);
@@ -137,6 +155,28 @@ hipError_t launch_unpermute(const void* rows, int f32, const int32_t* positions,
 hipError_t launch_unpermute_grad(const void* dy, const void* rows, int f32, const int32_t* positions,
                                  const float* weights, int64_t t, int32_t topk, int64_t hidden,
                                  void* d_rows, float* d_weights, int clear, hipStream_t stream);
+
+// Rows of k values (bf16, or fp32 where f32 is set) to int8 with a scale per row: fp32, or bf16 for the
+// channels of a weight.
+hipError_t launch_quantize_i8(const void* x, int f32, int64_t n, int64_t k, int8_t* codes, void* scales,
+                              int scales_f32, hipStream_t stream);
+// The root-mean-square norm of x + residual (null: of x); with codes in int8, else y.
+hipError_t launch_norm(const void* x, int f32, const void* residual, const void* weight, float eps, int64_t n,
+                       int64_t k, void* sum, void* y, int8_t* codes, float* scales, hipStream_t stream);
+// Its gradients.  norm_grad_parts: rows of k floats that `parts` holds for the gradient of the weight.
+int64_t norm_grad_parts(int64_t n, int64_t k, int f32);
+hipError_t launch_norm_grad(const void* dy, int f32, const void* d_sum, const void* sum, const void* weight,
+                            float eps, int64_t n, int64_t k, void* dx, float* d_weight, float* parts,
+                            hipStream_t stream);
+
+// The routing's balance loss.  balance_workgroups: above one, `ws` holds for each of them `experts` floats, and
+// behind all of those experts + 1 int32.  t may be 0.
+int64_t balance_workgroups(int64_t t, int32_t experts);
+hipError_t launch_balance_loss(const void* logits, int f32, const int32_t* ids, int64_t t, int32_t topk, int32_t experts,
+                               float coefficient, float* loss, int32_t* counts, void* ws, hipStream_t stream);
+hipError_t launch_balance_loss_grad(const void* logits, int f32, const int32_t* ids, int64_t t, int32_t topk,
+                                    int32_t experts, float coefficient, const int32_t* counts, const float* d_loss,
+                                    void* d_logits, hipStream_t stream);
 
 // Rows of one tile of the tiled kernel.
 int tiled_rows();
