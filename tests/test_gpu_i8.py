@@ -50,10 +50,10 @@ LENGTHS = [1, 3, 7, 8, 63, 64, 511, 512, 1027, 1111, 2048, 4096, 4160, 8200, 163
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("k", LENGTHS)
-def test_quantize_rows(wq, dtype, k):
-    _say("quantize", dtype, k)
-    x = _values(np.random.default_rng(k), 5, k, dtype)
+@pytest.mark.parametrize("n,k", [(5, k) for k in LENGTHS] + [(300, k) for k in (72, 520, 700, 1111, 3001, 8200, 12000)])
+def test_quantize_rows(wq, dtype, n, k):
+    _say("quantize", dtype, n, k)
+    x = _values(np.random.default_rng(k), n, k, dtype)
     codes, a = i8.quantize(x.double().numpy())
     q = wq.wq_quantize_i8(x.cuda())
     assert np.array_equal(q.codes.cpu().numpy(), codes)

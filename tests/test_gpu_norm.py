@@ -10,9 +10,11 @@ import i8_testutil as i8
 pytestmark = pytest.mark.gpu
 
 EPS = 1e-6
-# one element, shorter than a piece, one wave's rows with and without a ragged end, several waves', and rows
-# that are read again (from 65537 bf16 or 32769 fp32 values on)
-LENGTHS = [1, 5, 8, 64, 513, 1024, 1111, 2048, 4096, 4099, 8192, 12000, 16384, 20001, 66000, 70003]
+# one element, shorter than a piece, a quarter wave's rows, one wave's with and without a ragged end, several
+# waves', and rows that are read again (from 65537 bf16 or 32769 fp32 values on)
+LENGTHS = [1, 5, 8, 64, 136, 513, 1024, 1111, 2048, 4096, 4099, 8192, 12000, 16384, 20001, 40000, 66000, 70003]
+# few rows, and (where that takes other kernels) more than there are CUs
+ROWS = [(5, k) for k in LENGTHS] + [(300, k) for k in (40, 136, 513, 700, 1111, 2048, 3001, 4099, 8192, 12000)]
 
 
 @pytest.fixture(scope="module")
@@ -48,12 +50,12 @@ def _stored(x, res):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("k", LENGTHS)
-def test_norm(wq, dtype, k):
+@pytest.mark.parametrize("n,k", ROWS)
+def test_norm(wq, dtype, n, k):
     import torch
 
-    print("norm", dtype, k, flush=True)
-    x, res, w = _inputs(5, k, dtype, k)
+    print("norm", dtype, n, k, flush=True)
+    x, res, w = _inputs(n, k, dtype, k)
     r = _stored(x, res)
     y, total = wq.wq_rms_norm(x.cuda(), w.cuda(), res.cuda(), eps=EPS)
     assert torch.equal(total.cpu(), r)
@@ -66,12 +68,12 @@ def test_norm(wq, dtype, k):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("k", LENGTHS)
-def test_norm_i8(wq, dtype, k):
+@pytest.mark.parametrize("n,k", ROWS)
+def test_norm_i8(wq, dtype, n, k):
     import torch
 
-    print("norm i8", dtype, k, flush=True)
-    x, res, w = _inputs(5, k, dtype, k + 1)
+    print("norm i8", dtype, n, k, flush=True)
+    x, res, w = _inputs(n, k, dtype, k + 1)
     r = _stored(x, res)
     rows, total = wq.wq_rms_norm_i8(x.cuda(), w.cuda(), res.cuda(), eps=EPS)
     assert torch.equal(total.cpu(), r)
@@ -141,7 +143,7 @@ def test_edges(wq, dtype):
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("n,k", [(1, 1), (3, 5), (1, 8192), (700, 64), (2100, 100), (513, 1024), (33, 1111), (700, 2050),
-                                 (40, 4096), (600, 8192), (9, 16390), (30, 40000), (5, 70003), (520, 33000)])
+                                 (40, 4096), (300, 700), (300, 3001), (600, 8192), (257, 12000), (9, 16390), (30, 40000), (5, 70003), (520, 33000)])
 def test_gradients(wq, dtype, n, k):
     print("gradients", dtype, n, k, flush=True)
     x, res, w = _inputs(n, k, dtype, 5)

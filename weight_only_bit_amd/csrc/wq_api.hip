@@ -1099,8 +1099,7 @@ wq_status wq_rms_norm_grad(const void* dy, int32_t type, const void* d_sum, cons
 
 size_t wq_moe_balance_loss_workspace_bytes(int64_t t, int32_t experts) {
   if (t <= 0 || experts <= 0 || experts > kMaxExperts || t > (1ll << 30)) return 0;
-  const int64_t wgs = wq::balance_workgroups(t, experts);
-  return wgs > 1 ? (size_t)wgs * (2 * (size_t)experts + 1) * 4 : 0;
+  return wq::balance_workspace_bytes(t, experts);
 }
 
 wq_status wq_moe_balance_loss(const void* logits, int32_t type, const int32_t* topk_ids, int64_t t, int32_t topk,

@@ -5,10 +5,13 @@
 //   d_logits_te = d_loss coefficient / T * p_te (share_e - sum_j share_j p_tj)
 //
 // Tokens whose ids all lie outside [0, E) are padding: they count nowhere, their logits are not used and
-// get a gradient of zero.  A token's E logits lie in a group of lanes, the least power of two from E on, or
-// a wave with V logits in each lane; a group takes every G-th token.  Counts are integers, the sums of p
-// meet in a fixed order: the same bits every run.
+// get a gradient of zero.  A token's E logits lie in a group of L lanes, the least power of two from E on, or in
+// a wave with V logits a lane (expert e in lane e % 64); a group takes U tokens at a time, whose loads are all on
+// their way before the first is used.  Counts are integers (their order does not matter), the sums of p meet in
+// a fixed order: the same bits every run.
 #include <hip/hip_runtime.h>
+
+#include <type_traits>
 
 #include "wq_kernels.hpp"
 #include "wq_rows.hpp"
@@ -18,6 +21,8 @@ namespace wq {
 namespace {
 
 constexpr int kTopE = 512;
+constexpr int kLossThreads = 1024, kLossWaves = kLossThreads / 64;  // few, large workgroups: each leaves a part
+constexpr int kGradThreads = 256;
 
 // e^x for x <= 0: 2^(x log2 e), the product's rounding and log2 e's own put right to first order.
 __device__ __forceinline__ float exp_of(float x) {
@@ -28,287 +33,337 @@ __device__ __forceinline__ float exp_of(float x) {
   return y > 0.f ? __builtin_fmaf(y, lo * 0.693147182f, y) : y;
 }
 
-// Sum and maximum over a group of `lanes` lanes, a power of two.
-__device__ __forceinline__ float group_sum(float v, int lanes) {
-  if (lanes == 64) return wave_sum(v);
-  for (int d = lanes >> 1; d >= 1; d >>= 1) v += __shfl_xor(v, d);
-  return v;
-}
-__device__ __forceinline__ float group_max(float v, int lanes) {
-  for (int d = lanes >> 1; d >= 1; d >>= 1) v = fmaxf(v, __shfl_xor(v, d));
-  return v;
-}
+constexpr int tokens_of(int V) { return V == 1 ? 4 : 2; }
 
-// Where a thread's logits lie: lane `in` of group `group` of the launch holds the experts in, in + 64, ...
-struct Place {
-  int lanes, in;
-  int64_t group, groups;
+// U tokens of a group: every G-th from `first` on.  Behind t the loads repeat the last token's.
+template <typename T, int L, int V>
+struct Tokens {
+  static constexpr int U = tokens_of(V);
+  float x[U][V];  // logits, then e^(z - max)
+  float inv[U];   // 1 / sum of them
+  int32_t id[U];  // this lane's first id
+  __device__ __forceinline__ void load(const T* logits, const int32_t* ids, int64_t t, int32_t topk, int32_t experts,
+                                       int64_t first, int64_t groups) {
+    const int in = threadIdx.x & (L - 1);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t tok = first + u * groups < t ? first + u * groups : t - 1;
+      id[u] = in < topk ? ids[tok * topk + in] : -1;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const int e = in + 64 * v;
+        x[u][v] = e < experts ? to_f32(logits[tok * experts + e]) : -INFINITY;
+      }
+    }
+  }
+  // Whether token u has a pair (every lane of the group knows); found(e) for each of this lane's.
+  template <class Found>
+  __device__ __forceinline__ bool pairs(int u, const int32_t* ids, int64_t t, int32_t topk, int32_t experts, int64_t first,
+                                        int64_t groups, Found found) {
+    bool any = (uint32_t)id[u] < (uint32_t)experts;
+    if (any) found(id[u]);
+    if (topk > L) {
+      const int64_t tok = first + u * groups < t ? first + u * groups : t - 1;
+      for (int32_t j = (threadIdx.x & (L - 1)) + L; j < topk; j += L) {
+        const int32_t e = ids[tok * topk + j];
+        if ((uint32_t)e < (uint32_t)experts) {
+          any = true;
+          found(e);
+        }
+      }
+    }
+    const uint64_t votes = __ballot(any);
+    if constexpr (L == 64) return votes != 0;
+    else return ((votes >> ((threadIdx.x & 63) & ~(L - 1))) & ((1ull << L) - 1)) != 0;
+  }
+  // A row of -inf has no probability anywhere: zeros.
+  __device__ __forceinline__ void softmax() {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      float top = x[u][0];
+#pragma unroll
+      for (int v = 1; v < V; ++v) top = fmaxf(top, x[u][v]);
+      top = wave_max<L>(top);
+      float sum = 0.f;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        // (a NaN is no maximum: its difference stays one, also beside -inf)
+        x[u][v] = top == -INFINITY && x[u][v] == top ? 0.f : exp_of(x[u][v] - top);
+        sum += x[u][v];
+      }
+      sum = wave_sum<L>(sum);
+      inv[u] = sum == 0.f ? 0.f : 1.f / sum;
+    }
+  }
 };
-__device__ __forceinline__ Place place(int32_t experts) {
-  Place p;
-  p.lanes = 1;
-  while (p.lanes < 64 && p.lanes < experts) p.lanes *= 2;
-  p.in = threadIdx.x & (p.lanes - 1);
-  const int each = 256 / p.lanes;
-  p.group = (int64_t)blockIdx.x * each + threadIdx.x / p.lanes;
-  p.groups = (int64_t)gridDim.x * each;
-  return p;
-}
 
-// Whether token t has a pair (all lanes of its group agree); found(e) for every pair of it.
-template <class Found>
-__device__ __forceinline__ bool token_pairs(const int32_t* ids, int64_t t, int32_t topk, int32_t experts, const Place& at,
-                                            Found found) {
-  bool any = false;
-  for (int32_t j = at.in; j < topk; j += at.lanes) {
-    const int32_t e = ids[t * topk + j];
-    if ((uint32_t)e < (uint32_t)experts) {
-      any = true;
-      found(e);
-    }
+// loss and counts[experts] from every thread's sum of c_e (its experts' sums of p) and of c_e.
+__device__ __forceinline__ void conclude(double dot, int64_t all, int64_t tokens, int32_t experts, float coefficient,
+                                         float* loss, double* meet, int64_t* meet_n) {
+  for (int d = 32; d >= 1; d >>= 1) {
+    dot += __shfl_xor(dot, d);
+    all += __shfl_xor(all, d);
   }
-  const uint64_t votes = __ballot(any);
-  if (at.lanes == 64) return votes != 0;
-  const int first = (threadIdx.x & 63) & ~(at.lanes - 1);
-  return ((votes >> first) & ((1ull << at.lanes) - 1)) != 0;
-}
-
-// The logits of token t, and e^(z - max) with the reciprocal of its sum.  A row of -inf has no probability
-// anywhere: zeros.
-template <typename T, int V>
-__device__ __forceinline__ float softmax(const T* logits, int64_t t, int32_t experts, const Place& at, float (&x)[V]) {
-  float top = -INFINITY;
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    const int e = at.in + 64 * v;
-    x[v] = e < experts ? to_f32(logits[t * experts + e]) : -INFINITY;
-    top = fmaxf(top, x[v]);
-  }
-  top = group_max(top, at.lanes);
-  float sum = 0.f;
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    // (a NaN is no maximum: its difference stays one, also beside -inf)
-    x[v] = top == -INFINITY && x[v] == top ? 0.f : exp_of(x[v] - top);
-    sum += x[v];
-  }
-  sum = group_sum(sum, at.lanes);
-  return sum == 0.f ? 0.f : 1.f / sum;
-}
-
-// The loss from `wgs` rows of probability sums [E] and counts [E + 1] (the last: tokens): threads
-// segment x expert, segments of rows in order, in fp64.
-__device__ __forceinline__ void finish(const float* probs, const int32_t* pairs, int32_t wgs, int32_t experts,
-                                       float coefficient, float* loss, int32_t* counts, double* meet, int64_t* meet_n) {
-  const int threads = blockDim.x, tid = threadIdx.x;
-  // sums of every column: experts, and the tokens behind them
-  for (int c0 = 0; c0 <= experts; c0 += threads) {
-    const int cols = experts + 1 - c0 < threads ? experts + 1 - c0 : threads;
-    const int segs = threads / cols, seg = tid / cols, c = c0 + tid % cols;
-    double p = 0.0;
-    int64_t n = 0;
-    if (seg < segs) {
-      const int32_t from = (int32_t)((int64_t)wgs * seg / segs), to = (int32_t)((int64_t)wgs * (seg + 1) / segs);
-      for (int32_t w = from; w < to; ++w) {
-        if (c < experts) p += (double)probs[(int64_t)w * experts + c];
-        n += pairs[(int64_t)w * (experts + 1) + c];
-      }
-    }
-    __syncthreads();
-    meet[tid] = p;
-    meet_n[tid] = n;
-    __syncthreads();
-    if (tid < cols) {
-      for (int s = 1; s < segs; ++s) {
-        p += meet[s * cols + tid];
-        n += meet_n[s * cols + tid];
-      }
-      counts[c] = (int32_t)n;
-    }
-    // (256 threads and more than 255 experts: several rounds, so what the loss needs is kept below)
-    __syncthreads();
-    if (tid < cols) {
-      meet[threads + c] = p;
-      meet_n[threads + c] = n;
-    }
+  if ((threadIdx.x & 63) == 0) {
+    meet[threadIdx.x >> 6] = dot;
+    meet_n[threadIdx.x >> 6] = all;
   }
   __syncthreads();
-  double dot = 0.0;
-  int64_t all = 0;
-  for (int e = tid; e < experts; e += threads) {
-    dot += (double)meet_n[threads + e] * meet[threads + e];
-    all += meet_n[threads + e];
+  if (threadIdx.x != 0) return;
+  dot = 0.0;
+  all = 0;
+  for (int w = 0; w < kLossWaves; ++w) {
+    dot += meet[w];
+    all += meet_n[w];
   }
-  meet[tid] = dot;
-  meet_n[tid] = all;
-  __syncthreads();
-  for (int d = threads / 2; d >= 1; d /= 2) {
-    if (tid < d) {
-      meet[tid] += meet[tid + d];
-      meet_n[tid] += meet_n[tid + d];
-    }
-    __syncthreads();
-  }
-  if (tid == 0) {
-    const int64_t tokens = meet_n[threads + experts];
-    // no token with a pair: no loss
-    *loss = tokens ? (float)((double)coefficient * experts * meet[0] / ((double)meet_n[0] * (double)tokens)) : 0.f;
-  }
+  // no token with a pair: no loss
+  *loss = tokens ? (float)((double)coefficient * experts * dot / ((double)all * (double)tokens)) : 0.f;
 }
 
-template <typename T, int V>
-__global__ __launch_bounds__(256) void balance_kernel(const T* __restrict__ logits, const int32_t* __restrict__ ids,
-                                                      int64_t t, int32_t topk, int32_t experts, float coefficient,
-                                                      float* __restrict__ probs, int32_t* __restrict__ pairs,
-                                                      float* __restrict__ loss, int32_t* __restrict__ counts) {
+// Floats (and int32) of a part: experts + 1, the last count the tokens, in whole pieces of 16 bytes.
+__host__ __device__ constexpr int32_t part_pitch(int32_t experts) { return (experts + 4) / 4 * 4; }
+
+template <typename T, int L, int V>
+__global__ __launch_bounds__(kLossThreads) void balance_kernel(const T* __restrict__ logits, const int32_t* __restrict__ ids,
+                                                               int64_t t, int32_t topk, int32_t experts, float coefficient,
+                                                               float* __restrict__ probs, int32_t* __restrict__ pairs,
+                                                               float* __restrict__ loss, int32_t* __restrict__ counts) {
   __shared__ int32_t hist[kTopE + 1];
-  __shared__ float sums[256 * V];
-  __shared__ float prob[kTopE];
-  __shared__ double meet[256 + kTopE + 1];
-  __shared__ int64_t meet_n[256 + kTopE + 1];
-  const int tid = threadIdx.x;
-  const Place at = place(experts);
-  for (int i = tid; i <= experts; i += 256) hist[i] = 0;
+  __shared__ float sums[kLossWaves][L < 64 ? L : 64 * V];
+  __shared__ double meet[kLossWaves];
+  __shared__ int64_t meet_n[kLossWaves];
+  constexpr int U = tokens_of(V);
+  const int tid = threadIdx.x, lane = tid & 63;
+  constexpr int each = kLossThreads / L;
+  const int64_t group = (int64_t)blockIdx.x * each + tid / L, groups = (int64_t)gridDim.x * each;
+  for (int i = tid; i <= experts; i += kLossThreads) hist[i] = 0;
   __syncthreads();
   float acc[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) acc[v] = 0.f;
   int32_t tokens = 0;
-  // whole waves go round together: the reductions take every lane
-  const int64_t first = at.group - (threadIdx.x & 63) / at.lanes;
-  for (int64_t t0 = 0; first + t0 < t; t0 += at.groups) {
-    const int64_t tok = at.group + t0 < t ? at.group + t0 : t - 1;
-    const bool mine = at.group + t0 < t;
-    const bool real = token_pairs(ids, tok, topk, experts, at, [&](int32_t e) __attribute__((always_inline)) {
-      if (mine) atomicAdd(&hist[e], 1);
-    }) && mine;
-    float x[V];
-    const float inv = softmax<T, V>(logits, tok, experts, at, x);
+  // whole waves go round together: the votes take every lane
+  for (int64_t t0 = group; t0 - lane / L < t; t0 += groups * U) {
+    Tokens<T, L, V> k;
+    k.load(logits, ids, t, topk, experts, t0, groups);
+    bool real[U];
 #pragma unroll
-    for (int v = 0; v < V; ++v) acc[v] += real ? x[v] * inv : 0.f;
-    if (real && at.in == 0) ++tokens;
+    for (int u = 0; u < U; ++u) {
+      const bool mine = t0 + u * groups < t;
+      real[u] = k.pairs(u, ids, t, topk, experts, t0, groups, [&](int32_t e) __attribute__((always_inline)) {
+        if (mine) atomicAdd(&hist[e], 1);
+      }) && mine;
+      if (real[u] && (tid & (L - 1)) == 0) ++tokens;
+    }
+    k.softmax();
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int v = 0; v < V; ++v) acc[v] += real[u] ? k.x[u][v] * k.inv[u] : 0.f;
   }
   if (tokens) atomicAdd(&hist[experts], tokens);
 #pragma unroll
-  for (int v = 0; v < V; ++v) sums[v * 256 + tid] = acc[v];
+  for (int v = 0; v < V; ++v) {
+    for (int d = L; d < 64; d <<= 1) acc[v] += __shfl_xor(acc[v], d);  // the wave's groups
+    if (lane < L) sums[tid >> 6][lane + 64 * v] = acc[v];
+  }
   __syncthreads();
-  // expert e: lane e % lanes of every group of the workgroup, in order
   const bool one = gridDim.x == 1;
-  for (int e = tid; e < experts; e += 256) {
+  float* const prob = probs + (int64_t)blockIdx.x * part_pitch(experts);
+  int32_t* const pair = pairs + (int64_t)blockIdx.x * part_pitch(experts);
+  double dot = 0.0;
+  int64_t all = 0;
+  for (int e = tid; e <= experts; e += kLossThreads) {
     float s = 0.f;
-    for (int g = 0; g < 256; g += at.lanes) s += sums[(e >> 6) * 256 + g + (e & (at.lanes - 1))];
-    if (one) prob[e] = s;
-    else probs[(int64_t)blockIdx.x * experts + e] = s;
+    if (e < experts)
+#pragma unroll
+      for (int w = 0; w < kLossWaves; ++w) s += sums[w][e];
+    const int32_t c = hist[e];
+    if (one) {
+      counts[e] = c;
+      if (e < experts) {
+        dot = (double)c * s;
+        all = c;
+      }
+    } else {
+      prob[e] = s;
+      pair[e] = c;
+    }
   }
-  if (!one) {
-    for (int e = tid; e <= experts; e += 256) pairs[(int64_t)blockIdx.x * (experts + 1) + e] = hist[e];
-    return;
+  if (one) conclude(dot, all, hist[experts], experts, coefficient, loss, meet, meet_n);
+}
+
+// The parts' sums: threads of four columns each, and as many of them as the workgroup holds beside each other
+// for segments of the parts, eight loads in flight; segments and parts in order, in fp64.
+__global__ __launch_bounds__(kLossThreads) void balance_finish_kernel(const float* __restrict__ probs,
+                                                                      const int32_t* __restrict__ pairs, int32_t wgs,
+                                                                      int32_t experts, float coefficient,
+                                                                      float* __restrict__ loss, int32_t* __restrict__ counts) {
+  __shared__ double col_p[kLossThreads][4];
+  __shared__ int64_t col_n[kLossThreads][4];
+  __shared__ double meet[kLossWaves];
+  __shared__ int64_t meet_n[kLossWaves];
+  __shared__ int64_t tokens;
+  const int32_t pitch = part_pitch(experts), cols = pitch / 4, segs = kLossThreads / cols;
+  const int tid = threadIdx.x, seg = tid / cols, c = tid % cols;
+  double p[4] = {0.0, 0.0, 0.0, 0.0};
+  int64_t n[4] = {0, 0, 0, 0};
+  if (seg < segs) {
+    const int32_t from = (int32_t)((int64_t)wgs * seg / segs), to = (int32_t)((int64_t)wgs * (seg + 1) / segs);
+    constexpr int U = 8;
+    for (int32_t w = from; w < to; w += U) {
+      f32x4 pv[U];
+      u32x4 nv[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int64_t at = (int64_t)(w + u < to ? w + u : w) * pitch + 4 * c;
+        pv[u] = *reinterpret_cast<const f32x4*>(probs + at);
+        nv[u] = *reinterpret_cast<const u32x4*>(pairs + at);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (w + u < to)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            p[i] += (double)pv[u][i];
+            n[i] += (int32_t)nv[u][i];
+          }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    col_p[tid][i] = p[i];
+    col_n[tid][i] = n[i];
   }
   __syncthreads();
-  finish(prob, hist, 1, experts, coefficient, loss, counts, meet, meet_n);
+  double dot = 0.0;
+  int64_t all = 0;
+  if (tid <= experts) {
+    double ps = 0.0;
+    int64_t ns = 0;
+    for (int s = 0; s < segs; ++s) {
+      ps += col_p[s * cols + tid / 4][tid % 4];
+      ns += col_n[s * cols + tid / 4][tid % 4];
+    }
+    counts[tid] = (int32_t)ns;
+    if (tid < experts) {
+      dot = (double)ns * ps;
+      all = ns;
+    } else {
+      tokens = ns;
+    }
+  }
+  __syncthreads();
+  conclude(dot, all, tokens, experts, coefficient, loss, meet, meet_n);
 }
 
-__global__ __launch_bounds__(1024) void balance_finish_kernel(const float* __restrict__ probs,
-                                                              const int32_t* __restrict__ pairs, int32_t wgs,
-                                                              int32_t experts, float coefficient,
-                                                              float* __restrict__ loss, int32_t* __restrict__ counts) {
-  __shared__ double meet[1024 + kTopE + 1];
-  __shared__ int64_t meet_n[1024 + kTopE + 1];
-  finish(probs, pairs, wgs, experts, coefficient, loss, counts, meet, meet_n);
-}
-
-template <typename T, int V>
-__global__ __launch_bounds__(256) void balance_grad_kernel(const T* __restrict__ logits, const int32_t* __restrict__ ids,
-                                                           int64_t t, int32_t topk, int32_t experts, float coefficient,
-                                                           const int32_t* __restrict__ counts,
-                                                           const float* __restrict__ d_loss, T* __restrict__ d_logits) {
-  const Place at = place(experts);
+template <typename T, int L, int V>
+__global__ __launch_bounds__(kGradThreads) void balance_grad_kernel(const T* __restrict__ logits,
+                                                                    const int32_t* __restrict__ ids, int64_t t, int32_t topk,
+                                                                    int32_t experts, float coefficient,
+                                                                    const int32_t* __restrict__ counts,
+                                                                    const float* __restrict__ d_loss,
+                                                                    T* __restrict__ d_logits) {
+  constexpr int U = tokens_of(V);
+  constexpr int each = kGradThreads / L;
+  const int lane = threadIdx.x & 63, in = threadIdx.x & (L - 1);
+  const int64_t group = (int64_t)blockIdx.x * each + threadIdx.x / L, groups = (int64_t)gridDim.x * each;
   float share[V];
   int64_t all = 0;
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    const int e = at.in + 64 * v;
+    const int e = in + 64 * v;
     const int32_t c = e < experts ? counts[e] : 0;
     share[v] = (float)c;
     all += c;
   }
-  for (int d = at.lanes >> 1; d >= 1; d >>= 1) all += __shfl_xor(all, d);
+  for (int d = L >> 1; d >= 1; d >>= 1) all += __shfl_xor(all, d);
   const int32_t tokens = counts[experts];
   const float scale = all > 0 ? (float)((double)experts / (double)all) : 0.f;
   const float slope = tokens > 0 ? coefficient / (float)tokens * (d_loss ? *d_loss : 1.f) : 0.f;
 #pragma unroll
   for (int v = 0; v < V; ++v) share[v] *= scale;
-  const int64_t first = at.group - (threadIdx.x & 63) / at.lanes;
-  for (int64_t t0 = 0; first + t0 < t; t0 += at.groups) {
-    const bool mine = at.group + t0 < t;
-    const int64_t tok = mine ? at.group + t0 : t - 1;
-    const bool real = token_pairs(ids, tok, topk, experts, at, [](int32_t) {});
-    float x[V];
-    const float inv = softmax<T, V>(logits, tok, experts, at, x);
-    float dot = 0.f;
+  for (int64_t t0 = group; t0 - lane / L < t; t0 += groups * U) {
+    Tokens<T, L, V> k;
+    k.load(logits, ids, t, topk, experts, t0, groups);
+    bool real[U];
 #pragma unroll
-    for (int v = 0; v < V; ++v) dot = __builtin_fmaf(share[v], x[v], dot);
-    dot = group_sum(dot, at.lanes) * inv;
-    if (!mine) continue;
+    for (int u = 0; u < U; ++u) real[u] = k.pairs(u, ids, t, topk, experts, t0, groups, [](int32_t) {});
+    k.softmax();
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int e = at.in + 64 * v;
-      if (e < experts)
-        d_logits[tok * experts + e] = from_f32<T>(real ? slope * (x[v] * inv) * (share[v] - dot) : 0.f);
+    for (int u = 0; u < U; ++u) {
+      float dot = 0.f;
+#pragma unroll
+      for (int v = 0; v < V; ++v) dot = __builtin_fmaf(share[v], k.x[u][v], dot);
+      dot = wave_sum<L>(dot) * k.inv[u];
+      const int64_t tok = t0 + u * groups;
+      if (tok >= t) continue;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const int e = in + 64 * v;
+        if (e < experts)
+          d_logits[tok * experts + e] = from_f32<T>(real[u] ? slope * (k.x[u][v] * k.inv[u]) * (share[v] - dot) : 0.f);
+      }
     }
   }
 }
 
-// Tokens that a workgroup of 256 takes at a time.
-int64_t tokens_at_a_time(int32_t experts) {
-  int lanes = 1;
-  while (lanes < 64 && lanes < experts) lanes *= 2;
-  return 256 / lanes;
+// run(L, V) for a number of experts.
+template <class Run>
+void with_lanes(int32_t experts, Run run) {
+#define WQ_LANES(L, V) run(std::integral_constant<int, L>{}, std::integral_constant<int, V>{})
+  if (experts <= 1) WQ_LANES(1, 1);
+  else if (experts <= 2) WQ_LANES(2, 1);
+  else if (experts <= 4) WQ_LANES(4, 1);
+  else if (experts <= 8) WQ_LANES(8, 1);
+  else if (experts <= 16) WQ_LANES(16, 1);
+  else if (experts <= 32) WQ_LANES(32, 1);
+  else if (experts <= 64) WQ_LANES(64, 1);
+  else if (experts <= 128) WQ_LANES(64, 2);
+  else if (experts <= 256) WQ_LANES(64, 4);
+  else WQ_LANES(64, 8);
+#undef WQ_LANES
 }
 
-template <typename T, int V>
-void loss_v(const T* logits, const int32_t* ids, int64_t t, int32_t topk, int32_t experts, float coefficient, float* probs,
-            int32_t* pairs, int64_t wgs, float* loss, int32_t* counts, hipStream_t s) {
-  hipLaunchKernelGGL((balance_kernel<T, V>), dim3((unsigned)wgs), dim3(256), 0, s, logits, ids, t, topk, experts,
-                     coefficient, probs, pairs, loss, counts);
-}
-template <typename T, int V>
-void grad_v(const T* logits, const int32_t* ids, int64_t t, int32_t topk, int32_t experts, float coefficient,
-            const int32_t* counts, const float* d_loss, T* d_logits, hipStream_t s) {
-  const int64_t all = (t + tokens_at_a_time(experts) - 1) / tokens_at_a_time(experts);
-  hipLaunchKernelGGL((balance_grad_kernel<T, V>), dim3((unsigned)(all < 2048 ? all : 2048)), dim3(256), 0, s, logits, ids,
-                     t, topk, experts, coefficient, counts, d_loss, d_logits);
+// Rounds of a workgroup of `threads` over t tokens.
+int64_t rounds(int64_t t, int32_t experts, int threads) {
+  int64_t n = 0;
+  with_lanes(experts, [&](auto l, auto v) {
+    const int64_t each = threads / decltype(l)::value * tokens_of(decltype(v)::value);
+    n = (t + each - 1) / each;
+  });
+  return n;
 }
 
 }  // namespace
 
-int64_t balance_workgroups(int64_t t, int32_t experts) {
-  const int64_t each = 4 * tokens_at_a_time(experts);  // four rounds
-  const int64_t all = (t + each - 1) / each;
-  return all < 1 ? 1 : all < 512 ? all : 512;
+static int64_t balance_workgroups(int64_t t, int32_t experts) {
+  const int64_t all = rounds(t, experts, kLossThreads);
+  return all <= 4 ? 1 : all < 256 ? all : 256;
+}
+
+size_t balance_workspace_bytes(int64_t t, int32_t experts) {
+  const int64_t wgs = balance_workgroups(t, experts);
+  return wgs > 1 ? (size_t)wgs * part_pitch(experts) * 8 : 0;
 }
 
 hipError_t launch_balance_loss(const void* logits, int f32, const int32_t* ids, int64_t t, int32_t topk, int32_t experts,
                                float coefficient, float* loss, int32_t* counts, void* ws, hipStream_t stream) {
   const int64_t wgs = balance_workgroups(t, experts);
   float* const probs = static_cast<float*>(ws);
-  int32_t* const pairs = wgs > 1 ? reinterpret_cast<int32_t*>(probs + wgs * experts) : nullptr;
-  auto run = [&](auto vc) {
-    constexpr int V = decltype(vc)::value;
+  int32_t* const pairs = reinterpret_cast<int32_t*>(probs + wgs * part_pitch(experts));
+  with_lanes(experts, [&](auto l, auto v) {
+    constexpr int L = decltype(l)::value, V = decltype(v)::value;
     if (f32)
-      loss_v<float, V>(static_cast<const float*>(logits), ids, t, topk, experts, coefficient, probs, pairs, wgs, loss,
-                       counts, stream);
+      hipLaunchKernelGGL((balance_kernel<float, L, V>), dim3((unsigned)wgs), dim3(kLossThreads), 0, stream,
+                         static_cast<const float*>(logits), ids, t, topk, experts, coefficient, probs, pairs, loss, counts);
     else
-      loss_v<uint16_t, V>(static_cast<const uint16_t*>(logits), ids, t, topk, experts, coefficient, probs, pairs, wgs,
-                          loss, counts, stream);
-  };
-  if (experts <= 64) run(std::integral_constant<int, 1>{});
-  else if (experts <= 128) run(std::integral_constant<int, 2>{});
-  else if (experts <= 256) run(std::integral_constant<int, 4>{});
-  else run(std::integral_constant<int, 8>{});
-  hipError_t e = hipGetLastError();
+      hipLaunchKernelGGL((balance_kernel<uint16_t, L, V>), dim3((unsigned)wgs), dim3(kLossThreads), 0, stream,
+                         static_cast<const uint16_t*>(logits), ids, t, topk, experts, coefficient, probs, pairs, loss, counts);
+  });
+  const hipError_t e = hipGetLastError();
   if (e != hipSuccess || wgs == 1) return e;
-  hipLaunchKernelGGL(balance_finish_kernel, dim3(1), dim3(1024), 0, stream, probs, pairs, (int32_t)wgs, experts,
+  hipLaunchKernelGGL(balance_finish_kernel, dim3(1), dim3(kLossThreads), 0, stream, probs, pairs, (int32_t)wgs, experts,
                      coefficient, loss, counts);
   return hipGetLastError();
 }
@@ -316,19 +371,18 @@ hipError_t launch_balance_loss(const void* logits, int f32, const int32_t* ids, 
 hipError_t launch_balance_loss_grad(const void* logits, int f32, const int32_t* ids, int64_t t, int32_t topk,
                                     int32_t experts, float coefficient, const int32_t* counts, const float* d_loss,
                                     void* d_logits, hipStream_t stream) {
-  auto run = [&](auto vc) {
-    constexpr int V = decltype(vc)::value;
+  const int64_t all = rounds(t, experts, kGradThreads), wgs = all < 2048 ? all : 2048;
+  with_lanes(experts, [&](auto l, auto v) {
+    constexpr int L = decltype(l)::value, V = decltype(v)::value;
     if (f32)
-      grad_v<float, V>(static_cast<const float*>(logits), ids, t, topk, experts, coefficient, counts, d_loss,
-                       static_cast<float*>(d_logits), stream);
+      hipLaunchKernelGGL((balance_grad_kernel<float, L, V>), dim3((unsigned)wgs), dim3(kGradThreads), 0, stream,
+                         static_cast<const float*>(logits), ids, t, topk, experts, coefficient, counts, d_loss,
+                         static_cast<float*>(d_logits));
     else
-      grad_v<uint16_t, V>(static_cast<const uint16_t*>(logits), ids, t, topk, experts, coefficient, counts, d_loss,
-                          static_cast<uint16_t*>(d_logits), stream);
-  };
-  if (experts <= 64) run(std::integral_constant<int, 1>{});
-  else if (experts <= 128) run(std::integral_constant<int, 2>{});
-  else if (experts <= 256) run(std::integral_constant<int, 4>{});
-  else run(std::integral_constant<int, 8>{});
+      hipLaunchKernelGGL((balance_grad_kernel<uint16_t, L, V>), dim3((unsigned)wgs), dim3(kGradThreads), 0, stream,
+                         static_cast<const uint16_t*>(logits), ids, t, topk, experts, coefficient, counts, d_loss,
+                         static_cast<uint16_t*>(d_logits));
+  });
   return hipGetLastError();
 }
 

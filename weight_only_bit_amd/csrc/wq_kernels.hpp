@@ -169,9 +169,8 @@ hipError_t launch_norm_grad(const void* dy, int f32, const void* d_sum, const vo
                             float eps, int64_t n, int64_t k, void* dx, float* d_weight, float* parts,
                             hipStream_t stream);
 
-// The routing's balance loss.  balance_workgroups: above one, `ws` holds for each of them `experts` floats, and
-// behind all of those experts + 1 int32.  t may be 0.
-int64_t balance_workgroups(int64_t t, int32_t experts);
+// The routing's balance loss; ws: balance_workspace_bytes.  t may be 0 in the loss.
+size_t balance_workspace_bytes(int64_t t, int32_t experts);
 hipError_t launch_balance_loss(const void* logits, int f32, const int32_t* ids, int64_t t, int32_t topk, int32_t experts,
                                float coefficient, float* loss, int32_t* counts, void* ws, hipStream_t stream);
 hipError_t launch_balance_loss_grad(const void* logits, int f32, const int32_t* ids, int64_t t, int32_t topk,

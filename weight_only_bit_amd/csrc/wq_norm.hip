@@ -8,8 +8,12 @@
 //             d_weight_j = sum over rows of dy_j r_j inv
 //
 // All of them are bound by memory.  A row is held in registers between the pass that sums it and the pass
-// that writes it, so it is read once; only rows beyond 65536 bf16 (32768 fp32) values are read again.
+// that writes it, so it is read once; only rows beyond 65536 bf16 (32768 fp32) values, in the gradient 16384
+// (8192), are read again.  4096 x 8192 bf16: norm 54 us (5.0 TB/s, a copy of 2 GiB 4.8), in int8 51 us (4.6), the
+// gradient 63 us (4.3, its parts included); 32 x 8192: 3.7, 4.1 and 6.6 us, of which a launch takes 1.6.
 #include <hip/hip_runtime.h>
+
+#include <type_traits>
 
 #include "wq_kernels.hpp"
 #include "wq_rows.hpp"
@@ -83,7 +87,7 @@ template <typename T, int LANES, int P, int OUT>
 __global__ __launch_bounds__(LANES < 256 ? 256 : LANES) void norm_kernel(const NormArgs a, int64_t first) {
   constexpr int E = 16 / (int)sizeof(T);
   constexpr bool I8 = OUT != OUT_NORM, NORM = OUT <= OUT_NORM_I8;
-  constexpr int WAVES = LANES / 64;
+  constexpr int WAVES = LANES < 64 ? 1 : LANES / 64;
   typedef typename Wide<T>::V V;
   typedef typename Wide<T>::M M;
   const int tid = LANES < 256 ? (int)threadIdx.x % LANES : (int)threadIdx.x;
@@ -162,8 +166,8 @@ __global__ __launch_bounds__(LANES < 256 ? 256 : LANES) void norm_kernel(const N
     if constexpr (I8) top = larger(top, magnitude(NORM ? (V)f * (V)to_f32(wt) : (V)f));
   }
 
-  if constexpr (NORM) ss = wave_sum(ss);
-  if constexpr (I8) top = wave_max(top);
+  if constexpr (NORM) ss = wave_sum<(LANES < 64 ? LANES : 64)>(ss);
+  if constexpr (I8) top = wave_max<(LANES < 64 ? LANES : 64)>(top);
   if constexpr (WAVES > 1) {
     __shared__ float ss_all[WAVES];
     __shared__ M top_all[WAVES];
@@ -275,7 +279,7 @@ struct NormGradArgs {
 template <typename T, int LANES, int P>
 __global__ __launch_bounds__(LANES < 256 ? 256 : LANES) void norm_grad_kernel(const NormGradArgs a) {
   constexpr int E = 16 / (int)sizeof(T);
-  constexpr int WAVES = LANES / 64, GROUPS = LANES < 256 ? 256 / LANES : 1;
+  constexpr int WAVES = LANES < 64 ? 1 : LANES / 64, GROUPS = LANES < 256 ? 256 / LANES : 1;
   const int tid = LANES < 256 ? (int)threadIdx.x % LANES : (int)threadIdx.x;
   const int group = LANES < 256 ? (int)threadIdx.x / LANES : 0;
   const int64_t k = a.k, pieces = k / E;
@@ -347,8 +351,8 @@ __global__ __launch_bounds__(LANES < 256 ? 256 : LANES) void norm_grad_kernel(co
       ss = __builtin_fmaf(rt, rt, ss);
       dot = __builtin_fmaf(gt * wt, rt, dot);
     }
-    ss = wave_sum(ss);
-    dot = wave_sum(dot);
+    ss = wave_sum<(LANES < 64 ? LANES : 64)>(ss);
+    dot = wave_sum<(LANES < 64 ? LANES : 64)>(dot);
     if constexpr (WAVES > 1) {
       if ((tid & 63) == 0) {
         ss_all[turn][tid >> 6] = ss;
@@ -431,83 +435,123 @@ __global__ __launch_bounds__(LANES < 256 ? 256 : LANES) void norm_grad_kernel(co
   if (tid < tail) part[tcol] = dwt;
 }
 
-// d_weight[c] = sum over the parts, four quarters of them in order and then the quarters: 64 columns a
-// workgroup, a wave for each quarter.
-__global__ __launch_bounds__(256) void norm_parts_kernel(const float* __restrict__ parts, int32_t count, int64_t k,
-                                                         float* __restrict__ out) {
-  __shared__ float meet[4][64];
+// d_weight[c] = sum over the parts: 64 columns a workgroup, a sixteenth of the parts a wave, in order, and then
+// the sixteenths.  Eight loads of a lane in flight: the parts have just been written, and with one at a time
+// (and four waves) their way back took longer than the kernel before (4096 x 8192: 35 us).
+constexpr int kPartWaves = 16;
+__global__ __launch_bounds__(64 * kPartWaves) void norm_parts_kernel(const float* __restrict__ parts, int32_t count,
+                                                                     int64_t k, float* __restrict__ out) {
+  __shared__ float meet[kPartWaves][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t c = (int64_t)blockIdx.x * 64 + lane;
-  const int32_t from = (int32_t)((int64_t)count * wave / 4), to = (int32_t)((int64_t)count * (wave + 1) / 4);
+  const int32_t from = (int32_t)((int64_t)count * wave / kPartWaves), to = (int32_t)((int64_t)count * (wave + 1) / kPartWaves);
   float s = 0.f;
-  if (c < k)
-    for (int32_t i = from; i < to; ++i) s += parts[i * k + c];
+  if (c < k) {
+    constexpr int U = 8;
+    for (int32_t i = from; i < to; i += U) {
+      float v[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) v[u] = i + u < to ? parts[(int64_t)(i + u) * k + c] : 0.f;
+#pragma unroll
+      for (int u = 0; u < U; ++u) s += v[u];
+    }
+  }
   meet[wave][lane] = s;
   __syncthreads();
-  if (wave == 0 && c < k) out[c] = (meet[0][lane] + meet[1][lane]) + (meet[2][lane] + meet[3][lane]);
+  if (wave == 0 && c < k) {
+    s = 0.f;
+#pragma unroll
+    for (int w = 0; w < kPartWaves; ++w) s += meet[w][lane];
+    out[c] = s;
+  }
 }
 
-// Lanes of a row and pieces of a lane for rows of `pieces` pieces (a ragged end counts as none).
-enum { SHAPE_64x1, SHAPE_64x2, SHAPE_256x1, SHAPE_256x2, SHAPE_256x4, SHAPE_256x8, SHAPE_1024x8, SHAPE_LOOP };
-int shape_of(int64_t pieces) {
-  if (pieces <= 64) return SHAPE_64x1;
-  if (pieces <= 128) return SHAPE_64x2;
-  if (pieces <= 256) return SHAPE_256x1;
-  if (pieces <= 512) return SHAPE_256x2;
-  if (pieces <= 1024) return SHAPE_256x4;
-  if (pieces <= 2048) return SHAPE_256x8;
-  if (pieces <= 8192) return SHAPE_1024x8;
-  return SHAPE_LOOP;
-}
-int rows_of_workgroup(int shape) { return shape <= SHAPE_64x2 ? 4 : 1; }
+// Lanes of a row x pieces of a lane.
+enum Shape { S16x1, S64x1, S64x2, S64x4, S256x1, S256x2, S1024x1, S1024x2, S1024x4, S1024x8, S_LOOP };
+int64_t pieces_of(int64_t k, int f32) { return k / (f32 ? 4 : 8); }
 
-template <typename T, int OUT, int LANES, int P>
-hipError_t norm_shape(const NormArgs& a, hipStream_t s) {
-  constexpr int threads = LANES < 256 ? 256 : LANES, rows = threads / LANES;
-  return launch_in_parts((a.n + rows - 1) / rows, [&](int64_t first, dim3 grid) {
-    hipLaunchKernelGGL((norm_kernel<T, LANES, P, OUT>), grid, dim3(threads), 0, s, a, first);
-  }, threads);
+// By what was measured on both sides (us, in a graph, rows from memory; norm, in int8, gradient):
+//   16 lanes for rows of up to 16 pieces, a wave above (16 / 64): 65536 x 128 bf16 15.5 / 25.1, 16.8 / 33.6, 21 / 45
+//   with at most a row for every CU the lanes that take a piece each (64x2 / 256x1: 1 x 1111 3.3 / 2.4;
+//     256x2 / 1024x1: 32 x 4096 3.0 / 2.6, 3.3 / 3.0, 5.9 / 5.6)
+//   with more rows few lanes, for a row of several waves waits for them all: 32768 x 1024 (64x2 / 256x1) 53.7 /
+//     50.5, 50.0 / 54.8, 59 / 101;  8192 x 4096 (256x2 / 1024x1) 51.9 / 54.0, 48.7 / 55.4, 61 / 71;  but 4096 x
+//     8192 (256x4 / 1024x1) 56.3 / 54.0, 52.5 / 51.2, 64 / 63
+//   129 to 256 pieces, 16384 x 2048 (64x4 / 256x1): 57.0 / 51.4, 53.9 / 47.9, 61 / 65
+//   long rows from registers as far as they hold them: 512 x 65536 (1024x8 / read again) 56 / 70, 60 / 64; the
+//     gradient holds three arrays and its columns' sums, up to 2048 pieces
+Shape shape_of(int64_t n, int64_t pieces, bool grad) {
+  if (pieces <= 16) return S16x1;
+  if (pieces <= 64) return S64x1;
+  if (n <= 256) {
+    if (pieces <= 256) return S256x1;
+    if (pieces <= 1024) return S1024x1;
+  }
+  if (pieces <= 128) return S64x2;
+  if (pieces <= 256) return grad ? S64x4 : S256x1;
+  if (pieces <= 512) return S256x2;
+  if (pieces <= 1024) return S1024x1;
+  if (pieces <= 2048) return S1024x2;
+  if (pieces <= 4096 && !grad) return S1024x4;
+  if (pieces <= 8192 && !grad) return S1024x8;
+  return S_LOOP;
 }
+Shape grad_shape_of(int64_t n, int64_t k, int f32) { return shape_of(n, pieces_of(k, f32), true); }
+
+// run(lanes, pieces) with the shape's constants; the gradient has no shapes above 2048 pieces, the norm no 64x4.
+template <bool GRAD, class Run>
+hipError_t with_shape(Shape s, Run run) {
+#define WQ_SHAPE(L, P) return run(std::integral_constant<int, L>{}, std::integral_constant<int, P>{})
+  switch (s) {
+    case S16x1: WQ_SHAPE(16, 1);
+    case S64x1: WQ_SHAPE(64, 1);
+    case S64x2: WQ_SHAPE(64, 2);
+    case S256x1: WQ_SHAPE(256, 1);
+    case S256x2: WQ_SHAPE(256, 2);
+    case S1024x1: WQ_SHAPE(1024, 1);
+    case S1024x2: WQ_SHAPE(1024, 2);
+    default: break;
+  }
+  if constexpr (GRAD) {
+    if (s == S64x4) WQ_SHAPE(64, 4);
+  } else {
+    if (s == S1024x4) WQ_SHAPE(1024, 4);
+    if (s == S1024x8) WQ_SHAPE(1024, 8);
+  }
+  WQ_SHAPE(1024, 0);
+#undef WQ_SHAPE
+}
+
 template <typename T, int OUT>
 hipError_t norm_t(const NormArgs& a, hipStream_t s) {
-  switch (shape_of(a.k / (16 / (int64_t)sizeof(T)))) {
-    case SHAPE_64x1: return norm_shape<T, OUT, 64, 1>(a, s);
-    case SHAPE_64x2: return norm_shape<T, OUT, 64, 2>(a, s);
-    case SHAPE_256x1: return norm_shape<T, OUT, 256, 1>(a, s);
-    case SHAPE_256x2: return norm_shape<T, OUT, 256, 2>(a, s);
-    case SHAPE_256x4: return norm_shape<T, OUT, 256, 4>(a, s);
-    case SHAPE_256x8: return norm_shape<T, OUT, 256, 8>(a, s);
-    case SHAPE_1024x8: return norm_shape<T, OUT, 1024, 8>(a, s);
-    default: return norm_shape<T, OUT, 1024, 0>(a, s);
-  }
+  return with_shape<false>(shape_of(a.n, pieces_of(a.k, sizeof(T) == 4), false), [&](auto lanes, auto pieces) {
+    constexpr int LANES = decltype(lanes)::value, P = decltype(pieces)::value;
+    constexpr int threads = LANES < 256 ? 256 : LANES, rows = threads / LANES;
+    return launch_in_parts((a.n + rows - 1) / rows, [&](int64_t first, dim3 grid) {
+      hipLaunchKernelGGL((norm_kernel<T, LANES, P, OUT>), grid, dim3(threads), 0, s, a, first);
+    }, threads);
+  });
 }
 template <int OUT>
 hipError_t norm_any(const NormArgs& a, int f32, hipStream_t s) {
   return f32 ? norm_t<float, OUT>(a, s) : norm_t<uint16_t, OUT>(a, s);
 }
 
-// Workgroups of the gradient: two a CU, fewer for few rows.
+// Workgroups of the gradient: as many as a CU holds at a time, for each leaves a row of parts (256, 512, 1024:
+// 4096 x 8192 63, 66, 72 us; 65536 x 512 85, 59, 64); fewer for few rows.
 int64_t grad_workgroups(int64_t n, int64_t k, int f32) {
-  const int rows = rows_of_workgroup(shape_of(k / (f32 ? 4 : 8)));
+  const Shape s = grad_shape_of(n, k, f32);
+  const int64_t rows = s == S16x1 ? 16 : s <= S64x4 ? 4 : 1, most = s >= S1024x1 ? 256 : 512;
   const int64_t all = (n + rows - 1) / rows;
-  return all < 512 ? all : 512;
-}
-template <typename T, int LANES, int P>
-void grad_shape(const NormGradArgs& a, int64_t wgs, hipStream_t s) {
-  hipLaunchKernelGGL((norm_grad_kernel<T, LANES, P>), dim3((unsigned)wgs), dim3(LANES < 256 ? 256 : LANES), 0, s, a);
+  return all < most ? all : most;
 }
 template <typename T>
-void grad_t(const NormGradArgs& a, int64_t wgs, hipStream_t s) {
-  switch (shape_of(a.k / (16 / (int64_t)sizeof(T)))) {
-    case SHAPE_64x1: return grad_shape<T, 64, 1>(a, wgs, s);
-    case SHAPE_64x2: return grad_shape<T, 64, 2>(a, wgs, s);
-    case SHAPE_256x1: return grad_shape<T, 256, 1>(a, wgs, s);
-    case SHAPE_256x2: return grad_shape<T, 256, 2>(a, wgs, s);
-    case SHAPE_256x4: return grad_shape<T, 256, 4>(a, wgs, s);
-    case SHAPE_256x8: return grad_shape<T, 256, 8>(a, wgs, s);
-    case SHAPE_1024x8: return grad_shape<T, 1024, 8>(a, wgs, s);
-    default: return grad_shape<T, 1024, 0>(a, wgs, s);
-  }
+hipError_t grad_t(const NormGradArgs& a, int64_t wgs, hipStream_t s) {
+  return with_shape<true>(grad_shape_of(a.n, a.k, sizeof(T) == 4), [&](auto lanes, auto pieces) {
+    constexpr int LANES = decltype(lanes)::value, P = decltype(pieces)::value;
+    hipLaunchKernelGGL((norm_grad_kernel<T, LANES, P>), dim3((unsigned)wgs), dim3(LANES < 256 ? 256 : LANES), 0, s, a);
+    return hipGetLastError();
+  });
 }
 
 }  // namespace
@@ -541,13 +585,11 @@ hipError_t launch_norm_grad(const void* dy, int f32, const void* d_sum, const vo
   if (wgs > 0) {
     // one workgroup's sums are the gradient
     const NormGradArgs a{dy, d_sum, sum, weight, dx, !d_weight ? nullptr : wgs > 1 ? parts : d_weight, eps, n, k};
-    if (f32) grad_t<float>(a, wgs, stream);
-    else grad_t<uint16_t>(a, wgs, stream);
-    const hipError_t e = hipGetLastError();
+    const hipError_t e = f32 ? grad_t<float>(a, wgs, stream) : grad_t<uint16_t>(a, wgs, stream);
     if (e != hipSuccess) return e;
   }
   if (!d_weight || wgs == 1) return hipSuccess;  // (no workgroup: no parts, zeros)
-  hipLaunchKernelGGL(norm_parts_kernel, dim3((unsigned)((k + 63) / 64)), dim3(256), 0, stream, parts, (int32_t)wgs, k,
+  hipLaunchKernelGGL(norm_parts_kernel, dim3((unsigned)((k + 63) / 64)), dim3(64 * kPartWaves), 0, stream, parts, (int32_t)wgs, k,
                      d_weight);
   return hipGetLastError();
 }

@@ -1,4 +1,5 @@
-// wq_wave.hpp -- sums and maxima over the lanes of a wave, every lane ending with the same bits.
+// wq_wave.hpp -- sums and maxima over groups of a wave's lanes, every lane ending with the same bits.  LANES: a
+// power of two, the lanes of a group.
 #pragma once
 #include "wq_device.hpp"
 
@@ -14,45 +15,49 @@ __device__ __forceinline__ uint32_t wave_partner(uint32_t v) {
   return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, ctrl, 0xF, 0xF, true);
 }
 
+// join(v, the partner's v) over the group; join must not depend on the order of its arguments.
+template <int LANES, class Join>
+__device__ __forceinline__ uint32_t wave_join(uint32_t v, Join join) {
+  if constexpr (LANES > 1) v = join(v, wave_partner<0>(v));
+  if constexpr (LANES > 2) v = join(v, wave_partner<1>(v));
+  if constexpr (LANES > 4) v = join(v, wave_partner<2>(v));
+  if constexpr (LANES > 8) v = join(v, wave_partner<3>(v));
+  if constexpr (LANES > 16) {  // the two of a swap are this lane's value and its partner's, in some order
+    const auto p = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    v = join((uint32_t)p[0], (uint32_t)p[1]);
+  }
+  if constexpr (LANES > 32) {
+    const auto p = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    v = join((uint32_t)p[0], (uint32_t)p[1]);
+  }
+  return v;
+}
+template <int LANES = 64>
 __device__ __forceinline__ float wave_sum(float v) {
-  v += __uint_as_float(wave_partner<0>(__float_as_uint(v)));
-  v += __uint_as_float(wave_partner<1>(__float_as_uint(v)));
-  v += __uint_as_float(wave_partner<2>(__float_as_uint(v)));
-  v += __uint_as_float(wave_partner<3>(__float_as_uint(v)));
-  const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-  v = __uint_as_float(a[0]) + __uint_as_float(a[1]);
-  const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-  return __uint_as_float(b[0]) + __uint_as_float(b[1]);
+  return __uint_as_float(wave_join<LANES>(__float_as_uint(v), [](uint32_t a, uint32_t b) __attribute__((always_inline)) {
+    return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
+  }));
+}
+// A NaN is passed over.
+template <int LANES = 64>
+__device__ __forceinline__ float wave_max(float v) {
+  return __uint_as_float(wave_join<LANES>(__float_as_uint(v), [](uint32_t a, uint32_t b) __attribute__((always_inline)) {
+    return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
+  }));
 }
 
 __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) { return a > b ? a : b; }
 __device__ __forceinline__ uint64_t larger(uint64_t a, uint64_t b) { return a > b ? a : b; }
 
+template <int LANES = 64>
 __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
-  v = larger(v, wave_partner<0>(v));
-  v = larger(v, wave_partner<1>(v));
-  v = larger(v, wave_partner<2>(v));
-  v = larger(v, wave_partner<3>(v));
-  const auto a = __builtin_amdgcn_permlane16_swap(v, v, false, false);
-  v = larger((uint32_t)a[0], (uint32_t)a[1]);
-  const auto b = __builtin_amdgcn_permlane32_swap(v, v, false, false);
-  return larger((uint32_t)b[0], (uint32_t)b[1]);
+  return wave_join<LANES>(v, [](uint32_t a, uint32_t b) __attribute__((always_inline)) { return larger(a, b); });
 }
-template <int STEP>
-__device__ __forceinline__ uint64_t wave_partner64(uint64_t v) {
-  return (uint64_t)wave_partner<STEP>((uint32_t)(v >> 32)) << 32 | wave_partner<STEP>((uint32_t)v);
-}
+template <int LANES = 64>
 __device__ __forceinline__ uint64_t wave_max(uint64_t v) {
-  v = larger(v, wave_partner64<0>(v));
-  v = larger(v, wave_partner64<1>(v));
-  v = larger(v, wave_partner64<2>(v));
-  v = larger(v, wave_partner64<3>(v));
-  const auto al = __builtin_amdgcn_permlane16_swap((uint32_t)v, (uint32_t)v, false, false);
-  const auto ah = __builtin_amdgcn_permlane16_swap((uint32_t)(v >> 32), (uint32_t)(v >> 32), false, false);
-  v = larger((uint64_t)ah[0] << 32 | (uint32_t)al[0], (uint64_t)ah[1] << 32 | (uint32_t)al[1]);
-  const auto bl = __builtin_amdgcn_permlane32_swap((uint32_t)v, (uint32_t)v, false, false);
-  const auto bh = __builtin_amdgcn_permlane32_swap((uint32_t)(v >> 32), (uint32_t)(v >> 32), false, false);
-  return larger((uint64_t)bh[0] << 32 | (uint32_t)bl[0], (uint64_t)bh[1] << 32 | (uint32_t)bl[1]);
+  const uint32_t hi = (uint32_t)(v >> 32), top = wave_max<LANES>(hi);
+  // among the lanes with the largest upper half the largest lower one
+  return (uint64_t)top << 32 | wave_max<LANES>(hi == top ? (uint32_t)v : 0u);
 }
 
 }  // namespace wq
