@@ -5,10 +5,8 @@
 //   d_logits_te = d_loss coefficient / T * p_te (share_e - sum_j share_j p_tj)
 //
 // Tokens whose ids all lie outside [0, E) are padding: they count nowhere, their logits are not used and
-// get a gradient of zero.  A token's E logits lie in a group of L lanes, the least power of two from E on, or in
-// a wave with V logits a lane (expert e in lane e % 64); a group takes U tokens at a time, whose loads are all on
-// their way before the first is used.  Counts are integers (their order does not matter), the sums of p meet in
-// a fixed order: the same bits every run.
+// get a gradient of zero.  Counts are integers (their order does not matter), the sums of p meet in a fixed
+// order: the same bits every run.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
@@ -24,78 +22,94 @@ constexpr int kTopE = 512;
 constexpr int kLossThreads = 1024, kLossWaves = kLossThreads / 64;  // few, large workgroups: each leaves a part
 constexpr int kGradThreads = 256;
 
-// e^x for x <= 0: 2^(x log2 e), the product's rounding and log2 e's own put right to first order.
-__device__ __forceinline__ float exp_of(float x) {
-  const float hi = x * 1.44269502f;
-  const float lo = __builtin_fmaf(x, 1.44269502f, -hi) + x * 1.92596299e-8f;
-  const float y = __builtin_amdgcn_exp2f(hi);
-  // far below the range lo is no number (x = -inf): y is zero there
-  return y > 0.f ? __builtin_fmaf(y, lo * 0.693147182f, y) : y;
-}
-
-constexpr int tokens_of(int V) { return V == 1 ? 4 : 2; }
-
-// U tokens of a group: every G-th from `first` on.  Behind t the loads repeat the last token's.
-template <typename T, int L, int V>
-struct Tokens {
-  static constexpr int U = tokens_of(V);
-  float x[U][V];  // logits, then e^(z - max)
-  float inv[U];   // 1 / sum of them
-  int32_t id[U];  // this lane's first id
-  __device__ __forceinline__ void load(const T* logits, const int32_t* ids, int64_t t, int32_t topk, int32_t experts,
-                                       int64_t first, int64_t groups) {
-    const int in = threadIdx.x & (L - 1);
+// A token's logits in a group of L lanes, each P pieces of 16 bytes: piece q of the row in lane q % L.  Values
+// behind E are -inf.
+template <typename T, int L, int P>
+struct Row {
+  static constexpr int PE = 16 / (int)sizeof(T), N = P * PE;
+  float x[P][PE];  // logits, then e^(z - max)
+  float inv;       // 1 / their sum
+  __device__ __forceinline__ static int expert(int p, int i) { return ((int)(threadIdx.x & (L - 1)) + L * p) * PE + i; }
+  __device__ __forceinline__ void load(const T* row, int32_t experts) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int64_t tok = first + u * groups < t ? first + u * groups : t - 1;
-      id[u] = in < topk ? ids[tok * topk + in] : -1;
+    for (int p = 0; p < P; ++p) {
+      const int e = expert(p, 0);
+      if (e + PE <= experts) {
+        unpack(load_piece(row + e), x[p]);
+      } else {
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const int e = in + 64 * v;
-        x[u][v] = e < experts ? to_f32(logits[tok * experts + e]) : -INFINITY;
+        for (int i = 0; i < PE; ++i) x[p][i] = e + i < experts ? to_f32(row[e + i]) : -INFINITY;
       }
     }
   }
-  // Whether token u has a pair (every lane of the group knows); found(e) for each of this lane's.
-  template <class Found>
-  __device__ __forceinline__ bool pairs(int u, const int32_t* ids, int64_t t, int32_t topk, int32_t experts, int64_t first,
-                                        int64_t groups, Found found) {
-    bool any = (uint32_t)id[u] < (uint32_t)experts;
-    if (any) found(id[u]);
-    if (topk > L) {
-      const int64_t tok = first + u * groups < t ? first + u * groups : t - 1;
-      for (int32_t j = (threadIdx.x & (L - 1)) + L; j < topk; j += L) {
-        const int32_t e = ids[tok * topk + j];
-        if ((uint32_t)e < (uint32_t)experts) {
-          any = true;
-          found(e);
-        }
-      }
+  // e^(z - max) as 2^((z - max) log2 e): the difference's rounding and the product's, |z - max| 2^-24 each,
+  // are the probabilities' error.  A row of -inf, as which padding counts, has no probability anywhere: zeros.
+  __device__ __forceinline__ void softmax(bool real) {
+    if (!real) {
+#pragma unroll
+      for (int p = 0; p < P; ++p)
+#pragma unroll
+        for (int i = 0; i < PE; ++i) x[p][i] = -INFINITY;
     }
-    const uint64_t votes = __ballot(any);
-    if constexpr (L == 64) return votes != 0;
-    else return ((votes >> ((threadIdx.x & 63) & ~(L - 1))) & ((1ull << L) - 1)) != 0;
-  }
-  // A row of -inf has no probability anywhere: zeros.
-  __device__ __forceinline__ void softmax() {
+    float top = x[0][0];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      float top = x[u][0];
+    for (int p = 0; p < P; ++p)
 #pragma unroll
-      for (int v = 1; v < V; ++v) top = fmaxf(top, x[u][v]);
-      top = wave_max<L>(top);
-      float sum = 0.f;
+      for (int i = 0; i < PE; ++i) top = fmaxf(top, x[p][i]);
+    top = wave_max<L>(top);  // (a NaN is no maximum, and its difference stays one)
+    if (top == -INFINITY) top = 0.f;
+    float sum = 0.f;
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        // (a NaN is no maximum: its difference stays one, also beside -inf)
-        x[u][v] = top == -INFINITY && x[u][v] == top ? 0.f : exp_of(x[u][v] - top);
-        sum += x[u][v];
+    for (int p = 0; p < P; ++p)
+#pragma unroll
+      for (int i = 0; i < PE; ++i) {
+        x[p][i] = __builtin_amdgcn_exp2f((x[p][i] - top) * 1.44269504f);
+        sum += x[p][i];
       }
-      sum = wave_sum<L>(sum);
-      inv[u] = sum == 0.f ? 0.f : 1.f / sum;
-    }
+    sum = wave_sum<L>(sum);
+    inv = sum == 0.f ? 0.f : 1.f / sum;
   }
 };
+
+// Whether a token has a pair (every lane of its group knows); found(e) for each of this lane's.  Four ids a lane
+// are on their way before the first is looked at.
+template <int L, class Found>
+__device__ __forceinline__ bool token_pairs(const int32_t* ids, int32_t topk, int32_t experts, Found found) {
+  bool any = false;
+  for (int32_t j0 = threadIdx.x & (L - 1); j0 < topk; j0 += 4 * L) {
+    int32_t id[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) id[q] = j0 + q * L < topk ? ids[j0 + q * L] : -1;
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if ((uint32_t)id[q] < (uint32_t)experts) {
+        any = true;
+        found(id[q]);
+      }
+  }
+  return wave_join<L>(any ? 1u : 0u, [](uint32_t a, uint32_t b) __attribute__((always_inline)) { return a | b; }) != 0;
+}
+
+// The sum over the lanes that hold the same place in the groups of L of a wave.
+template <int L>
+__device__ __forceinline__ float across(float v) {
+  const auto turned = [](float f, auto c) __attribute__((always_inline)) {
+    return __uint_as_float((uint32_t)__builtin_amdgcn_mov_dpp((int)__float_as_uint(f), decltype(c)::value, 0xF, 0xF, true));
+  };
+  if constexpr (L <= 1) v += turned(v, std::integral_constant<int, 0xB1>{});   // lane ^ 1
+  if constexpr (L <= 2) v += turned(v, std::integral_constant<int, 0x4E>{});   // lane ^ 2
+  if constexpr (L <= 8) v += turned(v, std::integral_constant<int, 0x128>{});  // 8 lanes on, in the 16
+  if constexpr (L <= 4) v += turned(v, std::integral_constant<int, 0x124>{});  // 4 lanes on
+  if constexpr (L <= 16) {
+    const auto p = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(p[0]) + __uint_as_float(p[1]);
+  }
+  if constexpr (L <= 32) {
+    const auto p = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(p[0]) + __uint_as_float(p[1]);
+  }
+  return v;
+}
 
 // loss and counts[experts] from every thread's sum of c_e (its experts' sums of p) and of c_e.
 __device__ __forceinline__ void conclude(double dot, int64_t all, int64_t tokens, int32_t experts, float coefficient,
@@ -123,50 +137,46 @@ __device__ __forceinline__ void conclude(double dot, int64_t all, int64_t tokens
 // Floats (and int32) of a part: experts + 1, the last count the tokens, in whole pieces of 16 bytes.
 __host__ __device__ constexpr int32_t part_pitch(int32_t experts) { return (experts + 4) / 4 * 4; }
 
-template <typename T, int L, int V>
+template <typename T, int L, int P>
 __global__ __launch_bounds__(kLossThreads) void balance_kernel(const T* __restrict__ logits, const int32_t* __restrict__ ids,
                                                                int64_t t, int32_t topk, int32_t experts, float coefficient,
                                                                float* __restrict__ probs, int32_t* __restrict__ pairs,
                                                                float* __restrict__ loss, int32_t* __restrict__ counts) {
+  typedef Row<T, L, P> R;
   __shared__ int32_t hist[kTopE + 1];
-  __shared__ float sums[kLossWaves][L < 64 ? L : 64 * V];
+  __shared__ float sums[kLossWaves][L * R::N];
   __shared__ double meet[kLossWaves];
   __shared__ int64_t meet_n[kLossWaves];
-  constexpr int U = tokens_of(V);
   const int tid = threadIdx.x, lane = tid & 63;
   constexpr int each = kLossThreads / L;
-  const int64_t group = (int64_t)blockIdx.x * each + tid / L, groups = (int64_t)gridDim.x * each;
   for (int i = tid; i <= experts; i += kLossThreads) hist[i] = 0;
   __syncthreads();
-  float acc[V];
+  float acc[P][R::PE];
 #pragma unroll
-  for (int v = 0; v < V; ++v) acc[v] = 0.f;
+  for (int p = 0; p < P; ++p)
+#pragma unroll
+    for (int i = 0; i < R::PE; ++i) acc[p][i] = 0.f;
   int32_t tokens = 0;
-  // whole waves go round together: the votes take every lane
-  for (int64_t t0 = group; t0 - lane / L < t; t0 += groups * U) {
-    Tokens<T, L, V> k;
-    k.load(logits, ids, t, topk, experts, t0, groups);
-    bool real[U];
+  for (int64_t tok = (int64_t)blockIdx.x * each + tid / L; tok < t; tok += (int64_t)gridDim.x * each) {
+    R r;
+    r.load(logits + tok * experts, experts);
+    const bool real = token_pairs<L>(ids + tok * topk, topk, experts,
+                                     [&](int32_t e) __attribute__((always_inline)) { atomicAdd(&hist[e], 1); });
+    r.softmax(real);
+    if (real && (tid & (L - 1)) == 0) ++tokens;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const bool mine = t0 + u * groups < t;
-      real[u] = k.pairs(u, ids, t, topk, experts, t0, groups, [&](int32_t e) __attribute__((always_inline)) {
-        if (mine) atomicAdd(&hist[e], 1);
-      }) && mine;
-      if (real[u] && (tid & (L - 1)) == 0) ++tokens;
-    }
-    k.softmax();
+    for (int p = 0; p < P; ++p)
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-      for (int v = 0; v < V; ++v) acc[v] += real[u] ? k.x[u][v] * k.inv[u] : 0.f;
+      for (int i = 0; i < R::PE; ++i) acc[p][i] = __builtin_fmaf(r.x[p][i], r.inv, acc[p][i]);
   }
   if (tokens) atomicAdd(&hist[experts], tokens);
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    for (int d = L; d < 64; d <<= 1) acc[v] += __shfl_xor(acc[v], d);  // the wave's groups
-    if (lane < L) sums[tid >> 6][lane + 64 * v] = acc[v];
-  }
+  for (int p = 0; p < P; ++p)
+#pragma unroll
+    for (int i = 0; i < R::PE; ++i) {
+      const float v = across<L>(acc[p][i]);
+      if (lane < L) sums[tid >> 6][R::expert(p, i)] = v;
+    }
   __syncthreads();
   const bool one = gridDim.x == 1;
   float* const prob = probs + (int64_t)blockIdx.x * part_pitch(experts);
@@ -193,24 +203,26 @@ __global__ __launch_bounds__(kLossThreads) void balance_kernel(const T* __restri
   if (one) conclude(dot, all, hist[experts], experts, coefficient, loss, meet, meet_n);
 }
 
-// The parts' sums: threads of four columns each, and as many of them as the workgroup holds beside each other
-// for segments of the parts, eight loads in flight; segments and parts in order, in fp64.
+// The parts' sums: a thread has four columns of a segment of eight parts (more where the workgroup has not that
+// many threads), whose loads are all on their way together; segments in order, in fp64.  (As many segments as
+// threads instead: 7 us where this takes 4, most of it adding them up.)
 __global__ __launch_bounds__(kLossThreads) void balance_finish_kernel(const float* __restrict__ probs,
                                                                       const int32_t* __restrict__ pairs, int32_t wgs,
                                                                       int32_t experts, float coefficient,
                                                                       float* __restrict__ loss, int32_t* __restrict__ counts) {
+  constexpr int U = 8;
   __shared__ double col_p[kLossThreads][4];
-  __shared__ int64_t col_n[kLossThreads][4];
+  __shared__ int32_t col_n[kLossThreads][4];
   __shared__ double meet[kLossWaves];
   __shared__ int64_t meet_n[kLossWaves];
-  __shared__ int64_t tokens;
-  const int32_t pitch = part_pitch(experts), cols = pitch / 4, segs = kLossThreads / cols;
+  __shared__ int32_t tokens;
+  const int32_t pitch = part_pitch(experts), cols = pitch / 4, most = kLossThreads / cols;
+  const int32_t segs = (wgs + U - 1) / U < most ? (wgs + U - 1) / U : most;
   const int tid = threadIdx.x, seg = tid / cols, c = tid % cols;
-  double p[4] = {0.0, 0.0, 0.0, 0.0};
-  int64_t n[4] = {0, 0, 0, 0};
   if (seg < segs) {
     const int32_t from = (int32_t)((int64_t)wgs * seg / segs), to = (int32_t)((int64_t)wgs * (seg + 1) / segs);
-    constexpr int U = 8;
+    double p[4] = {0.0, 0.0, 0.0, 0.0};
+    int32_t n[4] = {0, 0, 0, 0};  // at most 2^30 pairs in all
     for (int32_t w = from; w < to; w += U) {
       f32x4 pv[U];
       u32x4 nv[U];
@@ -229,23 +241,24 @@ __global__ __launch_bounds__(kLossThreads) void balance_finish_kernel(const floa
             n[i] += (int32_t)nv[u][i];
           }
     }
-  }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    col_p[tid][i] = p[i];
-    col_n[tid][i] = n[i];
+    for (int i = 0; i < 4; ++i) {
+      col_p[tid][i] = p[i];
+      col_n[tid][i] = n[i];
+    }
   }
   __syncthreads();
   double dot = 0.0;
   int64_t all = 0;
   if (tid <= experts) {
     double ps = 0.0;
-    int64_t ns = 0;
+    int32_t ns = 0;
+#pragma unroll 4
     for (int s = 0; s < segs; ++s) {
       ps += col_p[s * cols + tid / 4][tid % 4];
       ns += col_n[s * cols + tid / 4][tid % 4];
     }
-    counts[tid] = (int32_t)ns;
+    counts[tid] = ns;
     if (tid < experts) {
       dot = (double)ns * ps;
       all = ns;
@@ -257,89 +270,90 @@ __global__ __launch_bounds__(kLossThreads) void balance_finish_kernel(const floa
   conclude(dot, all, tokens, experts, coefficient, loss, meet, meet_n);
 }
 
-template <typename T, int L, int V>
+template <typename T, int L, int P>
 __global__ __launch_bounds__(kGradThreads) void balance_grad_kernel(const T* __restrict__ logits,
                                                                     const int32_t* __restrict__ ids, int64_t t, int32_t topk,
                                                                     int32_t experts, float coefficient,
                                                                     const int32_t* __restrict__ counts,
                                                                     const float* __restrict__ d_loss,
                                                                     T* __restrict__ d_logits) {
-  constexpr int U = tokens_of(V);
+  typedef Row<T, L, P> R;
   constexpr int each = kGradThreads / L;
-  const int lane = threadIdx.x & 63, in = threadIdx.x & (L - 1);
-  const int64_t group = (int64_t)blockIdx.x * each + threadIdx.x / L, groups = (int64_t)gridDim.x * each;
-  float share[V];
+  const int lane = threadIdx.x & 63;
+  // every wave adds up the counts by itself
   int64_t all = 0;
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    const int e = in + 64 * v;
-    const int32_t c = e < experts ? counts[e] : 0;
-    share[v] = (float)c;
-    all += c;
-  }
-  for (int d = L >> 1; d >= 1; d >>= 1) all += __shfl_xor(all, d);
-  const int32_t tokens = counts[experts];
+  for (int e = lane; e < experts; e += 64) all += counts[e];
+  for (int d = 32; d >= 1; d >>= 1) all += __shfl_xor(all, d);
   const float scale = all > 0 ? (float)((double)experts / (double)all) : 0.f;
+  float share[P][R::PE];
+#pragma unroll
+  for (int p = 0; p < P; ++p)
+#pragma unroll
+    for (int i = 0; i < R::PE; ++i) share[p][i] = R::expert(p, i) < experts ? (float)counts[R::expert(p, i)] * scale : 0.f;
+  const int32_t tokens = counts[experts];
   const float slope = tokens > 0 ? coefficient / (float)tokens * (d_loss ? *d_loss : 1.f) : 0.f;
+  for (int64_t tok = (int64_t)blockIdx.x * each + threadIdx.x / L; tok < t; tok += (int64_t)gridDim.x * each) {
+    R r;
+    r.load(logits + tok * experts, experts);
+    const bool real = token_pairs<L>(ids + tok * topk, topk, experts, [](int32_t) {});
+    r.softmax(real);
+    float dot = 0.f;
 #pragma unroll
-  for (int v = 0; v < V; ++v) share[v] *= scale;
-  for (int64_t t0 = group; t0 - lane / L < t; t0 += groups * U) {
-    Tokens<T, L, V> k;
-    k.load(logits, ids, t, topk, experts, t0, groups);
-    bool real[U];
+    for (int p = 0; p < P; ++p)
 #pragma unroll
-    for (int u = 0; u < U; ++u) real[u] = k.pairs(u, ids, t, topk, experts, t0, groups, [](int32_t) {});
-    k.softmax();
+      for (int i = 0; i < R::PE; ++i) dot = __builtin_fmaf(share[p][i], r.x[p][i], dot);
+    dot = wave_sum<L>(dot) * r.inv;
+    const float factor = slope * r.inv;
+    T* const out = d_logits + tok * experts;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      float dot = 0.f;
+    for (int p = 0; p < P; ++p) {
+      const int e = R::expert(p, 0);
+      float d[R::PE];
 #pragma unroll
-      for (int v = 0; v < V; ++v) dot = __builtin_fmaf(share[v], k.x[u][v], dot);
-      dot = wave_sum<L>(dot) * k.inv[u];
-      const int64_t tok = t0 + u * groups;
-      if (tok >= t) continue;
+      for (int i = 0; i < R::PE; ++i) d[i] = r.x[p][i] * factor * (share[p][i] - dot);
+      if (e + R::PE <= experts) {
+        store_piece(out + e, pack(d));
+      } else {
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const int e = in + 64 * v;
-        if (e < experts)
-          d_logits[tok * experts + e] = from_f32<T>(real[u] ? slope * (k.x[u][v] * k.inv[u]) * (share[v] - dot) : 0.f);
+        for (int i = 0; i < R::PE; ++i)
+          if (e + i < experts) out[e + i] = from_f32<T>(d[i]);
       }
     }
   }
 }
 
-// run(L, V) for a number of experts.
-template <class Run>
+// run(L, P) for a number of experts: 16 values a lane, fewer lanes than a row's pieces, so that a wave holds
+// several tokens and their sums and divisions are shared by more values.
+template <typename T, class Run>
 void with_lanes(int32_t experts, Run run) {
-#define WQ_LANES(L, V) run(std::integral_constant<int, L>{}, std::integral_constant<int, V>{})
-  if (experts <= 1) WQ_LANES(1, 1);
-  else if (experts <= 2) WQ_LANES(2, 1);
-  else if (experts <= 4) WQ_LANES(4, 1);
-  else if (experts <= 8) WQ_LANES(8, 1);
-  else if (experts <= 16) WQ_LANES(16, 1);
-  else if (experts <= 32) WQ_LANES(32, 1);
-  else if (experts <= 64) WQ_LANES(64, 1);
-  else if (experts <= 128) WQ_LANES(64, 2);
-  else if (experts <= 256) WQ_LANES(64, 4);
-  else WQ_LANES(64, 8);
+  constexpr int PE = 16 / (int)sizeof(T);
+#define WQ_LANES(L, P) run(std::integral_constant<int, L>{}, std::integral_constant<int, P>{})
+  if (experts <= PE) return WQ_LANES(1, 1);
+  if constexpr (PE == 4) {
+    if (experts <= 8) return WQ_LANES(1, 2);
+  }
+  constexpr int P = 16 / PE;
+  if (experts <= 16) WQ_LANES(1, P);
+  else if (experts <= 32) WQ_LANES(2, P);
+  else if (experts <= 64) WQ_LANES(4, P);
+  else if (experts <= 128) WQ_LANES(8, P);
+  else if (experts <= 256) WQ_LANES(16, P);
+  else WQ_LANES(32, P);
 #undef WQ_LANES
 }
 
 // Rounds of a workgroup of `threads` over t tokens.
 int64_t rounds(int64_t t, int32_t experts, int threads) {
-  int64_t n = 0;
-  with_lanes(experts, [&](auto l, auto v) {
-    const int64_t each = threads / decltype(l)::value * tokens_of(decltype(v)::value);
-    n = (t + each - 1) / each;
-  });
-  return n;
+  int lanes = 1;
+  while (16 * lanes < experts) lanes *= 2;
+  return (t * lanes + threads - 1) / threads;
 }
 
 }  // namespace
 
 static int64_t balance_workgroups(int64_t t, int32_t experts) {
   const int64_t all = rounds(t, experts, kLossThreads);
-  return all <= 4 ? 1 : all < 256 ? all : 256;
+  return all <= 2 ? 1 : all < 256 ? all : 256;
 }
 
 size_t balance_workspace_bytes(int64_t t, int32_t experts) {
@@ -352,15 +366,15 @@ hipError_t launch_balance_loss(const void* logits, int f32, const int32_t* ids, 
   const int64_t wgs = balance_workgroups(t, experts);
   float* const probs = static_cast<float*>(ws);
   int32_t* const pairs = reinterpret_cast<int32_t*>(probs + wgs * part_pitch(experts));
-  with_lanes(experts, [&](auto l, auto v) {
-    constexpr int L = decltype(l)::value, V = decltype(v)::value;
-    if (f32)
-      hipLaunchKernelGGL((balance_kernel<float, L, V>), dim3((unsigned)wgs), dim3(kLossThreads), 0, stream,
-                         static_cast<const float*>(logits), ids, t, topk, experts, coefficient, probs, pairs, loss, counts);
-    else
-      hipLaunchKernelGGL((balance_kernel<uint16_t, L, V>), dim3((unsigned)wgs), dim3(kLossThreads), 0, stream,
-                         static_cast<const uint16_t*>(logits), ids, t, topk, experts, coefficient, probs, pairs, loss, counts);
-  });
+  const auto run = [&](const auto* z) {
+    typedef std::remove_const_t<std::remove_pointer_t<decltype(z)>> T;
+    with_lanes<T>(experts, [&](auto l, auto p) {
+      hipLaunchKernelGGL((balance_kernel<T, decltype(l)::value, decltype(p)::value>), dim3((unsigned)wgs),
+                         dim3(kLossThreads), 0, stream, z, ids, t, topk, experts, coefficient, probs, pairs, loss, counts);
+    });
+  };
+  if (f32) run(static_cast<const float*>(logits));
+  else run(static_cast<const uint16_t*>(logits));
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || wgs == 1) return e;
   hipLaunchKernelGGL(balance_finish_kernel, dim3(1), dim3(kLossThreads), 0, stream, probs, pairs, (int32_t)wgs, experts,
@@ -372,17 +386,16 @@ hipError_t launch_balance_loss_grad(const void* logits, int f32, const int32_t* 
                                     int32_t experts, float coefficient, const int32_t* counts, const float* d_loss,
                                     void* d_logits, hipStream_t stream) {
   const int64_t all = rounds(t, experts, kGradThreads), wgs = all < 2048 ? all : 2048;
-  with_lanes(experts, [&](auto l, auto v) {
-    constexpr int L = decltype(l)::value, V = decltype(v)::value;
-    if (f32)
-      hipLaunchKernelGGL((balance_grad_kernel<float, L, V>), dim3((unsigned)wgs), dim3(kGradThreads), 0, stream,
-                         static_cast<const float*>(logits), ids, t, topk, experts, coefficient, counts, d_loss,
-                         static_cast<float*>(d_logits));
-    else
-      hipLaunchKernelGGL((balance_grad_kernel<uint16_t, L, V>), dim3((unsigned)wgs), dim3(kGradThreads), 0, stream,
-                         static_cast<const uint16_t*>(logits), ids, t, topk, experts, coefficient, counts, d_loss,
-                         static_cast<uint16_t*>(d_logits));
-  });
+  const auto run = [&](auto* d) {
+    typedef std::remove_pointer_t<decltype(d)> T;
+    with_lanes<T>(experts, [&](auto l, auto p) {
+      hipLaunchKernelGGL((balance_grad_kernel<T, decltype(l)::value, decltype(p)::value>), dim3((unsigned)wgs),
+                         dim3(kGradThreads), 0, stream, static_cast<const T*>(logits), ids, t, topk, experts, coefficient,
+                         counts, d_loss, d);
+    });
+  };
+  if (f32) run(static_cast<float*>(d_logits));
+  else run(static_cast<uint16_t*>(d_logits));
   return hipGetLastError();
 }
 
