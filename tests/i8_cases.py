@@ -4,8 +4,7 @@ runs them."""
 from collections import namedtuple
 
 # The names of csrc/wq_i8_select.hpp, in its order.
-KERNELS = ("I8_STREAM_16", "I8_STREAM_32", "I8_TILES_64", "I8_TILES_128", "I8_TILES_128x256", "I8_TILES_128x256_ONE",
-           "I8_TILES_256")
+KERNELS = ("I8_STREAM_16", "I8_STREAM_32", "I8_TILES_64", "I8_TILES_128", "I8_TILES_128x256", "I8_TILES_256")
 
 Dense = namedtuple("Dense", "kernel m n k")
 # n that no 16-byte piece divides, k whose last step or stage (256, 128) ends inside; the last row tile has at
@@ -15,9 +14,8 @@ DENSE = [Dense("I8_STREAM_16", 1, 1, 64), Dense("I8_STREAM_16", 9, 77, 576), Den
          Dense("I8_TILES_64", 513, 900, 1088), Dense("I8_TILES_64", 500, 901, 64),
          Dense("I8_TILES_128", 1300, 1701, 832), Dense("I8_TILES_128", 1380, 1700, 448),
          Dense("I8_TILES_128x256", 1440, 4100, 1344), Dense("I8_TILES_128x256", 1500, 4099, 320),
-         Dense("I8_TILES_128x256_ONE", 4111, 4097, 576), Dense("I8_TILES_128x256_ONE", 4170, 4096, 832),
          Dense("I8_TILES_256", 3100, 4097, 1088), Dense("I8_TILES_256", 3172, 4100, 1152),
-         Dense("I8_TILES_256", 3250, 4096, 1088)]
+         Dense("I8_TILES_256", 3250, 4096, 64), Dense("I8_TILES_256", 3250, 4096, 192)]
 
 # counts: every expert's rows, empty experts among them; the rest of the t * topk pairs are dropped
 Experts = namedtuple("Experts", "kernel gate_up t topk n k counts")
@@ -25,9 +23,9 @@ _FEW, _EIGHT, _THREE, _LONG = (0, 17, 1, 16, 3), (1, 64, 65, 128, 0, 100, 30, 5)
 EXPERTS = [Experts("I8_STREAM_16", True, 20, 2, 65, 576, _FEW), Experts("I8_STREAM_16", False, 20, 2, 130, 576, _FEW),
            Experts("I8_TILES_128", True, 165, 2, 350, 832, (64, 161, 65)),
            Experts("I8_TILES_128", False, 165, 2, 701, 832, (64, 161, 65)),
-           Experts("I8_TILES_128x256", True, 100, 4, 1501, 1088, _EIGHT),
-           Experts("I8_TILES_128x256", False, 100, 4, 2972, 1088, _EIGHT),
-           Experts("I8_TILES_128x256_ONE", True, 300, 2, 2350, 704, _THREE),
-           Experts("I8_TILES_128x256_ONE", False, 300, 2, 4701, 960, _THREE),
+           Experts("I8_TILES_128", True, 300, 2, 2350, 704, _THREE),
+           Experts("I8_TILES_128", False, 300, 2, 4701, 64, _THREE),
+           Experts("I8_TILES_128x256", True, 100, 4, 6101, 448, _EIGHT),
+           Experts("I8_TILES_128x256", False, 100, 4, 12101, 448, _EIGHT),
            Experts("I8_TILES_256", True, 700, 2, 7201, 1088, _LONG),
            Experts("I8_TILES_256", False, 700, 2, 14401, 1088, _LONG)]

@@ -25,26 +25,23 @@ __device__ __forceinline__ void store_out(void* out, int f32, int64_t at, float 
 
 // ---------------------------------------------------------------------------------------------
 // Few rows: the weights stream from memory straight into v_mfma_i32_16x16x64_i8 operands.  Lane l supplies
-// row l % 16 of A (column of B) and 16 codes; it receives D[4 (l / 16) + i][l % 16].  In a step of 256 along
-// k lane group q = l / 16 takes the codes 64 q .. 64 q + 63, 16 per instruction: 64 contiguous bytes.  Any
-// order of the k sum is the same product.
+// row l % 16 of A (column of B) and 16 codes; it receives D[4 (l / 16) + i][l % 16].  Instruction i
+// of a step of 256 along k takes 64 of them, lane group q = l / 16 the codes 16 q .. 16 q + 15: a load touches
+// one 64-byte line of every row.
 // ---------------------------------------------------------------------------------------------
 __device__ __forceinline__ i32x4 mfma16(const u32x4& a, const u32x4& b, const i32x4& c) {
   return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, a), __builtin_bit_cast(i32x4, b), c, 0, 0, 0);
 }
 
-// A lane's four pieces of a step, zeros behind the row's end (k is a multiple of 64: all or none).
+// A lane's four pieces of a step, zeros behind the row's end (k is a multiple of 64, a piece's 64 codes are all
+// there or none).  codes: the row's first piece of this lane.
 struct Part {
   u32x4 c[4];
 };
 __device__ __forceinline__ void load_part(Part& p, const int8_t* codes, int32_t at, int32_t k) {
-  if (at < k) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) p.c[i] = *reinterpret_cast<const u32x4*>(codes + at + 16 * i);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) p.c[i] = (u32x4){0, 0, 0, 0};
-  }
+  for (int i = 0; i < 4; ++i)
+    p.c[i] = at + 64 * i < k ? *reinterpret_cast<const u32x4*>(codes + at + 64 * i) : (u32x4){0, 0, 0, 0};
 }
 
 // One workgroup of KS waves computes 16 MT rows by 16 columns (gate+up: of both matrices); its waves split
@@ -76,10 +73,10 @@ __global__ __launch_bounds__(64 * KS) void i8_stream_kernel(const I8Args a) {
   const int64_t wr = e * N + (nvalid ? nrow : N - 1);
   const int8_t* wc[NM];
   float sw[NM];
-  wc[0] = a.w0_codes + wr * K;
+  wc[0] = a.w0_codes + wr * K + 16 * q;
   sw[0] = bf16_bits_to_f32(a.w0_scales[wr]);
   if constexpr (NM == 2) {
-    wc[1] = a.w1_codes + wr * K;
+    wc[1] = a.w1_codes + wr * K + 16 * q;
     sw[1] = bf16_bits_to_f32(a.w1_scales[wr]);
   }
 
@@ -92,7 +89,7 @@ __global__ __launch_bounds__(64 * KS) void i8_stream_kernel(const I8Args a) {
       const int64_t r = m_base + ms + (16 * t + nl < left ? 16 * t + nl : 0);
       int64_t src = r;
       if constexpr (MODE == MODE_GATEUP) src = a.sorted_pairs[r] / a.topk;
-      xc[t] = a.x_codes + src * K;
+      xc[t] = a.x_codes + src * K + 16 * q;
       sx[t] = a.x_scales[src];
     }
     i32x4 acc[NM][MT];
@@ -105,9 +102,9 @@ __global__ __launch_bounds__(64 * KS) void i8_stream_kernel(const I8Args a) {
     };
     auto load = [&](Step& p, int32_t s) __attribute__((always_inline)) {
 #pragma unroll
-      for (int j = 0; j < NM; ++j) load_part(p.w[j], wc[j], 256 * s + 64 * q, K);
+      for (int j = 0; j < NM; ++j) load_part(p.w[j], wc[j], 256 * s, K);
 #pragma unroll
-      for (int t = 0; t < MT; ++t) load_part(p.x[t], xc[t], 256 * s + 64 * q, K);
+      for (int t = 0; t < MT; ++t) load_part(p.x[t], xc[t], 256 * s, K);
     };
     auto multiply = [&](const Step& p) __attribute__((always_inline)) {
 #pragma unroll
@@ -181,10 +178,8 @@ hipError_t launch_stream(const I8Args& a, int64_t gy, int64_t gz, hipStream_t s)
 //     stage takes piece 4 h + s, so a lane's four pieces are 64 contiguous bytes.
 //   * Rows of a stage are 128 bytes in LDS, 16-byte piece p of row r in slot p ^ (r / 2 % 8), which keeps
 //     the fragment reads free of bank conflicts; 8 lanes load a row.
-//   * Two buffers, one workgroup per CU (256 x 256): codes pass through registers, which hold a third stage
-//     on its way, so loads and LDS writes spread over the whole stage.
-//   * One buffer, two workgroups per CU (128 x 256): the next stage is copied without registers while the
-//     other workgroup multiplies, which also covers a tile's first loads and its stores.
+//   * Two buffers; codes pass through registers, which hold a third stage on its way, so loads and LDS writes
+//     spread over the whole stage.
 //   * The next slice's fragments are read under the current slice's MFMAs; the last slice of a stage is
 //     multiplied after the barrier that ends the stage, over the next stage's first reads.
 //   * The scales of the tile's rows and channels go to LDS at its start and meet the sums at its end.
@@ -262,7 +257,7 @@ __device__ __forceinline__ void store_blocks(void* out, int64_t stride, int64_t 
   }
 }
 // Rows row0 .. row0 + rows - 1 (at most 64 WM) of expert e, columns of tile ctile.
-template <int MODE, int WM, int WN, int BUFS>
+template <int MODE, int WM, int WN>
 __device__ __forceinline__ void i8_tile(const I8Args& a, const TileLds& lds, int64_t e, int64_t row0,
                                         int64_t rows, int64_t ctile) {
   constexpr int XR = 64 * WM, WR = 64 * WN;                   // rows of a stage
@@ -292,8 +287,8 @@ __device__ __forceinline__ void i8_tile(const I8Args& a, const TileLds& lds, int
   };
 
   // load role: load i of wave w brings stage rows 32 i + 8 w .. + 7, lane l the piece for its row's
-  // slot l % 8.  Loads go through buffer resources: a uniform base for the 32 rows and the stage, and
-  // a lane offset that is the same for every load (gate+up: one per row of tokens); rows behind the
+  // slot l % 8.  Loads go through buffer resources: a uniform base for the 32 rows, and a lane
+  // offset that is the same for every load (gate+up: one per row of tokens) plus the stage's; rows behind the
   // tile's or the matrix's end lie out of range and read zeros.
   const int piece = (lane & 7) ^ ((4 * wave + (lane >> 4)) & 7);
   const uint32_t off = (uint32_t)((8 * wave + (lane >> 3)) * (uint32_t)K + piece * 16);
@@ -311,13 +306,11 @@ __device__ __forceinline__ void i8_tile(const I8Args& a, const TileLds& lds, int
   constexpr int NX = 2 * WM, NC = 2 * WM + 2 * WN;
   auto load_codes = [&](int32_t g, int i, auto do_load) __attribute__((always_inline)) {
     const int32_t gc = g < last ? g : last;  // stages behind the last one load it again
-    const uint32_t out = gc == last && behind ? 0x7FFFFFF0u : 0u;
-    const int32_t at = gc * kStageBytes;
+    const uint32_t at = (uint32_t)gc * kStageBytes, out = gc == last && behind ? 0x7FFFFFF0u : 0u;
+    // the resources stay as they are from stage to stage; ranges are below 2^31 - 1024 (checked on the host)
     auto load = [&](const int8_t* base, int32_t bytes, uint32_t lane_off) __attribute__((always_inline)) {
-      const int32_t left = bytes - at;  // ranges are below 2^31 - 1024 (checked on the host)
-      do_load(__builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t*>(base + at), (short)0, left > 0 ? left : 0,
-                                                0x00020000),
-              (int)(lane_off | out));
+      do_load(__builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t*>(base), (short)0, bytes > 0 ? bytes : 0, 0x00020000),
+              (int)((lane_off + at) | out));
     };
     if (i < NX) {
       if constexpr (MODE == MODE_GATEUP)
@@ -337,9 +330,9 @@ __device__ __forceinline__ void i8_tile(const I8Args& a, const TileLds& lds, int
     return i < NX ? lds.x[ST] + (32 * i + 8 * wave) * kStageBytes
                   : lds.w[ST] + (32 * (i - NX) + 8 * wave) * kStageBytes;
   };
-  // Two buffers: a stage's codes pass through NC registers of 16 bytes per lane, in four groups: fetch
-  // loads group q of stage g, put writes it to a buffer.
-  u32x4 held[BUFS == 2 ? NC : 1];
+  // A stage's codes pass through NC registers of 16 bytes per lane, in four groups: fetch loads group q of
+  // stage g, put writes it to a buffer.
+  u32x4 held[NC];
   auto fetch_to = [&](u32x4* to, int32_t g, auto qc) __attribute__((always_inline)) {
     constexpr int Q = decltype(qc)::value;
 #pragma unroll
@@ -356,15 +349,6 @@ __device__ __forceinline__ void i8_tile(const I8Args& a, const TileLds& lds, int
   };
   auto fetch = [&](int32_t g, auto qc) __attribute__((always_inline)) { fetch_to(held, g, qc); };
   auto put = [&](auto qc, auto stc) __attribute__((always_inline)) { put_from(held, qc, stc); };
-  // One buffer: copied to LDS without registers.
-  auto copy = [&](int32_t g) __attribute__((always_inline)) {
-#pragma unroll
-    for (int i = 0; i < NC; ++i)
-      load_codes(g, i, [&](__amdgpu_buffer_rsrc_t r, int at) __attribute__((always_inline)) {
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(
-            r, (__attribute__((address_space(3))) void*)stage_rows(i, std::integral_constant<int, 0>{}), 16, at, 0, 0, 0);
-      });
-  };
   auto load_scales = [&]() __attribute__((always_inline)) {
     for (int r = tid; r < XR; r += 256) lds.sx[r] = a.x_scales[token_row(r)];
     for (int r = tid; r < WR; r += 256) {
@@ -410,10 +394,10 @@ __device__ __forceinline__ void i8_tile(const I8Args& a, const TileLds& lds, int
   constexpr std::integral_constant<int, 2> c2{};
   constexpr std::integral_constant<int, 3> c3{};
 
-  // ---- prologue: stage 0 written and the next on its way; with two buffers the first group of
-  // stage 1 is written, too, and that of stage 2 on its way; stage 0's first slice read ----
+  // ---- prologue: stage 0 and the first group of stage 1 written, the rest of stage 1 and the first group of
+  // stage 2 on their way; stage 0's first slice read ----
   Frag X;
-  if constexpr (BUFS == 2) {
+  {
     u32x4 early[NC];
     fetch_to(early, 0, c0);
     fetch_to(early, 0, c1);
@@ -432,11 +416,6 @@ __device__ __forceinline__ void i8_tile(const I8Args& a, const TileLds& lds, int
     fetch(2, c0);
     __syncthreads();
     read(X, 0, c0);
-  } else {
-    copy(0);
-    load_scales();
-    __builtin_amdgcn_s_waitcnt(0);  // the copies to LDS, too
-    __syncthreads();
   }
 
   // ---- stage g in buffers ST = g % 2 ----
@@ -490,52 +469,12 @@ __device__ __forceinline__ void i8_tile(const I8Args& a, const TileLds& lds, int
     mma(Y);
     interleave();
   };
-  // One buffer: once every wave's fragments of the last slice are in registers the next stage is
-  // copied over it; the CU's second workgroup multiplies meanwhile.
-  auto stage1 = [&](int32_t g) __attribute__((always_inline)) {
-    constexpr int NF = WM * WN;
-    constexpr int NR = WM + WN;
-    Frag Y;
-    auto reads = [&]() __attribute__((always_inline)) {
-#pragma unroll
-      for (int i = 0; i < NF; ++i) {
-        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-        if (i < NR) __builtin_amdgcn_sched_group_barrier(0x100, NF >= NR ? 1 : NR, 0);
-      }
-      __builtin_amdgcn_sched_barrier(0);
-    };
-    __builtin_amdgcn_sched_barrier(0);
-    read(X, 0, c0);
-    __builtin_amdgcn_sched_barrier(0);
-    read(Y, 1, c0);
-    mma(X);
-    reads();
-    read(X, 2, c0);
-    mma(Y);
-    reads();
-    read(Y, 3, c0);
-    mma(X);
-    reads();
-    __builtin_amdgcn_s_waitcnt(0xC07F);  // this wave's reads of the stage have returned
-    __builtin_amdgcn_s_barrier();
-    __builtin_amdgcn_sched_barrier(0);
-    copy(g + 1);
-    __builtin_amdgcn_sched_barrier(0);
-    mma(Y);
-    __builtin_amdgcn_s_waitcnt(0);  // the next stage is written
-    __builtin_amdgcn_s_barrier();
-    __builtin_amdgcn_sched_barrier(0);
-  };
   int32_t g = 0;
-  if constexpr (BUFS == 2) {
-    for (; g + 1 < steps; g += 2) {
-      stage(g, c0);
-      stage(g + 1, c1);
-    }
-    if (g < steps) stage(g, c0);
-  } else {
-    for (; g < steps; ++g) stage1(g);
+  for (; g + 1 < steps; g += 2) {
+    stage(g, c0);
+    stage(g + 1, c1);
   }
+  if (g < steps) stage(g, c0);
 
   // ---- epilogue, straight from registers ----
   float sx[WM];
@@ -560,17 +499,15 @@ __device__ __forceinline__ void i8_tile(const I8Args& a, const TileLds& lds, int
 }
 
 // WM: the largest tile's; a tile with few rows left takes a smaller one.
-template <int MODE, int WM, int WN, int BUFS>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(BUFS == 1 ? 2 : 1, BUFS == 1 ? 2 : WM * WN >= 8 ? 1 : 2)))
+template <int MODE, int WM, int WN>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, WM * WN >= 8 ? 1 : 2)))
 void i8_tiled_kernel(const I8Args a, int32_t experts) {
   constexpr int XR = 64 * WM, WR = 64 * WN;
-  __shared__ __attribute__((aligned(16))) uint8_t codes0[(BUFS == 1 ? XR + WR : XR) * kStageBytes];
-  __shared__ __attribute__((aligned(16))) uint8_t x1[BUFS == 1 ? 16 : XR * kStageBytes];
-  __shared__ __attribute__((aligned(16))) uint8_t w0[BUFS == 1 ? 16 : WR * kStageBytes];
-  __shared__ __attribute__((aligned(16))) uint8_t w1[BUFS == 1 ? 16 : WR * kStageBytes];
+  // (arrays apart: the compiler tells them apart, and waits for no write to the other buffer)
+  __shared__ __attribute__((aligned(16))) uint8_t x0[XR * kStageBytes], x1[XR * kStageBytes];
+  __shared__ __attribute__((aligned(16))) uint8_t w0[WR * kStageBytes], w1[WR * kStageBytes];
   __shared__ __attribute__((aligned(16))) float sx[XR], sw[WR];
-  // (two-buffer arrays apart: the compiler tells them apart, and waits for no write to the other)
-  const TileLds lds{{codes0, x1}, {BUFS == 1 ? codes0 + XR * kStageBytes : w0, w1}, sx, sw};
+  const TileLds lds{{x0, x1}, {w0, w1}, sx, sw};
   constexpr int64_t cols = MODE == MODE_GATEUP ? 32 * WN : 64 * WN;
   const int64_t col_tiles = (a.N + cols - 1) / cols;
   int64_t r, c, e = 0, row0, rows;
@@ -584,18 +521,18 @@ void i8_tiled_kernel(const I8Args a, int32_t experts) {
     tiles.find((int32_t)r, e, row0, rows);
   }
   if constexpr (WM == 4) {
-    if (rows > 128) i8_tile<MODE, 4, WN, BUFS>(a, lds, e, row0, rows, c);
-    else if (rows > 64) i8_tile<MODE, 2, WN, BUFS>(a, lds, e, row0, rows, c);
-    else i8_tile<MODE, 1, WN, BUFS>(a, lds, e, row0, rows, c);
+    if (rows > 128) i8_tile<MODE, 4, WN>(a, lds, e, row0, rows, c);
+    else if (rows > 64) i8_tile<MODE, 2, WN>(a, lds, e, row0, rows, c);
+    else i8_tile<MODE, 1, WN>(a, lds, e, row0, rows, c);
   } else if constexpr (WM == 2) {
-    if (rows > 64) i8_tile<MODE, 2, WN, BUFS>(a, lds, e, row0, rows, c);
-    else i8_tile<MODE, 1, WN, BUFS>(a, lds, e, row0, rows, c);
+    if (rows > 64) i8_tile<MODE, 2, WN>(a, lds, e, row0, rows, c);
+    else i8_tile<MODE, 1, WN>(a, lds, e, row0, rows, c);
   } else {
-    i8_tile<MODE, 1, WN, BUFS>(a, lds, e, row0, rows, c);
+    i8_tile<MODE, 1, WN>(a, lds, e, row0, rows, c);
   }
 }
 
-template <int MODE, int WM, int WN, int BUFS>
+template <int MODE, int WM, int WN>
 hipError_t launch_tiles(const I8Args& a, int64_t experts, hipStream_t s) {
   constexpr int64_t cols = MODE == MODE_GATEUP ? 32 * WN : 64 * WN;
   constexpr int64_t size = 64 * WM;
@@ -603,7 +540,7 @@ hipError_t launch_tiles(const I8Args& a, int64_t experts, hipStream_t s) {
   const int64_t row_tiles = (a.M + size - 1) / size + (MODE == MODE_DENSE ? 0 : experts);
   const int64_t wgs = (row_tiles * ((a.N + cols - 1) / cols) + 7) / 8 * 8;
   if (wgs >= (1ll << 24)) return hipErrorInvalidValue;
-  hipLaunchKernelGGL((i8_tiled_kernel<MODE, WM, WN, BUFS>), dim3((unsigned)wgs), dim3(256), 0, s, a, (int32_t)experts);
+  hipLaunchKernelGGL((i8_tiled_kernel<MODE, WM, WN>), dim3((unsigned)wgs), dim3(256), 0, s, a, (int32_t)experts);
   return hipGetLastError();
 }
 
@@ -626,11 +563,10 @@ hipError_t stream_dense(const I8Args& a, hipStream_t stream) {
 
 hipError_t product_dense(const I8Args& a, hipStream_t stream) {
   switch (i8_dense_kernel(a.M, a.N, a.K)) {
-    case I8_TILES_256: return launch_tiles<MODE_DENSE, 4, 4, 2>(a, 1, stream);
-    case I8_TILES_128x256_ONE: return launch_tiles<MODE_DENSE, 2, 4, 1>(a, 1, stream);
-    case I8_TILES_128x256: return launch_tiles<MODE_DENSE, 2, 4, 2>(a, 1, stream);
-    case I8_TILES_128: return launch_tiles<MODE_DENSE, 2, 2, 2>(a, 1, stream);
-    case I8_TILES_64: return launch_tiles<MODE_DENSE, 1, 1, 2>(a, 1, stream);
+    case I8_TILES_256: return launch_tiles<MODE_DENSE, 4, 4>(a, 1, stream);
+    case I8_TILES_128x256: return launch_tiles<MODE_DENSE, 2, 4>(a, 1, stream);
+    case I8_TILES_128: return launch_tiles<MODE_DENSE, 2, 2>(a, 1, stream);
+    case I8_TILES_64: return launch_tiles<MODE_DENSE, 1, 1>(a, 1, stream);
     case I8_STREAM_32: return stream_dense<2>(a, stream);
     default: return stream_dense<1>(a, stream);
   }
@@ -639,10 +575,9 @@ hipError_t product_dense(const I8Args& a, hipStream_t stream) {
 template <int MODE>
 hipError_t product_experts(const I8Args& a, int64_t experts, hipStream_t stream) {
   switch (i8_experts_kernel(MODE == MODE_GATEUP ? a.M / a.topk : 0, a.M, a.N, a.K, experts)) {
-    case I8_TILES_256: return launch_tiles<MODE, 4, 4, 2>(a, experts, stream);
-    case I8_TILES_128x256_ONE: return launch_tiles<MODE, 2, 4, 1>(a, experts, stream);
-    case I8_TILES_128x256: return launch_tiles<MODE, 2, 4, 2>(a, experts, stream);
-    case I8_TILES_128: return launch_tiles<MODE, 2, 2, 2>(a, experts, stream);
+    case I8_TILES_256: return launch_tiles<MODE, 4, 4>(a, experts, stream);
+    case I8_TILES_128x256: return launch_tiles<MODE, 2, 4>(a, experts, stream);
+    case I8_TILES_128: return launch_tiles<MODE, 2, 2>(a, experts, stream);
     default: return launch_stream<MODE, 1, 4>(a, experts, 1, stream);
   }
 }

@@ -10,11 +10,10 @@ namespace wq {
 enum I8Kernel : int32_t {
   I8_STREAM_16 = 0,  // 16 x 16, weights straight from memory
   I8_STREAM_32,      // 32 x 16
-  I8_TILES_64,       // 64 x 64, two buffers
-  I8_TILES_128,      // 128 x 128, two buffers
-  I8_TILES_128x256,  // two buffers
-  I8_TILES_128x256_ONE,  // one buffer, two workgroups per CU
-  I8_TILES_256       // 256 x 256, two buffers
+  I8_TILES_64,       // 64 x 64
+  I8_TILES_128,      // 128 x 128
+  I8_TILES_128x256,
+  I8_TILES_256       // 256 x 256
 };
 
 // The sum of k products of two codes (at most 2^14 each) stays below 2^31.
@@ -30,29 +29,46 @@ inline bool i8_tiles_fit(int64_t gathered, int64_t N, int64_t K) {
   return N * K <= most && gathered * K <= most;
 }
 
+// By what was measured on both sides of each border (us, in a graph, weights from memory):
+//   256 x 256 tiles where they fill the chip (256 x 256 / 128 x 256): 2048 x 8192 (256 tiles), k 8192: 113 / 133;
+//     4096 x 4096, k 1024: 24 / 28, k 4096: 62 / 73;  1024 x 8192 (128), k 8192: 79 / 68
+//   128 x 256 where those do (128 x 256 / 128 x 128): 1024 x 8192 (256), k 8192: 68 / 75;  2048 x 4096, k 4096: 37 /
+//     41;  2048 x 2048 (128), k 4096: 30 / 24
+//   128 x 128 above half the chip (128 x 128 / 64 x 64): 640 x 4096 (160), k 4096: 22.8 / 31.5;  512 x 4096 (128):
+//     22.9 / 21.0;  256 x 8192 (128), k 8192: 43.3 / 42.1
+//   streaming where few workgroups of 32 x 16 suffice (streaming / 64 x 64): 64 x 4096 (512), k 4096: 14.3 / 19.6;
+//     96 x 4096 (768): 19.4 / 19.2;  333 x 1111 (770), k 4160: 16.6 / 13.3;  64 x 8192 (1024), k 8192: 47 / 38
 inline I8Kernel i8_dense_kernel(int64_t M, int64_t N, int64_t K) {
   const auto tiles = [&](int64_t bm, int64_t bn) { return i8_ceil_div(M, bm) * i8_ceil_div(N, bn); };
   if (M > 32 && i8_tiles_fit(0, N, K)) {
-    if (tiles(256, 256) >= 192 && K > 1024) return I8_TILES_256;
-    if (tiles(128, 256) >= 512) return I8_TILES_128x256_ONE;
+    if (tiles(256, 256) >= 192) return I8_TILES_256;
     if (tiles(128, 256) >= 192) return I8_TILES_128x256;
-    if (tiles(128, 128) >= 128) return I8_TILES_128;
-    if (tiles(32, 16) >= 850) return I8_TILES_64;
+    if (tiles(128, 128) >= 144) return I8_TILES_128;
+    if (tiles(32, 16) >= 700) return I8_TILES_64;
   }
+  // 16 rows a workgroup where 32 would leave CUs without one: 64 x 1024, k 8192: 10.7 against 14.2
   return M > 16 && tiles(32, 16) >= 256 ? I8_STREAM_32 : I8_STREAM_16;
 }
 
 // The same for experts, `pairs` rows in all, gate+up of `gathered` tokens (down: 0), by the rows that an
-// expert has on average.
+// expert has on average (gate+up, down; 64 experts, hidden 8192, inter 3584 unless said otherwise):
+//   streaming for few, which reads the weights at memory's rate (streaming / 128 x 256): 3 rows 565 / 618, 302 /
+//     312; 4 rows 600 / 642, 332 / 326; 8 rows 623 / 650, 389 / 330; 16 rows 874 / 658, 554 / 337.  Gate+up goes on to
+//     10 rows, down, whose k is shorter, to 4; with few tiles to 16 (8 experts, 1024 x 1024; streaming / 128 x 128):
+//     8 rows 5.5 / 6.9, 4.3 / 6.4; 16 rows 7.3 / 7.0, 5.2 / 6.4; 32 rows 10.5 / 6.9, 7.4 / 6.5
+//   256 x 256 tiles from 128 rows on where they fill the chip, 128 x 256 below (256 x 256 / 128 x 256): 64 rows 691 /
+//     690, 378 / 379; 100 rows 719 / 712, 410 / 408; 128 rows 818 / 902, 459 / 525; 512 rows 2019 / 2329, 1112 / 1330
+//   128 x 128 where those would be few (128 x 128 / 256 x 256; 8 experts, 1024 x 1024): 128 rows (96 and 48 tiles) 9.3 /
+//     18.8, 8.2 / 17.1; 1024 rows (320 and 160) 32.5 / 41.4, 20.4 / 20.2; 16 experts, 2048 x 4096: 200 rows (456) 81 /
+//     66, 42.5 / 37.3; and (/ 128 x 256) 64 rows (384) 46.8 / 46.5, 24.8 / 26.7
 inline I8Kernel i8_experts_kernel(int64_t gathered, int64_t pairs, int64_t N, int64_t K, int64_t experts) {
   const int64_t active = pairs < experts ? pairs : experts;  // at most
   const double rows = (double)pairs / (double)experts;
   const int64_t cols = i8_ceil_div(gathered ? 2 * N : N, 256);
-  if (!i8_tiles_fit(gathered, N, K) || rows < 3.0) return I8_STREAM_16;
-  if ((pairs / 128 + active) * cols < 128) return rows <= 32.0 ? I8_STREAM_16 : I8_TILES_128;
-  if (rows < 128.0) return I8_TILES_128x256;
-  if (K <= 1024 || (pairs / 256 + active) * cols < 512) return I8_TILES_128x256_ONE;
-  return I8_TILES_256;
+  const bool few = (pairs / 128 + active) * cols < 512;
+  if (!i8_tiles_fit(gathered, N, K) || rows < (few ? 16.0 : gathered ? 10.0 : 4.0)) return I8_STREAM_16;
+  if (rows < 128.0) return few ? I8_TILES_128 : I8_TILES_128x256;
+  return (pairs / 256 + active) * cols < 400 ? I8_TILES_128 : I8_TILES_256;
 }
 
 }  // namespace wq
