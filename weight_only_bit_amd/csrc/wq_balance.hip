@@ -71,24 +71,34 @@ struct Row {
   }
 };
 
-// Whether a token has a pair (every lane of its group knows); found(e) for each of this lane's.  Four ids a lane
-// are on their way before the first is looked at.
-template <int L, class Found>
-__device__ __forceinline__ bool token_pairs(const int32_t* ids, int32_t topk, int32_t experts, Found found) {
-  bool any = false;
-  for (int32_t j0 = threadIdx.x & (L - 1); j0 < topk; j0 += 4 * L) {
-    int32_t id[4];
+// A token: its logits and this lane's first ids, on their way before the token in front of it is worked on.
+template <typename T, int L, int P>
+struct Token {
+  static constexpr int Q = 4;  // ids of a lane
+  Row<T, L, P> row;
+  int32_t id[Q];
+  __device__ __forceinline__ void load(const T* logits, const int32_t* ids, int64_t tok, int32_t topk, int32_t experts) {
+    row.load(logits + tok * experts, experts);
+    const int32_t in = threadIdx.x & (L - 1);
 #pragma unroll
-    for (int q = 0; q < 4; ++q) id[q] = j0 + q * L < topk ? ids[j0 + q * L] : -1;
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-      if ((uint32_t)id[q] < (uint32_t)experts) {
-        any = true;
-        found(id[q]);
-      }
+    for (int q = 0; q < Q; ++q) id[q] = in + q * L < topk ? ids[tok * topk + in + q * L] : -1;
   }
-  return wave_join<L>(any ? 1u : 0u, [](uint32_t a, uint32_t b) __attribute__((always_inline)) { return a | b; }) != 0;
-}
+  // Whether it has a pair (every lane of its group knows); found(e) for each of this lane's.
+  template <class Found>
+  __device__ __forceinline__ bool pairs(const int32_t* ids, int64_t tok, int32_t topk, int32_t experts, Found found) const {
+    bool any = false;
+    const auto look = [&](int32_t e) __attribute__((always_inline)) {
+      if ((uint32_t)e < (uint32_t)experts) {
+        any = true;
+        found(e);
+      }
+    };
+#pragma unroll
+    for (int q = 0; q < Q; ++q) look(id[q]);
+    for (int32_t j = (threadIdx.x & (L - 1)) + Q * L; j < topk; j += L) look(ids[tok * topk + j]);
+    return wave_join<L>(any ? 1u : 0u, [](uint32_t a, uint32_t b) __attribute__((always_inline)) { return a | b; }) != 0;
+  }
+};
 
 // The sum over the lanes that hold the same place in the groups of L of a wave.
 template <int L>
@@ -123,13 +133,14 @@ __device__ __forceinline__ void conclude(double dot, int64_t all, int64_t tokens
     meet_n[threadIdx.x >> 6] = all;
   }
   __syncthreads();
-  if (threadIdx.x != 0) return;
-  dot = 0.0;
-  all = 0;
-  for (int w = 0; w < kLossWaves; ++w) {
-    dot += meet[w];
-    all += meet_n[w];
+  if (threadIdx.x >= 64) return;
+  dot = threadIdx.x < kLossWaves ? meet[threadIdx.x] : 0.0;
+  all = threadIdx.x < kLossWaves ? meet_n[threadIdx.x] : 0;
+  for (int d = kLossWaves / 2; d >= 1; d >>= 1) {
+    dot += __shfl_xor(dot, d);
+    all += __shfl_xor(all, d);
   }
+  if (threadIdx.x != 0) return;
   // no token with a pair: no loss
   *loss = tokens ? (float)((double)coefficient * experts * dot / ((double)all * (double)tokens)) : 0.f;
 }
@@ -149,6 +160,10 @@ __global__ __launch_bounds__(kLossThreads) void balance_kernel(const T* __restri
   __shared__ int64_t meet_n[kLossWaves];
   const int tid = threadIdx.x, lane = tid & 63;
   constexpr int each = kLossThreads / L;
+  const int64_t stride = (int64_t)gridDim.x * each;
+  int64_t tok = (int64_t)blockIdx.x * each + tid / L;
+  Token<T, L, P> next;
+  if (tok < t) next.load(logits, ids, tok, topk, experts);
   for (int i = tid; i <= experts; i += kLossThreads) hist[i] = 0;
   __syncthreads();
   float acc[P][R::PE];
@@ -157,11 +172,12 @@ __global__ __launch_bounds__(kLossThreads) void balance_kernel(const T* __restri
 #pragma unroll
     for (int i = 0; i < R::PE; ++i) acc[p][i] = 0.f;
   int32_t tokens = 0;
-  for (int64_t tok = (int64_t)blockIdx.x * each + tid / L; tok < t; tok += (int64_t)gridDim.x * each) {
-    R r;
-    r.load(logits + tok * experts, experts);
-    const bool real = token_pairs<L>(ids + tok * topk, topk, experts,
-                                     [&](int32_t e) __attribute__((always_inline)) { atomicAdd(&hist[e], 1); });
+  for (; tok < t; tok += stride) {
+    const Token<T, L, P> now = next;
+    if (tok + stride < t) next.load(logits, ids, tok + stride, topk, experts);
+    const bool real = now.pairs(ids, tok, topk, experts,
+                                [&](int32_t e) __attribute__((always_inline)) { atomicAdd(&hist[e], 1); });
+    R r = now.row;
     r.softmax(real);
     if (real && (tid & (L - 1)) == 0) ++tokens;
 #pragma unroll
@@ -270,6 +286,64 @@ __global__ __launch_bounds__(kLossThreads) void balance_finish_kernel(const floa
   conclude(dot, all, tokens, experts, coefficient, loss, meet, meet_n);
 }
 
+// The same in two launches, where the parts are many bytes: one CU takes in 30 KB/us of what its L2 does not hold
+// (256 parts of 256 experts 8 us, of 512 14 us).  16 columns a workgroup and a 64th of the parts a thread of four ...
+constexpr int kColumns = 16;
+__global__ __launch_bounds__(256) void balance_columns_kernel(const float* __restrict__ probs,
+                                                              const int32_t* __restrict__ pairs, int32_t wgs,
+                                                              int32_t pitch, double* __restrict__ col_p,
+                                                              int32_t* __restrict__ col_n) {
+  __shared__ double meet_p[64][kColumns];
+  __shared__ int32_t meet_n[64][kColumns];
+  const int tid = threadIdx.x, seg = tid / 4, c = blockIdx.x * kColumns + 4 * (tid % 4);
+  double p[4] = {0.0, 0.0, 0.0, 0.0};
+  int32_t n[4] = {0, 0, 0, 0};
+  if (c < pitch) {
+#pragma unroll 4
+    for (int32_t w = seg; w < wgs; w += 64) {
+      const f32x4 pv = *reinterpret_cast<const f32x4*>(probs + (int64_t)w * pitch + c);
+      const u32x4 nv = *reinterpret_cast<const u32x4*>(pairs + (int64_t)w * pitch + c);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        p[i] += (double)pv[i];
+        n[i] += (int32_t)nv[i];
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    meet_p[seg][4 * (tid % 4) + i] = p[i];
+    meet_n[seg][4 * (tid % 4) + i] = n[i];
+  }
+  __syncthreads();
+  const int at = blockIdx.x * kColumns + tid;
+  if (tid >= kColumns || at >= pitch) return;
+  double ps = 0.0;
+  int32_t ns = 0;
+#pragma unroll 8
+  for (int s = 0; s < 64; ++s) {
+    ps += meet_p[s][tid];
+    ns += meet_n[s][tid];
+  }
+  col_p[at] = ps;
+  col_n[at] = ns;
+}
+
+// ... and the loss from the columns' sums.
+__global__ __launch_bounds__(kLossThreads) void balance_columns_finish_kernel(const double* __restrict__ col_p,
+                                                                              const int32_t* __restrict__ col_n,
+                                                                              int32_t experts, float coefficient,
+                                                                              float* __restrict__ loss,
+                                                                              int32_t* __restrict__ counts) {
+  __shared__ double meet[kLossWaves];
+  __shared__ int64_t meet_n[kLossWaves];
+  const int tid = threadIdx.x;
+  const int32_t tokens = col_n[experts], c = tid <= experts ? col_n[tid] : 0;
+  if (tid <= experts) counts[tid] = c;
+  const bool expert = tid < experts;
+  conclude(expert ? (double)c * col_p[tid] : 0.0, expert ? c : 0, tokens, experts, coefficient, loss, meet, meet_n);
+}
+
 template <typename T, int L, int P>
 __global__ __launch_bounds__(kGradThreads) void balance_grad_kernel(const T* __restrict__ logits,
                                                                     const int32_t* __restrict__ ids, int64_t t, int32_t topk,
@@ -292,10 +366,15 @@ __global__ __launch_bounds__(kGradThreads) void balance_grad_kernel(const T* __r
     for (int i = 0; i < R::PE; ++i) share[p][i] = R::expert(p, i) < experts ? (float)counts[R::expert(p, i)] * scale : 0.f;
   const int32_t tokens = counts[experts];
   const float slope = tokens > 0 ? coefficient / (float)tokens * (d_loss ? *d_loss : 1.f) : 0.f;
-  for (int64_t tok = (int64_t)blockIdx.x * each + threadIdx.x / L; tok < t; tok += (int64_t)gridDim.x * each) {
-    R r;
-    r.load(logits + tok * experts, experts);
-    const bool real = token_pairs<L>(ids + tok * topk, topk, experts, [](int32_t) {});
+  const int64_t stride = (int64_t)gridDim.x * each;
+  int64_t tok = (int64_t)blockIdx.x * each + threadIdx.x / L;
+  Token<T, L, P> next;
+  if (tok < t) next.load(logits, ids, tok, topk, experts);
+  for (; tok < t; tok += stride) {
+    const Token<T, L, P> now = next;
+    if (tok + stride < t) next.load(logits, ids, tok + stride, topk, experts);
+    const bool real = now.pairs(ids, tok, topk, experts, [](int32_t) {});
+    R r = now.row;
     r.softmax(real);
     float dot = 0.f;
 #pragma unroll
@@ -358,7 +437,8 @@ static int64_t balance_workgroups(int64_t t, int32_t experts) {
 
 size_t balance_workspace_bytes(int64_t t, int32_t experts) {
   const int64_t wgs = balance_workgroups(t, experts);
-  return wgs > 1 ? (size_t)wgs * part_pitch(experts) * 8 : 0;
+  // the parts, and behind them the columns' sums
+  return wgs > 1 ? (size_t)(8 * wgs + 12) * part_pitch(experts) : 0;
 }
 
 hipError_t launch_balance_loss(const void* logits, int f32, const int32_t* ids, int64_t t, int32_t topk, int32_t experts,
@@ -377,6 +457,18 @@ hipError_t launch_balance_loss(const void* logits, int f32, const int32_t* ids, 
   else run(static_cast<const uint16_t*>(logits));
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || wgs == 1) return e;
+  const int32_t pitch = part_pitch(experts);
+  if (wgs * pitch > 16384) {
+    double* const col_p = reinterpret_cast<double*>(pairs + wgs * pitch);  // (16-byte pieces up to here)
+    int32_t* const col_n = reinterpret_cast<int32_t*>(col_p + pitch);
+    hipLaunchKernelGGL(balance_columns_kernel, dim3((unsigned)((pitch + kColumns - 1) / kColumns)), dim3(256), 0, stream,
+                       probs, pairs, (int32_t)wgs, pitch, col_p, col_n);
+    const hipError_t e2 = hipGetLastError();
+    if (e2 != hipSuccess) return e2;
+    hipLaunchKernelGGL(balance_columns_finish_kernel, dim3(1), dim3(kLossThreads), 0, stream, col_p, col_n, experts,
+                       coefficient, loss, counts);
+    return hipGetLastError();
+  }
   hipLaunchKernelGGL(balance_finish_kernel, dim3(1), dim3(kLossThreads), 0, stream, probs, pairs, (int32_t)wgs, experts,
                      coefficient, loss, counts);
   return hipGetLastError();
@@ -385,7 +477,7 @@ hipError_t launch_balance_loss(const void* logits, int f32, const int32_t* ids, 
 hipError_t launch_balance_loss_grad(const void* logits, int f32, const int32_t* ids, int64_t t, int32_t topk,
                                     int32_t experts, float coefficient, const int32_t* counts, const float* d_loss,
                                     void* d_logits, hipStream_t stream) {
-  const int64_t all = rounds(t, experts, kGradThreads), wgs = all < 2048 ? all : 2048;
+  const int64_t all = rounds(t, experts, kGradThreads), wgs = all < 1024 ? all : 1024;
   const auto run = [&](auto* d) {
     typedef std::remove_pointer_t<decltype(d)> T;
     with_lanes<T>(experts, [&](auto l, auto p) {
