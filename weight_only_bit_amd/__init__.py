@@ -185,6 +185,7 @@ def _ptr(t):
 # ---------------------------------------------------------------------------------------------
 
 _kinds = None
+_tensor = None  # torch.Tensor, once a call has checked one
 
 
 def _dtypes():
@@ -199,8 +200,20 @@ def _dtypes():
 
 def _need(t, name, kind, shape=None, numel=None):
     """t must be a contiguous tensor of `kind` on the current GPU, of the given shape / size."""
+    # what passes takes few steps; what does not is named below
+    if (_tensor is not None and isinstance(t, _tensor) and t.is_cuda and t.dtype in _kinds[kind]
+            and t.get_device() == _current_device() and t.is_contiguous()
+            and (shape is None or t.shape == shape) and (numel is None or t.numel() == numel)):
+        return t
+    return _named_need(t, name, kind, shape, numel)
+
+
+def _named_need(t, name, kind, shape, numel):
+    global _tensor
     import torch
 
+    _dtypes()
+    _tensor = torch.Tensor
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch tensor, got {type(t).__name__}")
     if not t.is_cuda:
@@ -505,13 +518,15 @@ def wq_quantize_ccq(w, zp: int = 32, refine=True) -> PackedWeight:
 
 def _value_type(t, name):
     """(wq_type, _need kind) of a tensor that may hold bf16 (or its bits) or fp32."""
-    import torch
+    if _tensor is None or not isinstance(t, _tensor):
+        import torch
 
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name}: expected a torch tensor, got {type(t).__name__}")
-    if t.dtype in _dtypes()["bf16"]:
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name}: expected a torch tensor, got {type(t).__name__}")
+    kinds = _kinds or _dtypes()
+    if t.dtype in kinds["bf16"]:
         return TYPE_BF16, "bf16"
-    if t.dtype == torch.float32:
+    if t.dtype in kinds["f32"]:
         return TYPE_F32, "f32"
     raise TypeError(f"{name}: dtype {t.dtype} is neither bf16 nor f32")
 
@@ -718,14 +733,12 @@ class Int8Rows(NamedTuple):
 def wq_quantize_i8(x) -> Int8Rows:
     """bf16 or fp32 rows [n, k] to int8 with a scale per row (include/wq.h): the activations of the products
     below."""
-    import torch
-
     vt, kind = _value_type(x, "wq_quantize_i8 x")
     if x.dim() != 2 or x.shape[1] == 0:
         raise ValueError(f"wq_quantize_i8: x must be [n, k], got shape {tuple(x.shape)}")
     n, k = x.shape
     x = _need(x.contiguous(), "wq_quantize_i8 x", kind)
-    rows = Int8Rows(x.new_empty((n, k), dtype=torch.int8), x.new_empty(n, dtype=torch.float32))
+    rows = Int8Rows(x.new_empty((n, k), dtype=_kinds["i8"][0]), x.new_empty(n, dtype=_kinds["f32"][0]))
     _check(lib().wq_quantize_i8(_ptr(x), vt, n, k, _ptr(rows.codes), _ptr(rows.scales), TYPE_F32, _stream()),
            "wq_quantize_i8")
     return rows
@@ -733,8 +746,6 @@ def wq_quantize_i8(x) -> Int8Rows:
 
 def wq_quantize_i8_weight(w) -> PackedWeight:
     """bf16 or fp32 weights [n, k] or [E, n, k] to FMT_INT8 with a bf16 scale per output channel."""
-    import torch
-
     vt, kind = _value_type(w, "wq_quantize_i8_weight w")
     if w.dim() not in (2, 3):
         raise ValueError("wq_quantize_i8_weight: w must be [n, k] or [E, n, k]")
@@ -742,8 +753,8 @@ def wq_quantize_i8_weight(w) -> PackedWeight:
     if k <= 0 or k % 64:
         raise ValueError(f"wq_quantize_i8_weight: k = {k} is not a positive multiple of 64")
     w = _need(w.contiguous(), "wq_quantize_i8_weight w", kind)
-    codes = w.new_empty((E, n, k), dtype=torch.int8)
-    scales = w.new_empty((E, n), dtype=torch.bfloat16)
+    codes = w.new_empty((E, n, k), dtype=_kinds["i8"][0])
+    scales = w.new_empty((E, n), dtype=_kinds["bf16"][0])
     _check(lib().wq_quantize_i8(_ptr(w), vt, E * n, k, _ptr(codes), _ptr(scales), TYPE_BF16, _stream()),
            "wq_quantize_i8_weight")
     return PackedWeight(FMT_INT8, n, k, E, 0, codes=codes, scales=scales)
@@ -774,13 +785,11 @@ def wq_gemm_i8(x, w: PackedWeight, y=None, dtype=None):
 def wq_moe_gate_up_i8(x, offsets, sorted_pairs, topk: int, gate: PackedWeight, up: PackedWeight, h=None):
     """wq_moe_gate_up with both operands in int8; x: Int8Rows of the tokens [t, hidden].  h [t*topk, inter]
     bf16, rows in expert order; rows behind offsets[-1] (dropped pairs leave some) are not written."""
-    import torch
-
     t, codes, scales = _i8_rows(x, "wq_moe_gate_up_i8 x", gate.k)
     _need(offsets, "wq_moe_gate_up_i8 offsets", "i32", numel=gate.experts + 1)
     _need(sorted_pairs, "wq_moe_gate_up_i8 sorted_pairs", "i32", numel=t * topk)
     if h is None:
-        h = codes.new_empty((t * topk, gate.n), dtype=torch.bfloat16)
+        h = codes.new_empty((t * topk, gate.n), dtype=_kinds["bf16"][0])
     else:
         _need(h, "wq_moe_gate_up_i8 h", "bf16", shape=(t * topk, gate.n))
     _check(lib().wq_moe_gate_up_i8(_ptr(codes), _ptr(scales), t, _ptr(offsets), _ptr(sorted_pairs), topk,
@@ -800,6 +809,14 @@ def wq_moe_down_i8(h, offsets, down: PackedWeight, d=None, dtype=None):
     return d
 
 
+def _like(t, x, what, name, kind):
+    """t must be like x, which has passed _need."""
+    if (isinstance(t, _tensor) and t.dtype is x.dtype and t.shape == x.shape and t.is_contiguous()
+            and t.get_device() == x.get_device()):
+        return
+    _need(t, f"{what} {name}", kind, shape=x.shape)
+
+
 def _norm_inputs(x, weight, residual, sum, what):
     """(wq_type, _need kind, n, k, sum) of a norm's inputs; sum: the caller's array, a new one, or None where
     there is no residual."""
@@ -813,11 +830,11 @@ def _norm_inputs(x, weight, residual, sum, what):
         if sum is not None:
             raise ValueError(f"{what}: a sum without a residual")
         return vt, kind, n, k, None
-    _need(residual, f"{what} residual", kind, shape=(n, k))
+    _like(residual, x, what, "residual", kind)
     if sum is None:
         sum = x.new_empty((n, k))
     else:
-        _need(sum, f"{what} sum", kind, shape=(n, k))
+        _like(sum, x, what, "sum", kind)
     return vt, kind, n, k, sum
 
 
@@ -829,7 +846,7 @@ def wq_rms_norm(x, weight, residual=None, eps: float = 1e-6, y=None, sum=None):
     if y is None:
         y = x.new_empty((n, k))
     else:
-        _need(y, "wq_rms_norm y", kind, shape=(n, k))
+        _like(y, x, "wq_rms_norm", "y", kind)
     _check(lib().wq_rms_norm(_ptr(x), vt, _ptr(residual), _ptr(weight), eps, n, k, _ptr(total), _ptr(y), _stream()),
            "wq_rms_norm")
     return y, x if total is None else total
@@ -838,11 +855,9 @@ def wq_rms_norm(x, weight, residual=None, eps: float = 1e-6, y=None, sum=None):
 def wq_rms_norm_i8(x, weight, residual=None, eps: float = 1e-6, rows=None, sum=None):
     """(Int8Rows, sum): wq_rms_norm with the normed rows in int8, a scale each, as the int8 products take
     them."""
-    import torch
-
     vt, kind, n, k, total = _norm_inputs(x, weight, residual, sum, "wq_rms_norm_i8")
     if rows is None:
-        rows = Int8Rows(x.new_empty((n, k), dtype=torch.int8), x.new_empty(n, dtype=torch.float32))
+        rows = Int8Rows(x.new_empty((n, k), dtype=_kinds["i8"][0]), x.new_empty(n, dtype=_kinds["f32"][0]))
     else:
         if not isinstance(rows, tuple) or len(rows) != 2:
             raise TypeError(f"wq_rms_norm_i8 rows: expected Int8Rows, got {type(rows).__name__}")
@@ -860,32 +875,30 @@ def wq_rms_norm_grad(dy, sum, weight, d_sum=None, eps: float = 1e-6, dx=None, d_
     that reaches the sum from elsewhere.  dx is the gradient of x and of the residual alike, and may be d_sum's
     own tensor.  weight_grad False: d_weight is not computed and None.  ws: a uint8 tensor of
     wq_rms_norm_grad_workspace_bytes, allocated by the call if None."""
-    import torch
-
     vt, kind = _value_type(dy, "wq_rms_norm_grad dy")
     if dy.dim() != 2 or dy.shape[1] == 0:
         raise ValueError(f"wq_rms_norm_grad: dy must be [n, k], got shape {tuple(dy.shape)}")
     n, k = dy.shape
     _need(dy, "wq_rms_norm_grad dy", kind)
-    _need(sum, "wq_rms_norm_grad sum", kind, shape=(n, k))
+    _like(sum, dy, "wq_rms_norm_grad", "sum", kind)
     _need(weight, "wq_rms_norm_grad weight", kind, shape=(k,))
     if d_sum is not None:
-        _need(d_sum, "wq_rms_norm_grad d_sum", kind, shape=(n, k))
+        _like(d_sum, dy, "wq_rms_norm_grad", "d_sum", kind)
     if dx is None:
         dx = dy.new_empty((n, k))
     else:
-        _need(dx, "wq_rms_norm_grad dx", kind, shape=(n, k))
+        _like(dx, dy, "wq_rms_norm_grad", "dx", kind)
     if not weight_grad:
         if d_weight is not None:
             raise ValueError("wq_rms_norm_grad: a d_weight without weight_grad")
     elif d_weight is None:
-        d_weight = dy.new_empty(k, dtype=torch.float32)
+        d_weight = dy.new_empty(k, dtype=_kinds["f32"][0])
     else:
         _need(d_weight, "wq_rms_norm_grad d_weight", "f32", shape=(k,))
-    ws = _workspace(ws, wq_rms_norm_grad_workspace_bytes(n, k, vt) if weight_grad else 0, dy, "wq_rms_norm_grad")
-    _check(lib().wq_rms_norm_grad(_ptr(dy), vt, _ptr(d_sum), _ptr(sum), _ptr(weight), eps, n, k, _ptr(dx),
-                                  _ptr(d_weight), _ptr(ws), 0 if ws is None else ws.numel(), _stream()),
-           "wq_rms_norm_grad")
+    L = lib()
+    ws = _workspace(ws, L.wq_rms_norm_grad_workspace_bytes(n, k, vt) if weight_grad else 0, dy, "wq_rms_norm_grad")
+    _check(L.wq_rms_norm_grad(_ptr(dy), vt, _ptr(d_sum), _ptr(sum), _ptr(weight), eps, n, k, _ptr(dx), _ptr(d_weight),
+                              _ptr(ws), 0 if ws is None else ws.numel(), _stream()), "wq_rms_norm_grad")
     return dx, d_weight
 
 
@@ -895,10 +908,8 @@ def wq_rms_norm_grad_workspace_bytes(n: int, k: int, value_type: int) -> int:
 
 def _workspace(ws, need, like, what):
     """The caller's workspace checked, a new one, or None where none is needed."""
-    import torch
-
     if ws is None:
-        return like.new_empty(need, dtype=torch.uint8) if need else None
+        return like.new_empty(need, dtype=_kinds["u8"][0]) if need else None
     return _need(ws, f"{what} ws", "u8") if ws.numel() else None
 
 
@@ -923,21 +934,19 @@ def wq_moe_balance_loss(logits, topk_ids, coefficient: float = 1.0, loss=None, c
     """(loss f32 [], counts int32 [experts + 1]): the balance loss (include/wq.h) of the router's logits
     [t, experts], bf16 or fp32, and the ids that it chose; counts holds every expert's pairs and, last, the
     tokens that have a pair (padding, all of whose ids are no expert's, counts nowhere)."""
-    import torch
-
     vt, _, t, topk, experts = _balance_inputs(logits, topk_ids, "wq_moe_balance_loss")
     if loss is None:
-        loss = logits.new_empty((), dtype=torch.float32)
+        loss = logits.new_empty((), dtype=_kinds["f32"][0])
     else:
         _need(loss, "wq_moe_balance_loss loss", "f32", numel=1)
     if counts is None:
         counts = topk_ids.new_empty(experts + 1)
     else:
         _need(counts, "wq_moe_balance_loss counts", "i32", numel=experts + 1)
-    ws = _workspace(ws, wq_moe_balance_loss_workspace_bytes(t, experts), logits, "wq_moe_balance_loss")
-    _check(lib().wq_moe_balance_loss(_ptr(logits), vt, _ptr(topk_ids), t, topk, experts, coefficient, _ptr(loss),
-                                     _ptr(counts), _ptr(ws), 0 if ws is None else ws.numel(), _stream()),
-           "wq_moe_balance_loss")
+    L = lib()
+    ws = _workspace(ws, L.wq_moe_balance_loss_workspace_bytes(t, experts), logits, "wq_moe_balance_loss")
+    _check(L.wq_moe_balance_loss(_ptr(logits), vt, _ptr(topk_ids), t, topk, experts, coefficient, _ptr(loss), _ptr(counts),
+                                 _ptr(ws), 0 if ws is None else ws.numel(), _stream()), "wq_moe_balance_loss")
     return loss, counts
 
 
