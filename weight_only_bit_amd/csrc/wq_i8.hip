@@ -168,6 +168,115 @@ hipError_t launch_stream(const I8Args& a, int64_t gy, int64_t gz, hipStream_t s)
 }
 
 // ---------------------------------------------------------------------------------------------
+// Tens to hundreds of rows: 16 CT columns and 16 MT rows a workgroup.  A CU takes in 15 to 20 KB/us from memory,
+// however much it has asked for (64 x 64 tiles of 128 x 4096, k 4096: 19.3 us on 128 CUs with one stage on its way or
+// eight, 9.2 with the weights in L2), so the weights' columns are cut so finely that every CU brings some of them,
+// and the rows, which L2 holds, are read again: 64 x 8192, k 8192 26 us (38 with 64 x 64 tiles, 47 streaming).
+//   * Stages of 256 bytes of a row, 16 lanes a row; two of them on their way in registers, two in LDS, 16-byte
+//     piece p of row r in slot p ^ (r % 16): writes and fragment reads are free of bank conflicts.  Four, six or
+//     eight on their way gain nothing (64 x 8192: 27.4 to 28.5): a CU has two or three workgroups.
+//   * Wave v multiplies the codes 64 v .. 64 v + 63 of every stage, so each piece of LDS is read once; the waves'
+//     sums meet in LDS at the end.
+//   * The weights are the A operand: a lane ends with four consecutive outputs of one row.
+// ---------------------------------------------------------------------------------------------
+template <int MT, int CT>
+__global__ __launch_bounds__(256) void i8_narrow_kernel(const I8Args a) {
+  constexpr int XR = 16 * MT, WR = 16 * CT, NC = MT + CT;  // rows of a stage, loads of a thread and stage
+  constexpr int kRow = 256;                 // bytes of a row of a stage
+  __shared__ __attribute__((aligned(16))) uint8_t buf0[(XR + WR) * kRow], buf1[(XR + WR) * kRow];
+  const int tid = threadIdx.x, lane = tid & 63, nl = lane & 15, q = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int32_t K = (int32_t)a.K, stages = (K + kRow - 1) / kRow, last = stages - 1;
+  const int64_t n0 = (int64_t)blockIdx.x * WR, m0 = (int64_t)blockIdx.y * XR;
+  const int rows = (int)(a.M - m0 < XR ? a.M - m0 : XR), cols = (int)(a.N - n0 < WR ? a.N - n0 : WR);
+
+  // load role: row tid / 16 of 16 (load i: rows 16 i .. of the stage, activations and then weights), piece tid % 16.
+  // Rows behind the matrices' ends and pieces behind k lie out of their resource's range and read zeros.
+  const int r = tid >> 4, piece = tid & 15;
+  const uint32_t off = (uint32_t)r * (uint32_t)K + piece * 16;
+  const bool behind = last * kRow + piece * 16 >= K;
+  const uint32_t to = (uint32_t)(r * kRow + ((piece ^ r) << 4));
+  auto fetch = [&](u32x4 (&v)[NC], int32_t g) __attribute__((always_inline)) {
+    const int at = (int)((off + (uint32_t)g * kRow) | (g == last && behind ? 0x7FFFFFF0u : 0u));
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      const int8_t* const base = i < MT ? a.x_codes + (m0 + 16 * i) * K : a.w0_codes + (n0 + 16 * (i - MT)) * K;
+      const int have = i < MT ? rows - 16 * i : cols - 16 * (i - MT);
+      const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t*>(base), (short)0,
+                                                          have <= 0 ? 0 : (have < 16 ? have : 16) * K, 0x00020000);
+      v[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rsrc, at, 0, 0));
+    }
+  };
+  auto put = [&](const u32x4 (&v)[NC], uint8_t* buf) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < NC; ++i) *reinterpret_cast<u32x4*>(buf + to + i * 16 * kRow) = v[i];
+  };
+
+  i32x4 acc[CT][MT];
+#pragma unroll
+  for (int c = 0; c < CT; ++c)
+#pragma unroll
+    for (int t = 0; t < MT; ++t) acc[c][t] = (i32x4){0, 0, 0, 0};
+  const uint32_t from = (uint32_t)(nl * kRow + (((4 * wave + q) ^ nl) << 4));
+  u32x4 even[NC], odd[NC];
+  fetch(even, 0);
+  if (1 < stages) fetch(odd, 1);
+  put(even, buf0);
+  if (2 < stages) fetch(even, 2);
+  __syncthreads();
+  // Stage g in `here`; the next one goes to `there` from the registers that hold it, which take stage g + 3.
+  auto stage = [&](int32_t g, u32x4 (&next)[NC], const uint8_t* here, uint8_t* there) __attribute__((always_inline)) {
+    u32x4 f[NC];
+#pragma unroll
+    for (int i = 0; i < NC; ++i) f[i] = *reinterpret_cast<const u32x4*>(here + from + i * 16 * kRow);
+    if (g < last) put(next, there);
+    if (g + 3 < stages) fetch(next, g + 3);
+#pragma unroll
+    for (int c = 0; c < CT; ++c)
+#pragma unroll
+      for (int t = 0; t < MT; ++t) acc[c][t] = mfma16(f[MT + c], f[t], acc[c][t]);
+    __syncthreads();  // stage g has been read, stage g + 1 is written
+  };
+  for (int32_t g = 0; g < stages; g += 2) {
+    stage(g, odd, buf0, buf1);
+    if (g + 1 < stages) stage(g + 1, even, buf1, buf0);
+  }
+
+  // CT rounds, each with its columns' sums of the four waves
+  i32x4* const red = reinterpret_cast<i32x4*>(buf0);  // [wave][row tile][lane]
+#pragma unroll
+  for (int c = 0; c < CT; ++c) {
+    if (c > 0) __syncthreads();
+#pragma unroll
+    for (int t = 0; t < MT; ++t) red[(wave * MT + t) * 64 + lane] = acc[c][t];
+    __syncthreads();
+    const int64_t n = n0 + 16 * c + 4 * q;
+    float sw[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sw[i] = bf16_bits_to_f32(a.w0_scales[n + i < a.N ? n + i : a.N - 1]);
+    for (int t = wave; t < MT; t += 4) {
+      const int row = 16 * t + nl;
+      if (row >= rows) continue;
+      const float sx = a.x_scales[m0 + row];
+      i32x4 v = red[t * 64 + lane];
+#pragma unroll
+      for (int w = 1; w < 4; ++w) v += red[(w * MT + t) * 64 + lane];
+      const int64_t at = (m0 + row) * a.N + n;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (n + i < a.N) store_out(a.out, a.out_f32, at + i, (float)v[i] * sx * sw[i]);
+    }
+  }
+}
+
+template <int MT, int CT>
+hipError_t launch_narrow(const I8Args& a, hipStream_t s) {
+  hipLaunchKernelGGL((i8_narrow_kernel<MT, CT>),
+                     dim3((unsigned)i8_ceil_div(a.N, 16 * CT), (unsigned)i8_ceil_div(a.M, 16 * MT)), dim3(256), 0, s, a);
+  return hipGetLastError();
+}
+
+// ---------------------------------------------------------------------------------------------
 // Many rows: tiles staged in LDS.
 //
 // One workgroup of 4 waves, one per SIMD, computes 64 WM rows by 64 WN columns (256 x 256 for the
@@ -567,6 +676,9 @@ hipError_t product_dense(const I8Args& a, hipStream_t stream) {
     case I8_TILES_128x256: return launch_tiles<MODE_DENSE, 2, 4>(a, 1, stream);
     case I8_TILES_128: return launch_tiles<MODE_DENSE, 2, 2>(a, 1, stream);
     case I8_TILES_64: return launch_tiles<MODE_DENSE, 1, 1>(a, 1, stream);
+    case I8_NARROW_64x32: return launch_narrow<4, 2>(a, stream);
+    case I8_NARROW_64x16: return launch_narrow<4, 1>(a, stream);
+    case I8_NARROW_32x16: return launch_narrow<2, 1>(a, stream);
     case I8_STREAM_32: return stream_dense<2>(a, stream);
     default: return stream_dense<1>(a, stream);
   }

@@ -10,6 +10,9 @@ namespace wq {
 enum I8Kernel : int32_t {
   I8_STREAM_16 = 0,  // 16 x 16, weights straight from memory
   I8_STREAM_32,      // 32 x 16
+  I8_NARROW_32x16,   // few columns a workgroup, staged in LDS
+  I8_NARROW_64x16,
+  I8_NARROW_64x32,
   I8_TILES_64,       // 64 x 64
   I8_TILES_128,      // 128 x 128
   I8_TILES_128x256,
@@ -36,15 +39,28 @@ inline bool i8_tiles_fit(int64_t gathered, int64_t N, int64_t K) {
 //     41;  2048 x 2048 (128), k 4096: 30 / 24
 //   128 x 128 above half the chip (128 x 128 / 64 x 64): 640 x 4096 (160), k 4096: 22.8 / 31.5;  512 x 4096 (128):
 //     22.9 / 21.0;  256 x 8192 (128), k 8192: 43.3 / 42.1
-//   streaming where few workgroups of 32 x 16 suffice (streaming / 64 x 64): 64 x 4096 (512), k 4096: 14.3 / 19.6;
-//     96 x 4096 (768): 19.4 / 19.2;  333 x 1111 (770), k 4160: 16.6 / 13.3;  64 x 8192 (1024), k 8192: 47 / 38
+//   64 x 64 above it (64 x 64 / 64 x 32): 200 x 8192 (512), k 8192: 40 / 58;  64 x 28672 (448), k 4096: 31 / 45;  32 x
+//     28672 30 against 45 streaming and 37 with 32 x 16;  256 x 4096 (256): 19.1 / 16.3;  128 x 8192 (256): 37 / 31
+//   32 columns a workgroup, then 16 (64 x 32 / 64 x 16): 128 x 8192 (256 tiles of 64 x 64): 31 / 44;  256 x 4096: 16.3 /
+//     22;  64 x 8192 (128): 26.0 / 26.1;  128 x 4096 (128): 14.4 / 13.8
+//   streaming where those would leave CUs without a workgroup (streaming / 64 x 16): 64 x 4096 (256 workgroups), k
+//     4096: 14.2 / 12.6, k 1024: 5.7 / 5.1;  256 x 1024 (256), k 8192: 24 / 19.5;  48 x 2048 (128): 14.0 / 20.1;  and up
+//     to 32 rows (/ 32 x 16) 32 x 4096 (256): 9.5 / 11.7;  32 x 8192 (512), k 8192: 26.6 / 23.0;  16 rows stream
 inline I8Kernel i8_dense_kernel(int64_t M, int64_t N, int64_t K) {
   const auto tiles = [&](int64_t bm, int64_t bn) { return i8_ceil_div(M, bm) * i8_ceil_div(N, bn); };
-  if (M > 32 && i8_tiles_fit(0, N, K)) {
-    if (tiles(256, 256) >= 192) return I8_TILES_256;
-    if (tiles(128, 256) >= 192) return I8_TILES_128x256;
-    if (tiles(128, 128) >= 144) return I8_TILES_128;
-    if (tiles(32, 16) >= 700) return I8_TILES_64;
+  if (M > 16 && i8_tiles_fit(0, N, K)) {
+    if (M > 32) {
+      if (tiles(256, 256) >= 192) return I8_TILES_256;
+      if (tiles(128, 256) >= 192) return I8_TILES_128x256;
+      if (tiles(128, 128) >= 144) return I8_TILES_128;
+    }
+    if (tiles(64, 64) >= 384) return I8_TILES_64;
+    if (M > 32) {
+      if (tiles(64, 64) >= 192) return I8_NARROW_64x32;
+      if (tiles(64, 16) >= 192) return I8_NARROW_64x16;
+    } else if (tiles(32, 16) >= 384) {
+      return I8_NARROW_32x16;
+    }
   }
   // 16 rows a workgroup where 32 would leave CUs without one: 64 x 1024, k 8192: 10.7 against 14.2
   return M > 16 && tiles(32, 16) >= 256 ? I8_STREAM_32 : I8_STREAM_16;
