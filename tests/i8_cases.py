@@ -8,7 +8,7 @@ KERNELS = ("I8_STREAM_16", "I8_STREAM_32", "I8_NARROW_32x16", "I8_NARROW_64x16",
 
 Dense = namedtuple("Dense", "kernel m n k")
 # n that no 16-byte piece divides, k whose last step or stage (256, 128) ends inside; the last row tile of the
-# large tiles has at most 64 rows, 65 to 128, or more
+# large tiles has at most 64 rows, 65 to 128, 129 to 192, or more
 DENSE = [Dense("I8_STREAM_16", 1, 1, 64), Dense("I8_STREAM_16", 9, 77, 576), Dense("I8_STREAM_16", 300, 77, 192),
          Dense("I8_STREAM_32", 100, 1025, 1088), Dense("I8_STREAM_32", 32, 4097, 64),
          Dense("I8_NARROW_32x16", 17, 6150, 64), Dense("I8_NARROW_32x16", 32, 6145, 832),
@@ -20,11 +20,11 @@ DENSE = [Dense("I8_STREAM_16", 1, 1, 64), Dense("I8_STREAM_16", 9, 77, 576), Den
          Dense("I8_TILES_128", 1300, 1701, 832), Dense("I8_TILES_128", 1380, 1700, 448),
          Dense("I8_TILES_128x256", 1440, 4100, 1344), Dense("I8_TILES_128x256", 1500, 4099, 320),
          Dense("I8_TILES_256", 3100, 4097, 1088), Dense("I8_TILES_256", 3172, 4100, 1152),
-         Dense("I8_TILES_256", 3250, 4096, 64), Dense("I8_TILES_256", 3250, 4096, 192)]
+         Dense("I8_TILES_256", 3250, 4096, 64), Dense("I8_TILES_256", 3300, 4096, 192)]
 
 # counts: every expert's rows, empty experts among them; the rest of the t * topk pairs are dropped
 Experts = namedtuple("Experts", "kernel gate_up t topk n k counts")
-_FEW, _EIGHT, _THREE, _LONG = (0, 17, 1, 16, 3), (1, 64, 65, 128, 0, 100, 30, 5), (180, 326, 64), (300, 356, 0, 700)
+_FEW, _EIGHT, _THREE, _LONG = (0, 17, 1, 16, 3), (1, 64, 65, 128, 0, 100, 30, 5), (180, 326, 64), (300, 356, 0, 230, 444)
 EXPERTS = [Experts("I8_STREAM_16", True, 20, 2, 65, 576, _FEW), Experts("I8_STREAM_16", False, 20, 2, 130, 576, _FEW),
            Experts("I8_TILES_128", True, 165, 2, 350, 832, (64, 161, 65)),
            Experts("I8_TILES_128", False, 165, 2, 701, 832, (64, 161, 65)),
@@ -34,3 +34,8 @@ EXPERTS = [Experts("I8_STREAM_16", True, 20, 2, 65, 576, _FEW), Experts("I8_STRE
            Experts("I8_TILES_128x256", False, 100, 4, 12101, 448, _EIGHT),
            Experts("I8_TILES_256", True, 700, 2, 7201, 1088, _LONG),
            Experts("I8_TILES_256", False, 700, 2, 14401, 1088, _LONG)]
+
+
+def heights_of_last_tiles(counts, height):
+    """The kernels' heights of every expert's last row tile, in 64 rows."""
+    return {(c - 1) % height // 64 + 1 for c in counts if c}

@@ -8,8 +8,7 @@ import numpy as np
 import pytest
 
 import i8_testutil as i8
-from i8_cases import DENSE, EXPERTS, KERNELS
-from mx_cases import rows_of_last_tiles
+from i8_cases import DENSE, EXPERTS, KERNELS, heights_of_last_tiles
 from test_abi import _weight, wq  # noqa: F401  (fixture)
 
 P = [ctypes.c_void_p(0x100000000 * (i + 1)) for i in range(9)]
@@ -357,8 +356,8 @@ def test_cases_take_their_kernels(rules):
                 continue
             some = [g for g in group if g[0] == kernel]
             # every height of a last row tile, and a stage (128) that k ends inside
-            classes = set().union(*(rows_of_last_tiles(g[1], _height(kernel)) for g in some))
-            assert classes == set(range({256: 3, 128: 2, 64: 1}[_height(kernel)])), kernel
+            heights = set().union(*(heights_of_last_tiles(g[1], _height(kernel)) for g in some))
+            assert heights == set(range(1, _height(kernel) // 64 + 1)), (kernel, heights)
             assert any(g[2] % 128 for g in some), kernel
 
 

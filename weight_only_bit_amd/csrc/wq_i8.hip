@@ -626,11 +626,15 @@ void i8_tiled_kernel(const I8Args a, int32_t experts) {
     rows = a.M - row0 < XR ? a.M - row0 : XR;
   } else {
     ExpertTiles tiles{a.offsets, experts, XR};
-    if (!xcd_tile(blockIdx.x, (uint32_t)tiles.total(), (uint32_t)col_tiles, r, c)) return;
+    const uint32_t row_tiles = (uint32_t)tiles.total();
+    if (WM == 4 ? !xcd_block_tile(blockIdx.x, row_tiles, (uint32_t)col_tiles, r, c)
+                : !xcd_tile(blockIdx.x, row_tiles, (uint32_t)col_tiles, r, c))
+      return;
     tiles.find((int32_t)r, e, row0, rows);
   }
   if constexpr (WM == 4) {
-    if (rows > 128) i8_tile<MODE, 4, WN>(a, lds, e, row0, rows, c);
+    if (rows > 192) i8_tile<MODE, 4, WN>(a, lds, e, row0, rows, c);
+    else if (rows > 128) i8_tile<MODE, 3, WN>(a, lds, e, row0, rows, c);
     else if (rows > 64) i8_tile<MODE, 2, WN>(a, lds, e, row0, rows, c);
     else i8_tile<MODE, 1, WN>(a, lds, e, row0, rows, c);
   } else if constexpr (WM == 2) {
@@ -647,7 +651,8 @@ hipError_t launch_tiles(const I8Args& a, int64_t experts, hipStream_t s) {
   constexpr int64_t size = 64 * WM;
   // an expert's last tile may be partial: at most one more row tile per expert
   const int64_t row_tiles = (a.M + size - 1) / size + (MODE == MODE_DENSE ? 0 : experts);
-  const int64_t wgs = (row_tiles * ((a.N + cols - 1) / cols) + 7) / 8 * 8;
+  const int64_t col_tiles = (a.N + cols - 1) / cols;
+  const int64_t wgs = MODE != MODE_DENSE && WM == 4 ? block_grid(row_tiles, col_tiles) : (row_tiles * col_tiles + 7) / 8 * 8;
   if (wgs >= (1ll << 24)) return hipErrorInvalidValue;
   hipLaunchKernelGGL((i8_tiled_kernel<MODE, WM, WN>), dim3((unsigned)wgs), dim3(256), 0, s, a, (int32_t)experts);
   return hipGetLastError();

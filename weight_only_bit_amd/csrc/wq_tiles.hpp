@@ -23,6 +23,23 @@ __device__ __forceinline__ bool xcd_tile(uint32_t wg, uint32_t row_tiles, uint32
   return true;
 }
 
+// The same in blocks of kBlockRows x kBlockCols tiles that go round the XCDs, for experts' tiles that cost
+// unequally: an XCD's share of the list is then no run of them.  A grid of block_grid workgroups.
+constexpr uint32_t kBlockRows = 8, kBlockCols = 4;
+__host__ __device__ inline int64_t block_grid(int64_t row_tiles, int64_t col_tiles) {
+  const int64_t blocks = (row_tiles + kBlockRows - 1) / kBlockRows * ((col_tiles + kBlockCols - 1) / kBlockCols);
+  return (blocks + 7) / 8 * 8 * (kBlockRows * kBlockCols);
+}
+__device__ __forceinline__ bool xcd_block_tile(uint32_t wg, uint32_t row_tiles, uint32_t col_tiles, int64_t& r,
+                                               int64_t& c) {
+  constexpr uint32_t size = kBlockRows * kBlockCols;
+  const uint32_t k = wg >> 3, block = k / size * 8 + (wg & 7), in = k % size;
+  const uint32_t across = (col_tiles + kBlockCols - 1) / kBlockCols;
+  r = block / across * kBlockRows + in % kBlockRows;
+  c = block % across * kBlockCols + in / kBlockRows;
+  return r < row_tiles && c < col_tiles;
+}
+
 // The row tiles of an MoE product: every expert's rows in tiles of `size`, experts in order.  Every
 // wave counts and finds them by itself; lane l holds experts l, l + 64, ...
 struct ExpertTiles {
