@@ -145,15 +145,20 @@ def test_gemm(wq, case, out):
     assert (pad[case.m * case.n:] == 7).all()  # nothing behind the output
 
 
-@pytest.mark.parametrize("m,n,k", [(1, 16, 131008), (3, 5, 65600), (130, 257, 131008)])
+# streaming, few columns a workgroup of each kind, tiles of 64, 128, 128 x 256 and 256
+@pytest.mark.parametrize("m,n,k", [(1, 16, 131008), (100, 1025, 65600), (32, 6145, 65600), (64, 3100, 131008), (70, 8190, 65600),
+                                   (200, 8190, 65600), (1300, 1701, 131008), (1440, 4100, 65600), (3100, 4097, 131008)])
 def test_gemm_largest_sums(wq, m, n, k):
     """Every code -128, or 127 against -128: the largest sums of either sign stay in int32."""
+    import torch
+
     _say("largest sums", m, n, k)
     for a, b in ((-128, -128), (127, -128), (127, 127)):
-        c, wc = np.full((m, k), a, np.int8), np.full((1, n, k), b, np.int8)
-        s, ws = np.ones(m, np.float32), np.ones((1, n))
-        got = i8.to_host(wq.wq_gemm_i8(i8.rows(wq, c, s), i8.weight(wq, wc, ws), dtype=__import__("torch").float32))
-        assert np.array_equal(got, np.full((m, n), np.float32(a * b * k), np.float64))
+        x = wq.Int8Rows(torch.full((m, k), a, dtype=torch.int8, device="cuda"), torch.ones(m, device="cuda"))
+        w = wq.PackedWeight(wq.FMT_INT8, n, k, 1, 0, codes=torch.full((1, n, k), b, dtype=torch.int8, device="cuda"),
+                            scales=torch.ones((1, n), dtype=torch.bfloat16, device="cuda"))
+        y = wq.wq_gemm_i8(x, w, dtype=torch.float32)
+        assert (y == float(np.float32(a * b * k))).all()
 
 
 def test_gemm_nan_rows_and_zero_scales(wq):
@@ -261,3 +266,18 @@ def test_rows_beyond_32_bits(wq):
     y = wq.wq_gemm_i8(i8.rows(wq, c, s), i8.weight(wq, wc, ws), dtype=torch.float32)
     assert np.array_equal(i8.to_host(y[-3:]), i8.product_bits(c[-3:], s[-3:], wc[0], ws[0], "f32"))
     assert np.array_equal(i8.to_host(y[:3]), i8.product_bits(c[:3], s[:3], wc[0], ws[0], "f32"))
+
+
+def test_quantize_beyond_one_launch(wq):
+    """More workgroups of 1024 threads than one launch holds."""
+    import torch
+
+    _say("beyond one launch")
+    n, k = (1 << 22) + 5, 4104
+    base = torch.randn((1024, k), device="cuda").to(torch.bfloat16)
+    x = base.repeat(n // 1024 + 1, 1)[:n]
+    q = wq.wq_quantize_i8(x)
+    want = wq.wq_quantize_i8(base)
+    for at in (0, n // 2, n - 5):
+        rows = torch.arange(at, at + 5, device="cuda")
+        assert torch.equal(q.codes[rows], want.codes[rows % 1024]) and torch.equal(q.scales[rows], want.scales[rows % 1024])

@@ -229,3 +229,22 @@ def test_rows_beyond_32_bits(wq):
     dx, _ = wq.wq_rms_norm_grad(y, x, w, total)
     d2, _ = wq.wq_rms_norm_grad(y[-5:].clone(), x[-5:].clone(), w, total[-5:].clone())
     assert torch.equal(dx[-5:], d2)
+
+
+def test_columns_beyond_one_launch(wq):
+    """Two rows of more than 2^28 values: the weight's gradient takes several launches."""
+    import torch
+
+    print("columns beyond one launch", flush=True)
+    k = (1 << 28) + 72
+    x = torch.randn((2, 1 << 20), device="cuda").to(torch.bfloat16).repeat(1, k // (1 << 20) + 1)[:, :k].contiguous()
+    dy = torch.roll(x, 1, 0)
+    w = torch.ones(k, device="cuda", dtype=torch.bfloat16)
+    dx, dw = wq.wq_rms_norm_grad(dy, x, w)
+    inv = [1 / (x[i].double().square().mean() + EPS).sqrt().item() for i in range(2)]
+    for at in (0, k // 2, k - 64):
+        s = slice(at, at + 64)
+        ref = sum(dy[i, s].double() * x[i, s].double() * inv[i] for i in range(2))
+        mags = sum((dy[i, s].double() * x[i, s].double() * inv[i]).abs() for i in range(2))
+        # the mean's chain of additions is k / 1024 long
+        assert ((dw[s].double() - ref).abs() <= (i8.additions(k) + 20) * i8.U * mags + 1e-30).all()

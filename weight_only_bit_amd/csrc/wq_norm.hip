@@ -440,10 +440,10 @@ __global__ __launch_bounds__(LANES < 256 ? 256 : LANES) void norm_grad_kernel(co
 // (and four waves) their way back took longer than the kernel before (4096 x 8192: 35 us).
 constexpr int kPartWaves = 16;
 __global__ __launch_bounds__(64 * kPartWaves) void norm_parts_kernel(const float* __restrict__ parts, int32_t count,
-                                                                     int64_t k, float* __restrict__ out) {
+                                                                     int64_t k, float* __restrict__ out, int64_t first) {
   __shared__ float meet[kPartWaves][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t c = (int64_t)blockIdx.x * 64 + lane;
+  const int64_t c = (first + blockIdx.x) * 64 + lane;
   const int32_t from = (int32_t)((int64_t)count * wave / kPartWaves), to = (int32_t)((int64_t)count * (wave + 1) / kPartWaves);
   float s = 0.f;
   if (c < k) {
@@ -589,9 +589,9 @@ hipError_t launch_norm_grad(const void* dy, int f32, const void* d_sum, const vo
     if (e != hipSuccess) return e;
   }
   if (!d_weight || wgs == 1) return hipSuccess;  // (no workgroup: no parts, zeros)
-  hipLaunchKernelGGL(norm_parts_kernel, dim3((unsigned)((k + 63) / 64)), dim3(64 * kPartWaves), 0, stream, parts, (int32_t)wgs, k,
-                     d_weight);
-  return hipGetLastError();
+  return launch_in_parts((k + 63) / 64, [&](int64_t first, dim3 grid) {
+    hipLaunchKernelGGL(norm_parts_kernel, grid, dim3(64 * kPartWaves), 0, stream, parts, (int32_t)wgs, k, d_weight, first);
+  }, 64 * kPartWaves);
 }
 
 }  // namespace wq
