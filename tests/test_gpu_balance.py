@@ -148,6 +148,32 @@ def test_counts_of_several_calls(wq):
     _check(wq, z[:400], ids[:400], "f32", 0.5, 2.0, counts.cpu().numpy().astype(np.int64))
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("E", [1, 4, 8, 60, 512])
+def test_experts_used_alike(wq, dtype, E):
+    """Equal counts have no gradient; of counts a millionth apart it keeps its digits: each value's error is the
+    probabilities' (spans below 24 and sums of up to 512: under 64 * 2^-23) relative to what it is made of, the shares'
+    distances from the mean, not the shares."""
+    import torch
+
+    z, ids = _inputs(200, 2, E, dtype, 21)
+    zc, ic = z.cuda(), torch.from_numpy(ids).cuda()
+    pairs = np.full(E, 10**6, dtype=np.int64)
+    counts = np.append(pairs, 200)
+    d = wq.wq_moe_balance_loss_grad(zc, ic, torch.from_numpy(counts.astype(np.int32)).cuda(), 0.5)
+    assert (d == 0).all()
+    pairs += np.arange(E) % 3
+    counts = np.append(pairs, 200)
+    d = wq.wq_moe_balance_loss_grad(zc, ic, torch.from_numpy(counts.astype(np.int32)).cuda(), 0.5)
+    x = z.double().numpy()
+    p = np.exp(x - x.max(1, keepdims=True))
+    p /= p.sum(1, keepdims=True)
+    over = (E * pairs - pairs.sum()) / pairs.sum()  # whole numbers, one rounding
+    rd = 0.5 / 200 * p * (over - (p * over).sum(1, keepdims=True))
+    mags = 0.5 / 200 * p * (np.abs(over) + (p * np.abs(over)).sum(1, keepdims=True))
+    i8.assert_within(i8.to_host(d), rd, 4 * 64 * 2.0 ** -23 * mags + i8.HALF[dtype] * np.abs(rd) + 2.0 ** -133, "d")
+
+
 def test_gradient_against_differences(wq):
     rng = np.random.default_rng(2)
     z, ids = _inputs(60, 3, 20, "f32", 12)
