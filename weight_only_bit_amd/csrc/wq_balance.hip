@@ -359,15 +359,17 @@ __global__ __launch_bounds__(kGradThreads) void balance_grad_kernel(const T* __r
   for (int e = lane; e < experts; e += 64) all += counts[e];
   for (int d = 32; d >= 1; d >>= 1) all += __shfl_xor(all, d);
   // share_e - 1 = (E c_e - sum c) / sum c: the p of a token sum to 1, so the formula holds as well with what a share
-  // has over the mean, and that is a whole number's rounding; shares near 1 would lose the digits that differ
-  // (and experts that are used alike get a gradient of zero).
+  // has over the mean, a whole number (below 2^53) and one rounding; shares near 1 would lose the digits that
+  // differ (and experts that are used alike get a gradient of zero).
   const float scale = all > 0 ? 1.f / (float)all : 0.f;
   float share[P][R::PE];
 #pragma unroll
   for (int p = 0; p < P; ++p)
 #pragma unroll
     for (int i = 0; i < R::PE; ++i)
-      share[p][i] = R::expert(p, i) < experts ? (float)((int64_t)experts * counts[R::expert(p, i)] - all) * scale : 0.f;
+      share[p][i] = R::expert(p, i) < experts
+                        ? (float)__builtin_fma((double)counts[R::expert(p, i)], (double)experts, -(double)all) * scale
+                        : 0.f;
   const int32_t tokens = counts[experts];
   const float slope = tokens > 0 ? coefficient / (float)tokens * (d_loss ? *d_loss : 1.f) : 0.f;
   const int64_t stride = (int64_t)gridDim.x * each;
