@@ -28,6 +28,9 @@ __device__ __forceinline__ void store_out(void* out, int f32, int64_t at, float 
 // row l % 16 of A (column of B) and 16 codes; it receives D[4 (l / 16) + i][l % 16].  Instruction i
 // of a step of 256 along k takes 64 of them, lane group q = l / 16 the codes 16 q .. 16 q + 15: a load touches
 // one 64-byte line of every row.
+// Bound by the weights' way: one round trip to memory and what a CU takes in, where the workgroups are few (1, 8, 32 x
+// 4096, k 4096: 6.4, 7.2, 9.4 us, 16.8 MB), memory where they are many (32 tokens, top-8 of 64 experts, 3584 x 8192:
+// gate+up 600 us, 6.2 TB/s; 8192 x 3584: down 316).  More waves (8, 16) or deeper prefetch gain nothing.
 // ---------------------------------------------------------------------------------------------
 __device__ __forceinline__ i32x4 mfma16(const u32x4& a, const u32x4& b, const i32x4& c) {
   return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, a), __builtin_bit_cast(i32x4, b), c, 0, 0, 0);
@@ -292,6 +295,12 @@ hipError_t launch_narrow(const I8Args& a, hipStream_t s) {
 //   * The next slice's fragments are read under the current slice's MFMAs; the last slice of a stage is
 //     multiplied after the barrier that ends the stage, over the next stage's first reads.
 //   * The scales of the tile's rows and channels go to LDS at its start and meet the sums at its end.
+//   * 4096 x 8192, k 8192: 222 to 231 us, 2.38 to 2.48 PFLOP/s, bound by power: the matrix units are 0.76 busy at a
+//     clock that falls to 1.54 GHz.  8192 x 8192: 435 to 450 us, 2.44 to 2.53.
+//   * Experts (64, top-8 of 4096 tokens): gate+up 3584 x 8192 1955 to 1993 us (0.66 busy), down 8192 x 3584 1060 to
+//     1095 (0.55 busy): a tile's start and end, which do no matrix work, over its 64 or 28 stages, and the tiles that
+//     routing cuts short (exactly 512 rows an expert: down 980 to 990; one expert: 863).  Such tiles take a height of 64, 128,
+//     192 or 256 rows.
 // Results of rows behind a ragged tile's end and of columns behind N are not stored.
 // ---------------------------------------------------------------------------------------------
 constexpr int kStageBytes = 128;  // codes of one row of a stage
