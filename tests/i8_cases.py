@@ -4,19 +4,20 @@ runs them."""
 from collections import namedtuple
 
 # The names of csrc/wq_i8_select.hpp, in its order.
-KERNELS = ("I8_STREAM_16", "I8_STREAM_32", "I8_NARROW_32x16", "I8_NARROW_64x16", "I8_NARROW_64x32", "I8_TILES_64", "I8_TILES_128", "I8_TILES_128x256", "I8_TILES_256")
+KERNELS = ("I8_STREAM_16", "I8_STREAM_32", "I8_NARROW", "I8_TILES_64", "I8_TILES_128", "I8_TILES_128x256", "I8_TILES_256")
 
 Dense = namedtuple("Dense", "kernel m n k")
 # n that no 16-byte piece divides, k whose last step or stage (256, 128) ends inside; the last row tile of the
 # large tiles has at most 64 rows, 65 to 128, 129 to 192, or more
 DENSE = [Dense("I8_STREAM_16", 1, 1, 64), Dense("I8_STREAM_16", 9, 77, 576), Dense("I8_STREAM_16", 300, 77, 192),
-         Dense("I8_STREAM_32", 100, 1025, 1088), Dense("I8_STREAM_32", 32, 4097, 64),
-         Dense("I8_NARROW_32x16", 17, 6150, 64), Dense("I8_NARROW_32x16", 32, 6145, 832),
-         Dense("I8_NARROW_32x16", 31, 6151, 576), Dense("I8_NARROW_64x16", 33, 4099, 64),
-         Dense("I8_NARROW_64x16", 100, 1700, 320), Dense("I8_NARROW_64x16", 128, 1701, 1088),
-         Dense("I8_NARROW_64x16", 333, 1111, 704), Dense("I8_NARROW_64x32", 250, 3105, 192),
-         Dense("I8_NARROW_64x32", 70, 8190, 576), Dense("I8_TILES_64", 513, 3000, 1088),
-         Dense("I8_TILES_64", 20, 24600, 64),
+         Dense("I8_STREAM_32", 100, 1001, 1088), Dense("I8_STREAM_32", 32, 4095, 64),
+         Dense("I8_NARROW", 33, 2100, 64), Dense("I8_NARROW", 100, 1101, 320), Dense("I8_NARROW", 64, 4099, 576),
+         Dense("I8_NARROW", 127, 1053, 832), Dense("I8_NARROW", 128, 1701, 1088), Dense("I8_NARROW", 1500, 129, 192),
+         # every number of stages modulo the four that are on their way
+         Dense("I8_TILES_64", 20, 24600, 64), Dense("I8_TILES_64", 250, 3105, 192), Dense("I8_TILES_64", 100, 2601, 320),
+         Dense("I8_TILES_64", 64, 6000, 512), Dense("I8_TILES_64", 70, 8190, 576), Dense("I8_TILES_64", 333, 1111, 704),
+         Dense("I8_TILES_64", 32, 6145, 832), Dense("I8_TILES_64", 17, 4130, 960), Dense("I8_TILES_64", 513, 3000, 1088),
+         Dense("I8_TILES_64", 9, 8177, 1152), Dense("I8_TILES_64", 3, 24577, 448),
          Dense("I8_TILES_128", 1300, 1701, 832), Dense("I8_TILES_128", 1380, 1700, 448),
          Dense("I8_TILES_128x256", 1440, 4100, 1344), Dense("I8_TILES_128x256", 1500, 4099, 320),
          Dense("I8_TILES_256", 3100, 4097, 1088), Dense("I8_TILES_256", 3172, 4100, 1152),

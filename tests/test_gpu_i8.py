@@ -145,8 +145,8 @@ def test_gemm(wq, case, out):
     assert (pad[case.m * case.n:] == 7).all()  # nothing behind the output
 
 
-# streaming, few columns a workgroup of each kind, tiles of 64, 128, 128 x 256 and 256
-@pytest.mark.parametrize("m,n,k", [(1, 16, 131008), (100, 1025, 65600), (32, 6145, 65600), (64, 3100, 131008), (70, 8190, 65600),
+# streaming, few columns a workgroup, tiles of 64, 128, 128 x 256 and 256
+@pytest.mark.parametrize("m,n,k", [(1, 16, 131008), (100, 1025, 65600), (32, 6145, 65600), (64, 3100, 131008), (70, 8190, 65600), (9, 8177, 65600),
                                    (200, 8190, 65600), (1300, 1701, 131008), (1440, 4100, 65600), (3100, 4097, 131008)])
 def test_gemm_largest_sums(wq, m, n, k):
     """Every code -128, or 127 against -128: the largest sums of either sign stay in int32."""

@@ -365,7 +365,7 @@ def test_limits_of_the_tiles(rules):
     dense = lambda *a: KERNELS[rules.dense(*a)]
     # one expert's codes: n k up to 2^31 - 1024
     assert dense(64, (1 << 20) - 1, 2048).startswith("I8_TILES") and dense(64, 1 << 20, 2048) == "I8_STREAM_32"
-    assert dense(4096, 8192, 64) == "I8_TILES_256" and dense(16, 1 << 20, 1024) == "I8_STREAM_16"
+    assert dense(4096, 8192, 64) == "I8_TILES_256" and dense(16, 4096, 1024) == "I8_STREAM_16"
     # gate+up gathers its tokens from all of them: 262143 tokens of hidden 8192
     for t, tiles in ((262143, True), (262144, False)):
         assert (KERNELS[rules.experts(t, 8 * t, 3584, 8192, 64)] != "I8_STREAM_16") == tiles

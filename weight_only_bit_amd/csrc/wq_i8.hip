@@ -171,21 +171,19 @@ hipError_t launch_stream(const I8Args& a, int64_t gy, int64_t gz, hipStream_t s)
 }
 
 // ---------------------------------------------------------------------------------------------
-// Tens to hundreds of rows: 16 CT columns and 16 MT rows a workgroup.  A CU takes in 15 to 20 KB/us from memory,
-// however much it has asked for (64 x 64 tiles of 128 x 4096, k 4096: 19.3 us on 128 CUs with one stage on its way or
-// eight, 9.2 with the weights in L2), so the weights' columns are cut so finely that every CU brings some of them,
-// and the rows, which L2 holds, are read again: 64 x 8192, k 8192 26 us (38 with 64 x 64 tiles, 47 streaming).
+// Tens to hundreds of rows and few outputs: 32 rows by 16 columns a workgroup, where 64 x 64 tiles would leave most
+// CUs without one.  A CU takes in 15 to 25 KB/us from memory, so the weights' columns are cut so finely that every
+// CU brings some of them, and the rows, which L2 holds, are read again: 64 x 2560, k 8192 19.7 us (22.1 with 64 x 64
+// tiles, 24.5 streaming), 128 x 2048, k 4096 8.9 (9.9, 13.4).
 //   * Stages of 256 bytes of a row, 16 lanes a row; two of them on their way in registers, two in LDS, 16-byte
-//     piece p of row r in slot p ^ (r % 16): writes and fragment reads are free of bank conflicts.  Four, six or
-//     eight on their way gain nothing (64 x 8192: 27.4 to 28.5): a CU has two or three workgroups.
+//     piece p of row r in slot p ^ (r % 16): writes and fragment reads are free of bank conflicts.
 //   * Wave v multiplies the codes 64 v .. 64 v + 63 of every stage, so each piece of LDS is read once; the waves'
 //     sums meet in LDS at the end.
 //   * The weights are the A operand: a lane ends with four consecutive outputs of one row.
 // ---------------------------------------------------------------------------------------------
-template <int MT, int CT>
 __global__ __launch_bounds__(256) void i8_narrow_kernel(const I8Args a) {
-  constexpr int XR = 16 * MT, WR = 16 * CT, NC = MT + CT;  // rows of a stage, loads of a thread and stage
-  constexpr int kRow = 256;                 // bytes of a row of a stage
+  constexpr int MT = 2, XR = 16 * MT, WR = 16, NC = MT + 1;  // rows of a stage, loads of a thread and stage
+  constexpr int kRow = 256;                                  // bytes of a row of a stage
   __shared__ __attribute__((aligned(16))) uint8_t buf0[(XR + WR) * kRow], buf1[(XR + WR) * kRow];
   const int tid = threadIdx.x, lane = tid & 63, nl = lane & 15, q = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -203,8 +201,8 @@ __global__ __launch_bounds__(256) void i8_narrow_kernel(const I8Args a) {
     const int at = (int)((off + (uint32_t)g * kRow) | (g == last && behind ? 0x7FFFFFF0u : 0u));
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
-      const int8_t* const base = i < MT ? a.x_codes + (m0 + 16 * i) * K : a.w0_codes + (n0 + 16 * (i - MT)) * K;
-      const int have = i < MT ? rows - 16 * i : cols - 16 * (i - MT);
+      const int8_t* const base = i < MT ? a.x_codes + (m0 + 16 * i) * K : a.w0_codes + n0 * K;
+      const int have = i < MT ? rows - 16 * i : cols;
       const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t*>(base), (short)0,
                                                           have <= 0 ? 0 : (have < 16 ? have : 16) * K, 0x00020000);
       v[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rsrc, at, 0, 0));
@@ -215,11 +213,9 @@ __global__ __launch_bounds__(256) void i8_narrow_kernel(const I8Args a) {
     for (int i = 0; i < NC; ++i) *reinterpret_cast<u32x4*>(buf + to + i * 16 * kRow) = v[i];
   };
 
-  i32x4 acc[CT][MT];
+  i32x4 acc[MT];
 #pragma unroll
-  for (int c = 0; c < CT; ++c)
-#pragma unroll
-    for (int t = 0; t < MT; ++t) acc[c][t] = (i32x4){0, 0, 0, 0};
+  for (int t = 0; t < MT; ++t) acc[t] = (i32x4){0, 0, 0, 0};
   const uint32_t from = (uint32_t)(nl * kRow + (((4 * wave + q) ^ nl) << 4));
   u32x4 even[NC], odd[NC];
   fetch(even, 0);
@@ -235,9 +231,7 @@ __global__ __launch_bounds__(256) void i8_narrow_kernel(const I8Args a) {
     if (g < last) put(next, there);
     if (g + 3 < stages) fetch(next, g + 3);
 #pragma unroll
-    for (int c = 0; c < CT; ++c)
-#pragma unroll
-      for (int t = 0; t < MT; ++t) acc[c][t] = mfma16(f[MT + c], f[t], acc[c][t]);
+    for (int t = 0; t < MT; ++t) acc[t] = mfma16(f[MT], f[t], acc[t]);
     __syncthreads();  // stage g has been read, stage g + 1 is written
   };
   for (int32_t g = 0; g < stages; g += 2) {
@@ -245,37 +239,25 @@ __global__ __launch_bounds__(256) void i8_narrow_kernel(const I8Args a) {
     if (g + 1 < stages) stage(g + 1, even, buf1, buf0);
   }
 
-  // CT rounds, each with its columns' sums of the four waves
   i32x4* const red = reinterpret_cast<i32x4*>(buf0);  // [wave][row tile][lane]
 #pragma unroll
-  for (int c = 0; c < CT; ++c) {
-    if (c > 0) __syncthreads();
+  for (int t = 0; t < MT; ++t) red[(wave * MT + t) * 64 + lane] = acc[t];
+  __syncthreads();
+  const int row = 16 * wave + nl;  // row tile t is finished by wave t
+  if (wave >= MT || row >= rows) return;
+  i32x4 v = red[wave * 64 + lane];
 #pragma unroll
-    for (int t = 0; t < MT; ++t) red[(wave * MT + t) * 64 + lane] = acc[c][t];
-    __syncthreads();
-    const int64_t n = n0 + 16 * c + 4 * q;
-    float sw[4];
+  for (int w = 1; w < 4; ++w) v += red[(w * MT + wave) * 64 + lane];
+  const float sx = a.x_scales[m0 + row];
+  const int64_t n = n0 + 4 * q, at = (m0 + row) * a.N + n;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) sw[i] = bf16_bits_to_f32(a.w0_scales[n + i < a.N ? n + i : a.N - 1]);
-    for (int t = wave; t < MT; t += 4) {
-      const int row = 16 * t + nl;
-      if (row >= rows) continue;
-      const float sx = a.x_scales[m0 + row];
-      i32x4 v = red[t * 64 + lane];
-#pragma unroll
-      for (int w = 1; w < 4; ++w) v += red[(w * MT + t) * 64 + lane];
-      const int64_t at = (m0 + row) * a.N + n;
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (n + i < a.N) store_out(a.out, a.out_f32, at + i, (float)v[i] * sx * sw[i]);
-    }
-  }
+  for (int i = 0; i < 4; ++i)
+    if (n + i < a.N) store_out(a.out, a.out_f32, at + i, (float)v[i] * sx * bf16_bits_to_f32(a.w0_scales[n + i]));
 }
 
-template <int MT, int CT>
 hipError_t launch_narrow(const I8Args& a, hipStream_t s) {
-  hipLaunchKernelGGL((i8_narrow_kernel<MT, CT>),
-                     dim3((unsigned)i8_ceil_div(a.N, 16 * CT), (unsigned)i8_ceil_div(a.M, 16 * MT)), dim3(256), 0, s, a);
+  hipLaunchKernelGGL(i8_narrow_kernel, dim3((unsigned)i8_ceil_div(a.N, 16), (unsigned)i8_ceil_div(a.M, 32)), dim3(256), 0,
+                     s, a);
   return hipGetLastError();
 }
 
@@ -290,8 +272,8 @@ hipError_t launch_narrow(const I8Args& a, hipStream_t s) {
 //     stage takes piece 4 h + s, so a lane's four pieces are 64 contiguous bytes.
 //   * Rows of a stage are 128 bytes in LDS, 16-byte piece p of row r in slot p ^ (r / 2 % 8), which keeps
 //     the fragment reads free of bank conflicts; 8 lanes load a row.
-//   * Two buffers; codes pass through registers, which hold a third stage on its way, so loads and LDS writes
-//     spread over the whole stage.
+//   * Two buffers; codes pass through registers, which hold a third stage on its way (64 x 64 tiles: four more), so
+//     loads and LDS writes spread over the whole stage.
 //   * The next slice's fragments are read under the current slice's MFMAs; the last slice of a stage is
 //     multiplied after the barrier that ends the stage, over the next stage's first reads.
 //   * The scales of the tile's rows and channels go to LDS at its start and meet the sums at its end.
@@ -449,8 +431,11 @@ __device__ __forceinline__ void i8_tile(const I8Args& a, const TileLds& lds, int
                   : lds.w[ST] + (32 * (i - NX) + 8 * wave) * kStageBytes;
   };
   // A stage's codes pass through NC registers of 16 bytes per lane, in four groups: fetch loads group q of
-  // stage g, put writes it to a buffer.
-  u32x4 held[NC];
+  // stage g, put writes it to a buffer.  64 x 64 tiles, whose stages are short, have four sets of them, so that a
+  // load has four stages to arrive (1, 2, 4, 8 sets: 128 x 4096, k 4096 19.4, 15.0, 13.0, 13.8 us; 64 x 8192, k 8192 38,
+  // 28, 24.5, 25.2); larger ones gain nothing (128 x 128, 4 sets: 1024 x 4096 23.5 / 24.4, 256 x 256, 2: 224 / 226).
+  constexpr int SETS = WM * WN == 1 ? 4 : 1;
+  u32x4 held[SETS][NC];
   auto fetch_to = [&](u32x4* to, int32_t g, auto qc) __attribute__((always_inline)) {
     constexpr int Q = decltype(qc)::value;
 #pragma unroll
@@ -465,8 +450,8 @@ __device__ __forceinline__ void i8_tile(const I8Args& a, const TileLds& lds, int
     for (int i = NC * Q / 4; i < NC * (Q + 1) / 4; ++i)
       *reinterpret_cast<u32x4*>(stage_rows(i, stc) + lane * 16) = from[i];
   };
-  auto fetch = [&](int32_t g, auto qc) __attribute__((always_inline)) { fetch_to(held, g, qc); };
-  auto put = [&](auto qc, auto stc) __attribute__((always_inline)) { put_from(held, qc, stc); };
+  auto fetch = [&](int32_t g, auto qc, int set) __attribute__((always_inline)) { fetch_to(held[set], g, qc); };
+  auto put = [&](auto qc, auto stc, int set) __attribute__((always_inline)) { put_from(held[set], qc, stc); };
   auto load_scales = [&]() __attribute__((always_inline)) {
     for (int r = tid; r < XR; r += 256) lds.sx[r] = a.x_scales[token_row(r)];
     for (int r = tid; r < WR; r += 256) {
@@ -512,8 +497,8 @@ __device__ __forceinline__ void i8_tile(const I8Args& a, const TileLds& lds, int
   constexpr std::integral_constant<int, 2> c2{};
   constexpr std::integral_constant<int, 3> c3{};
 
-  // ---- prologue: stage 0 and the first group of stage 1 written, the rest of stage 1 and the first group of
-  // stage 2 on their way; stage 0's first slice read ----
+  // ---- prologue: stage 0 and the first group of stage 1 written, the rest of stages 1 .. SETS and the first group
+  // of the one behind on their way; stage 0's first slice read ----
   Frag X;
   {
     u32x4 early[NC];
@@ -521,28 +506,32 @@ __device__ __forceinline__ void i8_tile(const I8Args& a, const TileLds& lds, int
     fetch_to(early, 0, c1);
     fetch_to(early, 0, c2);
     fetch_to(early, 0, c3);
-    fetch(1, c0);
-    fetch(1, c1);
-    fetch(1, c2);
-    fetch(1, c3);
+#pragma unroll
+    for (int i = 1; i <= SETS; ++i) {
+      fetch(i, c0, i % SETS);
+      fetch(i, c1, i % SETS);
+      fetch(i, c2, i % SETS);
+      fetch(i, c3, i % SETS);
+    }
     load_scales();
     put_from(early, c0, c0);
     put_from(early, c1, c0);
     put_from(early, c2, c0);
     put_from(early, c3, c0);
-    put(c0, c1);
-    fetch(2, c0);
+    put(c0, c1, 1 % SETS);
+    fetch(SETS + 1, c0, 1 % SETS);
     __syncthreads();
     read(X, 0, c0);
   }
 
-  // ---- stage g in buffers ST = g % 2 ----
+  // ---- stage g, u = g % max(SETS, 2), in buffers ST = g % 2 ----
   // Each slice's MFMAs cover the next slice's fragment reads, one group's writes to the other
-  // buffers (a stage ahead) and, into the registers that frees, its loads (two stages ahead): a
-  // load has a whole stage to arrive, and no wait but a write's own counts it.
+  // buffers (a stage ahead) and, into the registers that frees, its loads (1 + SETS stages ahead): a
+  // load has SETS stages to arrive, and no wait but a write's own counts it.
   // Masks: 0x8 MFMA, 0x20 loads, 0x100 LDS reads, 0x200 LDS writes.
-  auto stage = [&](int32_t g, auto stc) __attribute__((always_inline)) {
-    constexpr int ST = decltype(stc)::value;
+  auto stage = [&](int32_t g, auto uc) __attribute__((always_inline)) {
+    constexpr int u = decltype(uc)::value, ST = u % 2, one = (u + 1) % SETS, two = (u + 2) % SETS;
+    constexpr std::integral_constant<int, ST> stc{};
     constexpr std::integral_constant<int, ST ^ 1> other{};
     constexpr int NF = WM * WN, NR = WM + WN;  // MFMAs and fragment reads of a slice
     constexpr int NP = (NC + 3) / 4;           // pieces of a group
@@ -562,18 +551,18 @@ __device__ __forceinline__ void i8_tile(const I8Args& a, const TileLds& lds, int
     Frag Y;
     __builtin_amdgcn_sched_barrier(0);
     read(Y, 1, stc);
-    put(c1, other);
-    fetch(g + 2, c1);
+    put(c1, other, one);
+    fetch(g + 1 + SETS, c1, one);
     mma(X);
     interleave();
     read(X, 2, stc);
-    put(c2, other);
-    fetch(g + 2, c2);
+    put(c2, other, one);
+    fetch(g + 1 + SETS, c2, one);
     mma(Y);
     interleave();
     read(Y, 3, stc);
-    put(c3, other);
-    fetch(g + 2, c3);
+    put(c3, other, one);
+    fetch(g + 1 + SETS, c3, one);
     mma(X);
     interleave();
     // This wave's writes of stage g + 1 are done and its reads of stage g returned; after the barrier
@@ -582,17 +571,26 @@ __device__ __forceinline__ void i8_tile(const I8Args& a, const TileLds& lds, int
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
     read(X, 0, other);
-    put(c0, stc);
-    fetch(g + 3, c0);
+    put(c0, stc, two);
+    fetch(g + 2 + SETS, c0, two);
     mma(Y);
     interleave();
   };
+  constexpr int U = SETS > 2 ? 4 : 2;
   int32_t g = 0;
-  for (; g + 1 < steps; g += 2) {
+  for (; g + U <= steps; g += U) {
     stage(g, c0);
     stage(g + 1, c1);
+    if constexpr (U == 4) {
+      stage(g + 2, c2);
+      stage(g + 3, c3);
+    }
   }
   if (g < steps) stage(g, c0);
+  if constexpr (U == 4) {
+    if (g + 1 < steps) stage(g + 1, c1);
+    if (g + 2 < steps) stage(g + 2, c2);
+  }
 
   // ---- epilogue, straight from registers ----
   float sx[WM];
@@ -690,9 +688,7 @@ hipError_t product_dense(const I8Args& a, hipStream_t stream) {
     case I8_TILES_128x256: return launch_tiles<MODE_DENSE, 2, 4>(a, 1, stream);
     case I8_TILES_128: return launch_tiles<MODE_DENSE, 2, 2>(a, 1, stream);
     case I8_TILES_64: return launch_tiles<MODE_DENSE, 1, 1>(a, 1, stream);
-    case I8_NARROW_64x32: return launch_narrow<4, 2>(a, stream);
-    case I8_NARROW_64x16: return launch_narrow<4, 1>(a, stream);
-    case I8_NARROW_32x16: return launch_narrow<2, 1>(a, stream);
+    case I8_NARROW: return launch_narrow(a, stream);
     case I8_STREAM_32: return stream_dense<2>(a, stream);
     default: return stream_dense<1>(a, stream);
   }

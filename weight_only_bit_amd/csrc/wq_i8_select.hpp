@@ -10,9 +10,7 @@ namespace wq {
 enum I8Kernel : int32_t {
   I8_STREAM_16 = 0,  // 16 x 16, weights straight from memory
   I8_STREAM_32,      // 32 x 16
-  I8_NARROW_32x16,   // few columns a workgroup, staged in LDS
-  I8_NARROW_64x16,
-  I8_NARROW_64x32,
+  I8_NARROW,         // 32 x 16, staged in LDS
   I8_TILES_64,       // 64 x 64
   I8_TILES_128,      // 128 x 128
   I8_TILES_128x256,
@@ -37,33 +35,30 @@ inline bool i8_tiles_fit(int64_t gathered, int64_t N, int64_t K) {
 //     4096 x 4096, k 1024: 24 / 28, k 4096: 62 / 73;  1024 x 8192 (128), k 8192: 79 / 68
 //   128 x 256 where those do (128 x 256 / 128 x 128): 1024 x 8192 (256), k 8192: 68 / 75;  2048 x 4096, k 4096: 37 /
 //     41;  2048 x 2048 (128), k 4096: 30 / 24
-//   128 x 128 above half the chip (128 x 128 / 64 x 64): 640 x 4096 (160), k 4096: 22.8 / 31.5;  512 x 4096 (128):
-//     22.9 / 21.0;  256 x 8192 (128), k 8192: 43.3 / 42.1
-//   64 x 64 above it (64 x 64 / 64 x 32): 200 x 8192 (512), k 8192: 40 / 58;  64 x 28672 (448), k 4096: 31 / 45;  32 x
-//     28672 30 against 45 streaming and 37 with 32 x 16;  256 x 4096 (256): 19.1 / 16.3;  128 x 8192 (256): 37 / 31
-//   32 columns a workgroup, then 16 (64 x 32 / 64 x 16): 128 x 8192 (256 tiles of 64 x 64): 31 / 44;  256 x 4096: 16.3 /
-//     22;  64 x 8192 (128): 26.0 / 26.1;  128 x 4096 (128): 14.4 / 13.8
-//   streaming where those would leave CUs without a workgroup (streaming / 64 x 16): 64 x 4096 (256 workgroups), k
-//     4096: 14.2 / 12.6, k 1024: 5.7 / 5.1;  256 x 1024 (256), k 8192: 24 / 19.5;  48 x 2048 (128): 14.0 / 20.1;  and up
-//     to 32 rows (/ 32 x 16) 32 x 4096 (256): 9.5 / 11.7;  32 x 8192 (512), k 8192: 26.6 / 23.0;  16 rows stream
+//   128 x 128 above half the chip (128 x 128 / 64 x 64): 640 x 4096 (160), k 4096: 22.8 / 26.1;  320 x 8192 (192), k
+//     8192: 41 / 54;  512 x 4096 (128): 22.9 / 19.1;  256 x 8192 (128), k 8192: 43.4 / 39.1
+//   64 x 64 from a third of the chip on (64 x 64 / 32 x 16 / streaming 32 x 16): 128 x 4096 (128 tiles), k 4096: 13.0 /
+//     14.2 / 25;  333 x 1111 (108), k 4160: 10.9 / 11.8 / 16.9;  48 x 5120 (80), k 8192: 21.1 / 21.8 / 33;  256 x 1280
+//     (80), k 4096: 10.1 / 9.6 / 18.8;  64 x 4608 (72): 13.8 / 13.3 / 19.5;  256 x 1024 (64), k 8192: 15.9 / 14.1 / 24;
+//     17 to 32 rows 32 x 8192 (128), k 8192: 20.9 / 23.1 / 26.2;  32 x 4112 (65), k 4096: 11.7 / 12.1 / 14.2
+//   streaming where its workgroups are at most one for every CU (streaming / 32 x 16): 32 x 4096 (256), k 4096: 9.5 /
+//     11.7;  64 x 2048 (256): 8.6 / 8.6;  96 x 2048 (384): 13.5 / 8.9;  64 x 4096 (512): 14.3 / 12.2;  and 16 rows where
+//     those are (16 x 16 / 32 x 16): 32 x 2048 (256) 6.7 / 8.5;  200 x 300 (247), k 8192: 10.4 / 13.8;  32 x 2560 (320), k
+//     4096: 9.9 / 8.6;  64 x 1536 (384): 10.0 / 8.6
+//   up to 16 rows 64 x 64 where the weights are many (64 x 64 / 16 x 16): 16 x 11264 (176), k 4096: 13.5 / 15.7;  16 x
+//     8192 (128): 11.8 / 11.9, k 8192: 19.7 / 20.6;  16 x 6144 (96), k 4096: 11.2 / 11.3;  8 x 28672 (448): 27.5 / 30.7;  8 x
+//     11264: 13.4 / 13.6;  1 x 28672: 26.8 / 27.8;  1 x 16384 (256): 18.2 / 16.0;  8 x 8192 (128), k 8192: 19.2 / 18.4
 inline I8Kernel i8_dense_kernel(int64_t M, int64_t N, int64_t K) {
   const auto tiles = [&](int64_t bm, int64_t bn) { return i8_ceil_div(M, bm) * i8_ceil_div(N, bn); };
-  if (M > 16 && i8_tiles_fit(0, N, K)) {
-    if (M > 32) {
-      if (tiles(256, 256) >= 192) return I8_TILES_256;
-      if (tiles(128, 256) >= 192) return I8_TILES_128x256;
-      if (tiles(128, 128) >= 144) return I8_TILES_128;
-    }
-    if (tiles(64, 64) >= 384) return I8_TILES_64;
-    if (M > 32) {
-      if (tiles(64, 64) >= 192) return I8_NARROW_64x32;
-      if (tiles(64, 16) >= 192) return I8_NARROW_64x16;
-    } else if (tiles(32, 16) >= 384) {
-      return I8_NARROW_32x16;
-    }
-  }
-  // 16 rows a workgroup where 32 would leave CUs without one: 64 x 1024, k 8192: 10.7 against 14.2
-  return M > 16 && tiles(32, 16) >= 256 ? I8_STREAM_32 : I8_STREAM_16;
+  const bool fit = i8_tiles_fit(0, N, K);
+  if (M <= 16) return fit && tiles(64, 64) >= (M > 8 ? 128 : 384) ? I8_TILES_64 : I8_STREAM_16;
+  if (tiles(16, 16) <= 256) return I8_STREAM_16;
+  if (tiles(32, 16) <= 256 || !fit) return I8_STREAM_32;
+  if (M <= 32) return I8_TILES_64;
+  if (tiles(256, 256) >= 192) return I8_TILES_256;
+  if (tiles(128, 256) >= 192) return I8_TILES_128x256;
+  if (tiles(128, 128) >= 144) return I8_TILES_128;
+  return tiles(64, 64) >= 80 ? I8_TILES_64 : I8_NARROW;
 }
 
 // The same for experts, `pairs` rows in all, gate+up of `gathered` tokens (down: 0), by the rows that an
