@@ -29,8 +29,8 @@ __device__ __forceinline__ void store_out(void* out, int f32, int64_t at, float 
 // of a step of 256 along k takes 64 of them, lane group q = l / 16 the codes 16 q .. 16 q + 15: a load touches
 // one 64-byte line of every row.
 // Bound by the weights' way: one round trip to memory and what a CU takes in, where the workgroups are few (1, 8, 32 x
-// 4096, k 4096: 6.4, 7.2, 9.4 us, 16.8 MB), memory where they are many (32 tokens, top-8 of 64 experts, 3584 x 8192:
-// gate+up 600 us, 6.2 TB/s; 8192 x 3584: down 316).  More waves (8, 16) or deeper prefetch gain nothing.
+// 4096, k 4096: 6.0, 6.9, 9.4 us, 16.8 MB), memory where they are many (32 tokens, top-8 of 64 experts, 3584 x 8192:
+// gate+up 600 us, 6.2 TB/s; 8192 x 3584: down 316).  More waves (8, 16) gain nothing.
 // ---------------------------------------------------------------------------------------------
 __device__ __forceinline__ i32x4 mfma16(const u32x4& a, const u32x4& b, const i32x4& c) {
   return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, a), __builtin_bit_cast(i32x4, b), c, 0, 0, 0);
@@ -117,8 +117,24 @@ __global__ __launch_bounds__(64 * KS) void i8_stream_kernel(const I8Args a) {
 #pragma unroll
           for (int t = 0; t < MT; ++t) acc[j][t] = mfma16(p.x[t].c[i], p.w[j].c[i], acc[j][t]);
     };
-    // two steps at hand, the next one's loads in flight under each product
-    if (s_begin < s_end) {
+    if constexpr (MODE == MODE_DENSE) {
+      // few workgroups: four steps on their way (2 / 3 / 4: 1 x 4096, k 4096 6.6 / 6.4 / 6.0; 20 x 4096, k 8192 14.2 /
+      // 13.9 / 13.5)
+      constexpr int AHEAD = 4;
+      Step held[AHEAD];
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i)
+        if (s_begin + i < s_end) load(held[i], s_begin + i);
+      for (int32_t s = s_begin; s < s_end; s += AHEAD) {
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i)
+          if (s + i < s_end) {
+            multiply(held[i]);
+            if (s + i + AHEAD < s_end) load(held[i], s + i + AHEAD);
+          }
+      }
+    } else if (s_begin < s_end) {
+      // many: two, which leave room for more waves (2 / 3 / 4: 32 tokens, gate+up 598 / 602 / 690)
       Step A, B;
       load(A, s_begin);
       int32_t s = s_begin;
