@@ -294,9 +294,9 @@ hipError_t launch_narrow(const I8Args& a, hipStream_t s) {
 //     multiplied after the barrier that ends the stage, over the next stage's first reads.
 //   * The scales of the tile's rows and channels go to LDS at its start and meet the sums at its end.
 //   * 4096 x 8192, k 8192: 222 to 231 us, 2.38 to 2.48 PFLOP/s, bound by power: the matrix units are 0.76 busy at a
-//     clock that falls to 1.54 GHz.  8192 x 8192: 435 to 450 us, 2.44 to 2.53.
-//   * Experts (64, top-8 of 4096 tokens): gate+up 3584 x 8192 1955 to 1993 us (0.66 busy), down 8192 x 3584 1060 to
-//     1095 (0.55 busy): a tile's start and end, which do no matrix work, over its 64 or 28 stages, and the tiles that
+//     clock that falls to about 1.5 GHz.  8192 x 8192: 435 to 450 us, 2.44 to 2.53.
+//   * Experts (64, top-8 of 4096 tokens): gate+up 3584 x 8192 1955 to 1993 us (0.66 busy), down 8192 x 3584 1050 to
+//     1095 (0.56 busy): a tile's start and end, which do no matrix work, over its 64 or 28 stages, and the tiles that
 //     routing cuts short (exactly 512 rows an expert: down 980 to 990; one expert: 863).  Such tiles take a height of 64, 128,
 //     192 or 256 rows.
 // Results of rows behind a ragged tile's end and of columns behind N are not stored.
