@@ -31,8 +31,8 @@ EXPERTS = [Experts("I8_STREAM_16", True, 20, 2, 65, 576, _FEW), Experts("I8_STRE
            Experts("I8_TILES_128", False, 165, 2, 701, 832, (64, 161, 65)),
            Experts("I8_TILES_128", True, 300, 2, 2350, 704, _THREE),
            Experts("I8_TILES_128", False, 300, 2, 4701, 64, _THREE),
-           Experts("I8_TILES_128x256", True, 100, 4, 6101, 448, _EIGHT),
-           Experts("I8_TILES_128x256", False, 100, 4, 12101, 448, _EIGHT),
+           Experts("I8_TILES_128x256", True, 100, 4, 8201, 448, _EIGHT),
+           Experts("I8_TILES_128x256", False, 100, 4, 16301, 448, _EIGHT),
            Experts("I8_TILES_256", True, 700, 2, 7201, 1088, _LONG),
            Experts("I8_TILES_256", False, 700, 2, 14401, 1088, _LONG)]
 

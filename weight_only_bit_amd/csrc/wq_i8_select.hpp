@@ -71,14 +71,16 @@ inline I8Kernel i8_dense_kernel(int64_t M, int64_t N, int64_t K) {
 //     690, 378 / 379; 100 rows 719 / 712, 410 / 408; 128 rows 818 / 902, 459 / 525; 512 rows 2019 / 2329, 1112 / 1330
 //   128 x 128 where those would be few (128 x 128 / 256 x 256; 8 experts, 1024 x 1024): 128 rows (96 and 48 tiles) 9.3 /
 //     18.8, 8.2 / 17.1; 1024 rows (320 and 160) 32.5 / 41.4, 20.4 / 20.2; 16 experts, 2048 x 4096: 200 rows (456) 81 /
-//     66, 42.5 / 37.3; and (/ 128 x 256) 64 rows (384) 46.8 / 46.5, 24.8 / 26.7
+//     66, 42.5 / 37.3; and (/ 128 x 256) 64 rows (384) 46.8 / 46.5, 24.8 / 26.7;
+//     64 experts, 1024 x 2048: 8 rows (544) 43.8 / 46.4, 25.7 / 27.9, 64 rows (544) 50.4 / 52.2, 28.9 / 32.5; hidden
+//     8192, inter 3584: 8 rows (1808) 635 / 632, 329 / 330
 inline I8Kernel i8_experts_kernel(int64_t gathered, int64_t pairs, int64_t N, int64_t K, int64_t experts) {
   const int64_t active = pairs < experts ? pairs : experts;  // at most
   const double rows = (double)pairs / (double)experts;
   const int64_t cols = i8_ceil_div(gathered ? 2 * N : N, 256);
-  const bool few = (pairs / 128 + active) * cols < 512;
-  if (!i8_tiles_fit(gathered, N, K) || rows < (few ? 16.0 : gathered ? 10.0 : 4.0)) return I8_STREAM_16;
-  if (rows < 128.0) return few ? I8_TILES_128 : I8_TILES_128x256;
+  const int64_t tiles = (pairs / 128 + active) * cols;  // of 128 x 256, at most
+  if (!i8_tiles_fit(gathered, N, K) || rows < (tiles < 512 ? 16.0 : gathered ? 10.0 : 4.0)) return I8_STREAM_16;
+  if (rows < 128.0) return tiles < 700 ? I8_TILES_128 : I8_TILES_128x256;
   return (pairs / 256 + active) * cols < 400 ? I8_TILES_128 : I8_TILES_256;
 }
 
