@@ -1,0 +1,48 @@
+"""Digits of the balance loss's probabilities, and padding beside what is not finite, on the GPU against the
+definition in 64 bits."""
+import numpy as np
+import pytest
+
+import i8_testutil as i8
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def wq():
+    import torch
+
+    import weight_only_bit_amd as wq
+
+    assert torch.cuda.is_available(), "GPU tests need a GPU"
+    wq.lib()
+    return wq
+
+
+@pytest.mark.parametrize("E", [3, 9, 65, 301])
+def test_probabilities_far_from_the_largest(wq, E):
+    """Logits of 0 and of -20 to -70: the differences from the maximum are exact, so a probability's error holds no
+    multiple of them.  Counts under which expert 0 has the mean share, so that the gradients of the others are their
+    probability times their share's distance: off by the exponential (3 roundings), its sum (a chain of 16 + 5) and the
+    sum's reciprocal, the slope, the factor, the share (3), its distance and two products."""
+    import torch
+
+    rng = np.random.default_rng(E)
+    t = 300
+    z = -rng.uniform(20, 70, (t, E)).astype(np.float32)
+    z[:, 0] = 0
+    ids = rng.integers(0, E, (t, 2)).astype(np.int32)
+    pairs = np.full(E, 10000)
+    pairs[1::2] += 7000
+    pairs[2::2] -= 7000
+    counts = np.append(pairs, t)
+    d = wq.wq_moe_balance_loss_grad(torch.from_numpy(z).cuda(), torch.from_numpy(ids).cuda(),
+                                    torch.from_numpy(counts.astype(np.int32)).cuda())
+    p = np.exp(z.astype(np.float64))
+    p /= p.sum(1, keepdims=True)
+    over = (E * pairs - pairs.sum()) / pairs.sum()
+    assert over[0] == 0
+    ref = p * (over - (p * over).sum(1, keepdims=True)) / t
+    mags = p * (np.abs(over) + (p * np.abs(over)).sum(1, keepdims=True)) / t
+    assert mags[:, 1:].min() > 2.0 ** -110
+    i8.assert_within(i8.to_host(d), ref, (3 + 21 + 1 + 1 + 1 + 3 + 1 + 2) * i8.U * mags, "d_logits")
