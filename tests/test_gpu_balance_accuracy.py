@@ -46,3 +46,31 @@ def test_probabilities_far_from_the_largest(wq, E):
     mags = p * (np.abs(over) + (p * np.abs(over)).sum(1, keepdims=True)) / t
     assert mags[:, 1:].min() > 2.0 ** -110
     i8.assert_within(i8.to_host(d), ref, (3 + 21 + 1 + 1 + 1 + 3 + 1 + 2) * i8.U * mags, "d_logits")
+
+
+def test_probabilities_beside_many_small_ones(wq):
+    """One logit of 0 and 14 whose exponentials are a part of 2^-24, too small each to change a sum of one: a chain of
+    16 additions loses up to 15 of them, sums of four lose 4 + 2 halves of a step.  Sizes that are powers of two make
+    slope and shares exact, so that what is left are the exponential (3), its sum (6), the reciprocal, two products and the
+    share's distance."""
+    import torch
+
+    E, t = 16, 256
+    rng = np.random.default_rng(4)
+    z = np.zeros((t, E), np.float32)
+    z[:, 1:] = np.log(np.linspace(0.6, 0.99, t))[:, None] - 24 * np.log(2)
+    z[:, 15] = -rng.uniform(20, 70, t)
+    ids = rng.integers(0, E, (t, 2)).astype(np.int32)
+    pairs = np.full(E, 1 << 14)
+    pairs[1] -= 1 << 13
+    pairs[15] += 1 << 13
+    counts = np.append(pairs, t)
+    d = wq.wq_moe_balance_loss_grad(torch.from_numpy(z).cuda(), torch.from_numpy(ids).cuda(),
+                                    torch.from_numpy(counts.astype(np.int32)).cuda())
+    p = np.exp(z.astype(np.float64))
+    p /= p.sum(1, keepdims=True)
+    over = (E * pairs - pairs.sum()) / pairs.sum()
+    ref = p * (over - (p * over).sum(1, keepdims=True)) / t
+    mags = p * (np.abs(over) + (p * np.abs(over)).sum(1, keepdims=True)) / t
+    some = [1, 15]
+    i8.assert_within(i8.to_host(d)[:, some], ref[:, some], (3 + 6 + 1 + 2 + 1) * i8.U * mags[:, some], "d_logits")
