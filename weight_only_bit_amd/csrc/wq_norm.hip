@@ -435,34 +435,46 @@ __global__ __launch_bounds__(LANES < 256 ? 256 : LANES) void norm_grad_kernel(co
   if (tid < tail) part[tcol] = dwt;
 }
 
-// d_weight[c] = sum over the parts: 64 columns a workgroup, a sixteenth of the parts a wave, in order, and then
-// the sixteenths.  Eight loads of a lane in flight: the parts have just been written, and with one at a time
-// (and four waves) their way back took longer than the kernel before (4096 x 8192: 35 us).
+// d_weight[c] = sum over the parts, in fp64 (up to 512 of them; chains of 32 and 16 in fp32 were off by 1.25e-7 of the
+// gradient at 333 x 1111 fp32, this by 6.3e-8) and in a fixed order: 64 columns a workgroup, a sixteenth of the parts
+// a wave, and then the sixteenths.  Eight loads of a lane in flight, none under a condition: the parts have just been
+// written, and with one at a time (and four waves) their way back took longer than the kernel before (4096 x 8192:
+// 35 us).
 constexpr int kPartWaves = 16;
 __global__ __launch_bounds__(64 * kPartWaves) void norm_parts_kernel(const float* __restrict__ parts, int32_t count,
                                                                      int64_t k, float* __restrict__ out, int64_t first) {
-  __shared__ float meet[kPartWaves][64];
+  __shared__ double meet[kPartWaves][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t c = (first + blockIdx.x) * 64 + lane;
   const int32_t from = (int32_t)((int64_t)count * wave / kPartWaves), to = (int32_t)((int64_t)count * (wave + 1) / kPartWaves);
-  float s = 0.f;
+  double s = 0.0;
   if (c < k) {
-    constexpr int U = 8;
-    for (int32_t i = from; i < to; i += U) {
+    const float* p = parts + (int64_t)from * k + c;
+    int32_t left = to - from;
+    const auto add = [&](auto count) __attribute__((always_inline)) {
+      constexpr int U = decltype(count)::value;
       float v[U];
 #pragma unroll
-      for (int u = 0; u < U; ++u) v[u] = i + u < to ? parts[(int64_t)(i + u) * k + c] : 0.f;
+      for (int u = 0; u < U; ++u) v[u] = p[u * k];
+      double t[2] = {0.0, 0.0};
 #pragma unroll
-      for (int u = 0; u < U; ++u) s += v[u];
-    }
+      for (int u = 0; u < U; ++u) t[u & 1] += (double)v[u];
+      s += t[0] + t[1];
+      p += U * k;
+      left -= U;
+    };
+    while (left >= 8) add(std::integral_constant<int, 8>{});
+    if (left >= 4) add(std::integral_constant<int, 4>{});
+    if (left >= 2) add(std::integral_constant<int, 2>{});
+    if (left > 0) add(std::integral_constant<int, 1>{});
   }
   meet[wave][lane] = s;
   __syncthreads();
   if (wave == 0 && c < k) {
-    s = 0.f;
+    double all[2] = {0.0, 0.0};
 #pragma unroll
-    for (int w = 0; w < kPartWaves; ++w) s += meet[w][lane];
-    out[c] = s;
+    for (int w = 0; w < kPartWaves; ++w) all[w & 1] += meet[w][lane];
+    out[c] = (float)(all[0] + all[1]);
   }
 }
 
