@@ -382,7 +382,8 @@ wq_status wq_moe_down_i8(const int8_t* h_codes, const float* h_scales, int64_t n
  *   r = x + residual, rounded to `type` and written to sum;  inv = 1 / sqrt(mean_j r_j^2 + eps)
  *   y_j = r_j inv weight_j
  * residual and sum may both be NULL: r = x.  sum may be x or residual itself (the same address).
- * Squares are summed in fp32: where they sum to 2^128 and more inv is 0.
+ * Squares are summed in fp32: where they sum to 2^128 and more inv is 0, and so it is where both they and eps
+ * are 0 (a row of zeros, or of magnitudes below 2^-75; with eps == 0 rows below 2^-63 lose digits).
  * n == 0 is a no-op. */
 wq_status wq_rms_norm(const void* x, int32_t type, const void* residual, const void* weight,
                       float eps, int64_t n, int64_t k, void* sum, void* y, void* stream);

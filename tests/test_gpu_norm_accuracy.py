@@ -40,3 +40,35 @@ def test_large_rows_leave_the_weights_small_gradients(wq, dtype, n, k):
     inv = 1 / np.sqrt((f(row) ** 2).mean() + 1e-6)
     terms = f(dy)[16: n - 16] * f(row) * inv
     i8.assert_within(i8.to_host(dw), terms.sum(0), (i8.additions(k) + 5 + 16 + 1) * i8.U * np.abs(terms).sum(0), "d_weight")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("k", [5, 64, 1111, 8192, 70003])
+def test_rows_of_zeros_without_an_epsilon(wq, dtype, k):
+    """eps = 0: a row of zeros, or of values whose squares vanish, is normed to zeros (scale 0 in int8) and passes no
+    gradient on but the sum's own; the rows beside it, a NaN's too, are as ever."""
+    import torch
+
+    print("no epsilon", dtype, k, flush=True)
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    g = torch.Generator().manual_seed(k)
+    x, dy, ds = (torch.randn((9, k), generator=g).to(dt) for _ in range(3))
+    w = (1 + 0.1 * torch.randn(k, generator=g)).to(dt)
+    x[2], x[5] = 0, 1e-30
+    x[7, k // 2] = float("nan")
+    ok = [0, 1, 3, 4, 6, 8]
+    f = lambda t: t.double().numpy()
+    y, _ = wq.wq_rms_norm(x.cuda(), w.cuda(), eps=0.0)
+    y = y.cpu()
+    assert (y[[2, 5]] == 0).all() and y[7].isnan().all()
+    i8.assert_within(f(y[ok]), *i8.norm_bound(f(x[ok]), f(w), 0.0, dtype), "y")
+    rows, _ = wq.wq_rms_norm_i8(x.cuda(), w.cuda(), eps=0.0)
+    scales = rows.scales.cpu()
+    assert (scales[[2, 5]] == 0).all() and scales[7].isnan() and (rows.codes[[2, 7]] == 0).all()
+    assert np.array_equal(rows.codes.cpu().numpy()[ok], i8.quantize(f(x[ok]) * f(w))[0])
+    real = ok + [2, 5]
+    dx, dw = wq.wq_rms_norm_grad(dy[real].cuda(), x[real].cuda(), w.cuda(), ds[real].cuda(), eps=0.0)
+    rx, bx, rw, bw = i8.norm_grad_bounds(f(dy[ok]), f(x[ok]), f(w), 0.0, f(ds[ok]), dtype)
+    i8.assert_within(i8.to_host(dx)[:6], rx, bx, "dx")
+    assert torch.equal(dx.cpu()[6:], ds[[2, 5]])
+    i8.assert_within(i8.to_host(dw), rw, bw, "d_weight")

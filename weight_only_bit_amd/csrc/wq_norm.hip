@@ -67,6 +67,12 @@ struct __attribute__((packed)) Codes8 {
   uint32_t lo, hi;
 };
 
+// 1 / sqrt(mean + eps), and 0 where both are 0 (a row of zeros, or of values whose squares vanish in fp32).
+__device__ __forceinline__ float inverse_root(float squares, int64_t k, float eps) {
+  const float m = squares / (float)k + eps;
+  return m == 0.f ? 0.f : 1.f / sqrtf(m);
+}
+
 enum { OUT_NORM = 0, OUT_NORM_I8 = 1, OUT_ROWS = 2, OUT_WEIGHT = 3 };
 
 struct NormArgs {
@@ -184,7 +190,7 @@ __global__ __launch_bounds__(LANES < 256 ? 256 : LANES) void norm_kernel(const N
     }
   }
   float inv = 1.f;
-  if constexpr (NORM) inv = 1.f / sqrtf(ss / (float)k + a.eps);
+  if constexpr (NORM) inv = inverse_root(ss, k, a.eps);
 
   // r of the long rows comes again from where this thread left it
   const T* const again = NORM && res ? sum : x;
@@ -367,7 +373,7 @@ __global__ __launch_bounds__(LANES < 256 ? 256 : LANES) void norm_grad_kernel(co
       }
       turn ^= 1;
     }
-    const float inv = 1.f / sqrtf(ss / (float)k + a.eps);
+    const float inv = inverse_root(ss, k, a.eps);
     const float m = dot / (float)k * inv * inv;
     auto put = [&](u32x4 rv1, u32x4 gv1, u32x4 wv, u32x4 sv1, int64_t j, float (&d)[E]) __attribute__((always_inline)) {
       float f[E], g[E], w[E], s[E];
