@@ -74,3 +74,19 @@ def test_probabilities_beside_many_small_ones(wq):
     mags = p * (np.abs(over) + (p * np.abs(over)).sum(1, keepdims=True)) / t
     some = [1, 15]
     i8.assert_within(i8.to_host(d)[:, some], ref[:, some], (3 + 6 + 1 + 2 + 1) * i8.U * mags[:, some], "d_logits")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d_loss", [float("inf"), float("nan")])
+def test_padding_beside_a_loss_that_is_not_finite(wq, dtype, d_loss):
+    """Padding's gradient is zero whatever reaches the loss; the tokens' is not finite."""
+    import torch
+
+    for E in (3, 8, 64, 300):
+        z = torch.randn(40, E, device="cuda").to(torch.float32 if dtype == "f32" else torch.bfloat16)
+        ids = torch.randint(0, E, (40, 2), device="cuda", dtype=torch.int32)
+        ids[:, 0] = 0  # loaded unevenly: no gradient is zero
+        ids[30:] = -1
+        _, counts = wq.wq_moe_balance_loss(z, ids)
+        d = wq.wq_moe_balance_loss_grad(z, ids, counts, d_loss=torch.tensor(d_loss, device="cuda"))
+        assert (d[30:] == 0).all() and not d[:30].isfinite().any()

@@ -406,7 +406,7 @@ __global__ __launch_bounds__(kGradThreads) void balance_grad_kernel(const T* __r
 #pragma unroll
       for (int i = 0; i < R::PE; ++i) s[i & 3] = __builtin_fmaf(share[p][i], r.x[p][i], s[i & 3]);
     const float dot = wave_sum<L>((s[0] + s[1]) + (s[2] + s[3])) * r.inv;
-    const float factor = slope * r.inv;
+    const float factor = real ? slope * r.inv : 0.f;  // (a slope that is not finite leaves padding's zeros)
     T* const out = d_logits + tok * experts;
 #pragma unroll
     for (int p = 0; p < P; ++p) {
