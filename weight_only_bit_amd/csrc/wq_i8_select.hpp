@@ -37,6 +37,9 @@ inline bool i8_tiles_fit(int64_t gathered, int64_t N, int64_t K) {
 //     41;  2048 x 2048 (128), k 4096: 30 / 24
 //   128 x 128 above half the chip (128 x 128 / 64 x 64): 640 x 4096 (160), k 4096: 22.8 / 26.1;  320 x 8192 (192), k
 //     8192: 41 / 54;  512 x 4096 (128): 22.9 / 19.1;  256 x 8192 (128), k 8192: 43.4 / 39.1
+//   but 64 x 64 for up to 64 rows, of which a taller tile computes no more (64 x 64 / 128 x 128 / 256 x 256): 33 x 24576, k
+//     8192: 47.4 / 55.6 / 62.9;  33 x 128256, k 4096: 126.6 / 144.4 / 136.5;  64 x 28672: 30.8 / 31.3 / 35.8;  64 x
+//     128256: 130.7 / 140.6 / 137.3;  64 x 49152, k 1024: 16.7 / 15.1 / 15.5;  65 x 49152, k 4096: 60.3 / 49.2 / 50.0
 //   64 x 64 from a third of the chip on (64 x 64 / 32 x 16 / streaming 32 x 16): 128 x 4096 (128 tiles), k 4096: 13.0 /
 //     14.2 / 25;  333 x 1111 (108), k 4160: 10.9 / 11.8 / 16.9;  48 x 5120 (80), k 8192: 21.1 / 21.8 / 33;  256 x 1280
 //     (80), k 4096: 10.1 / 9.6 / 18.8;  64 x 4608 (72): 13.8 / 13.3 / 19.5;  256 x 1024 (64), k 8192: 15.9 / 14.1 / 24;
@@ -55,9 +58,11 @@ inline I8Kernel i8_dense_kernel(int64_t M, int64_t N, int64_t K) {
   if (tiles(16, 16) <= 256) return I8_STREAM_16;
   if (tiles(32, 16) <= 256 || !fit) return I8_STREAM_32;
   if (M <= 32) return I8_TILES_64;
-  if (tiles(256, 256) >= 192) return I8_TILES_256;
-  if (tiles(128, 256) >= 192) return I8_TILES_128x256;
-  if (tiles(128, 128) >= 144) return I8_TILES_128;
+  if (M > 64) {
+    if (tiles(256, 256) >= 192) return I8_TILES_256;
+    if (tiles(128, 256) >= 192) return I8_TILES_128x256;
+    if (tiles(128, 128) >= 144) return I8_TILES_128;
+  }
   return tiles(64, 64) >= 80 ? I8_TILES_64 : I8_NARROW;
 }
 
