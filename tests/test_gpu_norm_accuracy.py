@@ -72,3 +72,25 @@ def test_rows_of_zeros_without_an_epsilon(wq, dtype, k):
     i8.assert_within(i8.to_host(dx)[:6], rx, bx, "dx")
     assert torch.equal(dx.cpu()[6:], ds[[2, 5]])
     i8.assert_within(i8.to_host(dw), rw, bw, "d_weight")
+
+
+def test_gradients_of_very_long_rows(wq):
+    """dx and d_weight of two rows of 2^28 + 72 ones of either sign: the lanes' and the waves' sums are whole numbers
+    up to 2^24 and exact, so that 16 additions, inv and a few products are the errors."""
+    import torch
+
+    print("very long rows", flush=True)
+    k = (1 << 28) + 72
+    r, dy = ((torch.randint(0, 2, (2, k), device="cuda", dtype=torch.int8) * 2 - 1).to(torch.bfloat16) for _ in range(2))
+    ds = torch.zeros_like(r)
+    ds[:, -9:] = 4
+    dx, dw = wq.wq_rms_norm_grad(dy, r, torch.ones(k, device="cuda", dtype=torch.bfloat16), ds)
+    inv = 1 / np.sqrt(1 + 1e-6)
+    mean = [float((dy[i] == r[i]).sum() * 2 - k) / k for i in range(2)]
+    for at in (0, k // 3, k - 4000):
+        s = slice(at, at + 4000)
+        a, g, d = (t[:, s].double().cpu().numpy() for t in (r, dy, ds))
+        ref = inv * (g - a * inv ** 2 * np.array(mean)[:, None]) + d
+        i8.assert_within(i8.to_host(dx[:, s]), ref, np.abs(ref) * (i8.HALF["bf16"] + 26 * i8.U), "dx")
+        ref = (g * a * inv).sum(0)
+        i8.assert_within(i8.to_host(dw[s]), ref, 2 * 26 * i8.U, "d_weight")
