@@ -923,6 +923,8 @@ def wq_moe_balance_loss_workspace_bytes(t: int, experts: int) -> int:
 
 def _balance_inputs(logits, topk_ids, what):
     vt, kind = _value_type(logits, f"{what} logits")
+    if not hasattr(topk_ids, "dim"):
+        raise TypeError(f"{what} topk_ids: expected a torch tensor, got {type(topk_ids).__name__}")
     if logits.dim() != 2 or topk_ids.dim() != 2:
         raise ValueError(f"{what}: logits must be [t, experts] and topk_ids [t, topk]")
     _need(logits, f"{what} logits", kind)
