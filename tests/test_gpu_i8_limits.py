@@ -122,3 +122,30 @@ def test_largest_dense_weight(wq, m, n):
     for a in (0, n // 2, n - 1000):
         w = wq.PackedWeight(wq.FMT_INT8, 1000, k, 1, 0, codes=codes[:, a: a + 1000].clone(), scales=scales[:, a: a + 1000].clone())
         assert torch.equal(y[:, a: a + 1000], wq.wq_gemm_i8(x, w)), a
+
+
+def test_strided_inputs_are_refused(wq):
+    """Rows that are not contiguous: only the quantisers copy them."""
+    import torch
+
+    wide = torch.randn((6, 256), device="cuda")
+    x, w = wide[:, :128], torch.ones(128, device="cuda")
+    c = x.contiguous()
+    rows = wq.wq_quantize_i8(c)
+    weight = wq.wq_quantize_i8_weight(torch.randn((64, 128), device="cuda"))
+    ids = torch.zeros((6, 4), dtype=torch.int32, device="cuda")
+    off, pairs = wq.wq_moe_route(ids[:, :2].contiguous(), 1)
+    codes = torch.zeros((6, 256), dtype=torch.int8, device="cuda")[:, :128]
+    strided = wq.Int8Rows(codes, rows.scales)
+    counts = torch.ones(129, dtype=torch.int32, device="cuda")
+    for call in (lambda: wq.wq_rms_norm(x, w), lambda: wq.wq_rms_norm(c, w, x), lambda: wq.wq_rms_norm(c, w, y=x),
+                 lambda: wq.wq_rms_norm_i8(x, w), lambda: wq.wq_rms_norm_i8(c, w, rows=strided),
+                 lambda: wq.wq_rms_norm_grad(x, c, w), lambda: wq.wq_rms_norm_grad(c, x, w),
+                 lambda: wq.wq_rms_norm_grad(c, c, w, x), lambda: wq.wq_rms_norm_grad(c, c, w, dx=x),
+                 lambda: wq.wq_gemm_i8(strided, weight), lambda: wq.wq_gemm_i8(rows, weight, y=wide[:, :64]),
+                 lambda: wq.wq_moe_gate_up_i8(strided, off, pairs, 2, weight, weight), lambda: wq.wq_moe_down_i8(strided, off, weight),
+                 lambda: wq.wq_moe_balance_loss(x, ids), lambda: wq.wq_moe_balance_loss(c, ids[:, :2]),
+                 lambda: wq.wq_moe_balance_loss_grad(x, ids, counts), lambda: wq.wq_moe_balance_loss_grad(c, ids, counts, d_logits=x)):
+        with pytest.raises(ValueError, match="contiguous"):
+            call()
+    assert torch.equal(wq.wq_quantize_i8(x).codes, rows.codes)
