@@ -417,7 +417,8 @@ size_t wq_moe_balance_loss_workspace_bytes(int64_t t, int32_t experts);
  *   loss = coefficient * sum_e (experts c_e / sum_i c_i) * (sum_t p_te / T)      (f32, one value)
  *   counts[e] = c_e, counts[experts] = T                                         (int32 [experts + 1])
  * Tokens whose ids all lie outside [0, experts) are padding: they count nowhere and their logits are not
- * used.  Without any token the loss is 0.  A row of -inf has no probability anywhere.  ws: as in
+ * used.  Without any token the loss is 0.  A row of -inf has no probability anywhere (zeros, where a softmax has NaN).
+ * ws: as in
  * wq_rms_norm_grad.  At most 512 experts and 2^30 pairs. */
 wq_status wq_moe_balance_loss(const void* logits, int32_t type, const int32_t* topk_ids, int64_t t,
                               int32_t topk, int32_t experts, float coefficient, float* loss,
@@ -425,7 +426,8 @@ wq_status wq_moe_balance_loss(const void* logits, int32_t type, const int32_t* t
 
 /* d_logits [t][experts] of wq_moe_balance_loss for d_loss (f32, one value in device memory; NULL: 1), with
  * the counts that it gave, or the sums of several calls' counts where the loss is over all of their tokens
- * (the shares are no function of the logits):
+ * (the shares are no function of the logits; wq_moe_balance_loss gives the loss of its own tokens, and the calls'
+ * losses do not add up to that of all):
  *   share_e = experts c_e / sum_i c_i
  *   d_logits_te = d_loss * coefficient / T * p_te (share_e - sum_j share_j p_tj)   (0 for padding) */
 wq_status wq_moe_balance_loss_grad(const void* logits, int32_t type, const int32_t* topk_ids,

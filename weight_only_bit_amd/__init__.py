@@ -732,7 +732,7 @@ class Int8Rows(NamedTuple):
 
 def wq_quantize_i8(x) -> Int8Rows:
     """bf16 or fp32 rows [n, k] to int8 with a scale per row (include/wq.h): the activations of the products
-    below."""
+    below.  Rows that are not contiguous are copied first, as by the other quantisers; the norms refuse them."""
     vt, kind = _value_type(x, "wq_quantize_i8 x")
     if x.dim() != 2 or x.shape[1] == 0:
         raise ValueError(f"wq_quantize_i8: x must be [n, k], got shape {tuple(x.shape)}")
@@ -953,8 +953,9 @@ def wq_moe_balance_loss(logits, topk_ids, coefficient: float = 1.0, loss=None, c
 
 
 def wq_moe_balance_loss_grad(logits, topk_ids, counts, coefficient: float = 1.0, d_loss=None, d_logits=None):
-    """d_logits [t, experts] of wq_moe_balance_loss; counts as it gave them (or the sum of several calls'),
-    d_loss: an fp32 tensor of one value (None: 1)."""
+    """d_logits [t, experts] of wq_moe_balance_loss; counts as it gave them, d_loss: an fp32 tensor of one value
+    (None: 1).  With the sum of several calls' counts: of the loss over all of their tokens, which is not the sum of
+    the calls' losses."""
     vt, kind, t, topk, experts = _balance_inputs(logits, topk_ids, "wq_moe_balance_loss_grad")
     _need(counts, "wq_moe_balance_loss_grad counts", "i32", numel=experts + 1)
     if d_loss is not None:

@@ -10,9 +10,10 @@
 //
 // Both read the logits once, the gradient writes as many bytes, and e^z is computed again in the gradient rather than
 // kept.  A lane holds 16 values, so a token of 64 experts is 4 lanes and a wave's sums and divisions serve 16 tokens.
-// Large ones are bound by memory: 65536 x 256 fp32 loss 22 us in a graph (13.4 us, 5.2 TB/s, and the parts' sums), gradient
-// 30 us (27, 5.0 TB/s, and the launch).  Small ones by launches: 4096 x 64 bf16 9.2 us (two of them) and 4.6; 256 x 8 fp32
-// 5.7 (one workgroup, no parts) and 2.9.
+// Large ones in fp32 are bound by memory: 65536 x 256 loss 22.5 to 23 us in a graph (15 us, 4.6 TB/s, and the parts'
+// sums), gradient 30 us (27, 5.0 TB/s, and the launch); in bf16, where half the bytes bring as many values, by the vector
+// operations of a value: 65536 x 512 34 and 44 us, of which four operations of the exponential take 4.  Small ones by
+// launches: 4096 x 64 bf16 9.8 us (two of them) and 4.7; 256 x 8 fp32 5.8 to 6.1 (one workgroup, no parts) and 2.9.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>

@@ -28,8 +28,9 @@ __device__ __forceinline__ void store_out(void* out, int f32, int64_t at, float 
 // row l % 16 of A (column of B) and 16 codes; it receives D[4 (l / 16) + i][l % 16].  Instruction i
 // of a step of 256 along k takes 64 of them, lane group q = l / 16 the codes 16 q .. 16 q + 15: a load touches
 // one 64-byte line of every row.
-// Bound by the weights' way: one round trip to memory and what a CU takes in, where the workgroups are few (1, 8, 32 x
-// 4096, k 4096: 6.0, 6.9, 9.4 us, 16.8 MB), memory where they are many (32 tokens, top-8 of 64 experts, 3584 x 8192:
+// Bound by the operands' way: one round trip to memory and what a CU takes in, weights and (16 or 32 rows for every 16
+// columns) as many or twice as many bytes of activations again, where the workgroups are few (1, 8, 32 x 4096, k 4096:
+// 6.0, 6.9, 9.4 us; 32 rows: 64 KB + 128 KB a CU), memory where they are many (32 tokens, top-8 of 64 experts, 3584 x 8192:
 // gate+up 600 us, 6.2 TB/s; 8192 x 3584: down 316).  More waves (8, 16) gain nothing.
 // ---------------------------------------------------------------------------------------------
 __device__ __forceinline__ i32x4 mfma16(const u32x4& a, const u32x4& b, const i32x4& c) {
@@ -188,8 +189,9 @@ hipError_t launch_stream(const I8Args& a, int64_t gy, int64_t gz, hipStream_t s)
 
 // ---------------------------------------------------------------------------------------------
 // Tens to hundreds of rows and few outputs: 32 rows by 16 columns a workgroup, where 64 x 64 tiles would leave most
-// CUs without one.  A CU takes in 15 to 25 KB/us from memory, so the weights' columns are cut so finely that every
-// CU brings some of them, and the rows, which L2 holds, are read again: 64 x 2560, k 8192 19.7 us (22.1 with 64 x 64
+// CUs without one.  A CU takes in 26 to 45 KB/us, both operands counted, and each workgroup reads all of k for its rows
+// and columns, so the columns are cut so finely that every CU takes in some, though the rows, which L2 holds, are read
+// again by each: 64 x 2560, k 8192 19.7 us (22.1 with 64 x 64
 // tiles, 24.5 streaming), 128 x 2048, k 4096 8.9 (9.9, 13.4).
 //   * Stages of 256 bytes of a row, 16 lanes a row; two of them on their way in registers, two in LDS, 16-byte
 //     piece p of row r in slot p ^ (r % 16): writes and fragment reads are free of bank conflicts.

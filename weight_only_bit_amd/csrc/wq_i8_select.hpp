@@ -43,7 +43,8 @@ inline bool i8_tiles_fit(int64_t gathered, int64_t N, int64_t K) {
 //   64 x 64 from a third of the chip on (64 x 64 / 32 x 16 / streaming 32 x 16): 128 x 4096 (128 tiles), k 4096: 13.0 /
 //     14.2 / 25;  333 x 1111 (108), k 4160: 10.9 / 11.8 / 16.9;  48 x 5120 (80), k 8192: 21.1 / 21.8 / 33;  256 x 1280
 //     (80), k 4096: 10.1 / 9.6 / 18.8;  64 x 4608 (72): 13.8 / 13.3 / 19.5;  256 x 1024 (64), k 8192: 15.9 / 14.1 / 24;
-//     17 to 32 rows 32 x 8192 (128), k 8192: 20.9 / 23.1 / 26.2;  32 x 4112 (65), k 4096: 11.7 / 12.1 / 14.2
+//     17 to 32 rows 32 x 8192 (128), k 8192: 20.9 / 23.1 / 26.2;  32 x 4112 (65), k 4096: 11.7 / 12.1 / 14.2;  at 80
+//     tiles either may be 5 % faster
 //   streaming where its workgroups are at most one for every CU (streaming / 32 x 16): 32 x 4096 (256), k 4096: 9.5 /
 //     11.7;  64 x 2048 (256): 8.6 / 8.6;  96 x 2048 (384): 13.5 / 8.9;  64 x 4096 (512): 14.3 / 12.2;  and 16 rows where
 //     those are (16 x 16 / 32 x 16): 32 x 2048 (256) 6.7 / 8.5;  200 x 300 (247), k 8192: 10.4 / 13.8;  32 x 2560 (320), k
@@ -67,7 +68,9 @@ inline I8Kernel i8_dense_kernel(int64_t M, int64_t N, int64_t K) {
 }
 
 // The same for experts, `pairs` rows in all, gate+up of `gathered` tokens (down: 0), by the rows that an
-// expert has on average (gate+up, down; 64 experts, hidden 8192, inter 3584 unless said otherwise):
+// expert has on average, measured with even routing (gate+up, down; 64 experts, hidden 8192, inter 3584 unless said
+// otherwise).  Uneven routing costs the streaming kernel, whose workgroup takes an expert's rows 16 at a time, and not the
+// tiles (8 experts, 1024 x 1024, 512 rows on average, skew 0 / 1.1: streaming 99 / 209, 128 x 128 tiles 21.2 / 21.3):
 //   streaming for few, which reads the weights at memory's rate (streaming / 128 x 256): 3 rows 565 / 618, 302 /
 //     312; 4 rows 600 / 642, 332 / 326; 8 rows 623 / 650, 389 / 330; 16 rows 874 / 658, 554 / 337.  Gate+up goes on to
 //     10 rows, down, whose k is shorter, to 4; with few tiles to 16 (8 experts, 1024 x 1024; streaming / 128 x 128):
@@ -79,6 +82,9 @@ inline I8Kernel i8_dense_kernel(int64_t M, int64_t N, int64_t K) {
 //     66, 42.5 / 37.3; and (/ 128 x 256) 64 rows (384) 46.8 / 46.5, 24.8 / 26.7;
 //     64 experts, 1024 x 2048: 8 rows (544) 43.8 / 46.4, 25.7 / 27.9, 64 rows (544) 50.4 / 52.2, 28.9 / 32.5; hidden
 //     8192, inter 3584: 8 rows (1808) 635 / 632, 329 / 330
+//   not told apart: 128 x 256 from 128 rows on, where 256 x 256 tiles are few (/ 128 x 128; 16 experts, 2048 x 4096, 128
+//     rows: 75.4 / 87.3, 41.9 / 39.3);  not built: 64 x 64 tiles (/ 128 x 128; 8 experts, 1024 x 1024, 64 rows: 7.9 / 8.8,
+//     6.1 / 7.8; 64 experts, 1024 x 2048, 16 rows: 42.8 / 44.6, 27.9 / 26.3, 64 rows: 59.8 / 50.4, 39.6 / 28.9)
 inline I8Kernel i8_experts_kernel(int64_t gathered, int64_t pairs, int64_t N, int64_t K, int64_t experts) {
   const int64_t active = pairs < experts ? pairs : experts;  // at most
   const double rows = (double)pairs / (double)experts;

@@ -9,8 +9,10 @@
 //
 // All of them are bound by memory.  A row is held in registers between the pass that sums it and the pass
 // that writes it, so it is read once; only rows beyond 65536 bf16 (32768 fp32) values, in the gradient 16384
-// (8192), are read again.  4096 x 8192 bf16: norm 54 us (5.0 TB/s, a copy of 2 GiB 4.8), in int8 51 us (4.6), the
-// gradient 63 us (4.3, its parts included); 32 x 8192: 3.7, 4.1 and 6.6 us, of which a launch takes 1.6.
+// (8192), are read again.  4096 x 8192 bf16: norm 53 us (5.1 TB/s, copies of 2 GiB 4.8 to 5.6), in int8 50 us (4.7), the
+// gradient 62 us (4.3, its parts included); 32 x 8192: 3.7, 4.1 and 6.5 us, of which a launch takes 1.6.  Short rows
+// are bound by a chain of dependent steps a row, with no next row on its way and, below 16 pieces, idle lanes: 65536 x 64
+// bf16 10.6, 12.3 and 17.3 us where their bytes take 6, 5 and 6.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
@@ -98,7 +100,7 @@ __global__ __launch_bounds__(LANES < 256 ? 256 : LANES) void norm_kernel(const N
   typedef typename Wide<T>::M M;
   const int tid = LANES < 256 ? (int)threadIdx.x % LANES : (int)threadIdx.x;
   const int64_t row = LANES < 256 ? (first + blockIdx.x) * (256 / LANES) + threadIdx.x / LANES : first + blockIdx.x;
-  if (row >= a.n) return;  // whole waves, and of rows of several waves the whole workgroup
+  if (row >= a.n) return;  // whole groups of LANES, and of rows of several waves the whole workgroup
   const int64_t k = a.k, pieces = k / E, base = row * k;
   const int tail = (int)(k % E);
   const int64_t tcol = pieces * E + tid;  // of the lanes below `tail`
@@ -497,7 +499,9 @@ int64_t pieces_of(int64_t k, int f32) { return k / (f32 ? 4 : 8); }
 //     8192 (256x4 / 1024x1) 56.3 / 54.0, 52.5 / 51.2, 64 / 63
 //   129 to 256 pieces, 16384 x 2048 (64x4 / 256x1): 57.0 / 51.4, 53.9 / 47.9, 61 / 65
 //   long rows from registers as far as they hold them: 512 x 65536 (1024x8 / read again) 56 / 70, 60 / 64; the
-//     gradient holds three arrays and its columns' sums, up to 2048 pieces
+//     gradient holds three arrays and its columns' sums, up to 2048 pieces (above 1024 of bf16 16 of its 128
+//     registers spill: 1024 x 16384 42 us where the bytes take 24); longer rows are read twice and their columns'
+//     sums go through the workspace for every row, 8 bytes more a value (512 x 65536 131, the bytes 48)
 Shape shape_of(int64_t n, int64_t pieces, bool grad) {
   if (pieces <= 16) return S16x1;
   if (pieces <= 64) return S64x1;
